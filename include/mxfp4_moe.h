@@ -66,6 +66,13 @@ typedef enum {
 #define MXFP4_DECODE_MAX_K 3072      /* mxfp4_moe_decode: all of a row's loads in flight at once */
 #define MXFP4_DECODE_MAX_T 64        /* mxfp4_moe_decode_batch: tokens ranked one per lane */
 
+#define MOE_NORM_MAX_N 16384         /* the norms: a row stays in one workgroup's registers */
+#define MOE_BALANCE_MAX_T (1 << 30)  /* moe_balance, moe_route_backward */
+
+/* Element types of the arguments that take one (`const void*` with a *_dtype). */
+#define MXFP4_DTYPE_BF16 0
+#define MXFP4_DTYPE_F32 1
+
 /* Projection paths for mxfp4_expert_proj. */
 #define MXFP4_PATH_AUTO 0  /* GEMV while T * k <= 16 * min(E, T * k), grouped GEMM otherwise */
 #define MXFP4_PATH_GEMV 1  /* decode GEMV: 128-bit weight streaming, exact bf16 products, fp32 sums */
@@ -453,6 +460,166 @@ int mxfp4_dequantize(const uint8_t* blocks, const uint8_t* scales, long long row
  *   T >= 0, k >= 1, N >= 1.  T = 0 returns MXFP4_OK and enqueues nothing.
  */
 int moe_combine(const float* proj, const float* gates, int T, int k, int N, float* y, void* stream);
+
+/*
+ * The block's input norm: the root-mean-square norm of each row of the
+ * residual stream, the input of mxfp4_moe_router and of the experts.
+ *
+ *   x       [T, N] bf16 or fp32 (x_dtype), T >= 0, 1 <= N <= MOE_NORM_MAX_N.
+ *   w       [N] bf16.
+ *   eps     > 0.
+ *   xn      [T, N] bf16 out: xn[t, n] = bf16(x[t, n] * r * w[n]) with
+ *           r = (sum_n x[t, n]^2 / N + eps)^(-1/2), in fp32, rounded once.  (A
+ *           row whose sum of squares passes fp32's range gets r = 0.)
+ * Pointers need the alignment of their elements only.  One kernel launch; T = 0
+ * returns MXFP4_OK and enqueues nothing.
+ */
+int moe_norm(const void* x, int x_dtype, const uint16_t* w, int T, int N, float eps, uint16_t* xn, void* stream);
+
+/* Workspace bytes of moe_norm_backward; (size_t)-1 for invalid sizes. */
+size_t moe_norm_backward_workspace_size(int T, int N);
+
+/*
+ * The gradients of moe_norm.
+ *
+ *   dxn     [T, N] bf16: the gradient of xn.
+ *   x, x_dtype, w, eps: as given to moe_norm.
+ *   dres    [T, N] of x's type, or NULL (none): the gradient that reaches x past
+ *           the norm, along the residual stream.
+ *   dx      [T, N] of x's type, out; may be dres.  With x^ = x * r:
+ *           dx = dres + r * (dxn w - x^ * sum_n(dxn w x^) / N), in fp32, rounded once.
+ *   dw      [N] fp32 out, or NULL: dw[n] = sum_t dxn[t, n] * x^[t, n], added in a
+ *           fixed order.  T = 0 writes zeros.
+ *   workspace, workspace_bytes: at least moe_norm_backward_workspace_size(T, N)
+ *           bytes, 16-byte aligned; may be NULL where that is 0 or dw is NULL.
+ *           Calls that share a workspace must be ordered on one stream.
+ */
+int moe_norm_backward(const uint16_t* dxn, const void* x, int x_dtype, const uint16_t* w, const void* dres, int T,
+                      int N, float eps, void* dx, float* dw, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The block's output: the gate-weighted combine of a token's k expert outputs,
+ * the output norm, the residual scale and sum, and the next block's input norm,
+ * in one pass.
+ *
+ *   proj    [T, k, N] fp32 or bf16 (proj_dtype): the experts' outputs
+ *           (mxfp4_expert_proj's out), or with k = 1 and gates NULL any block's
+ *           output (moe_combine's or mxfp4_expert_proj_combine's y).
+ *           T >= 0, 1 <= k <= MXFP4_MAX_TOPK, 1 <= N <= MOE_NORM_MAX_N.
+ *   gates   [T, k] fp32, or NULL: every gate 1.  h = sum_s gates[t, s] *
+ *           proj[t, s, :] in slot order, the bits of moe_combine: a slot with gate 0
+ *           adds nothing, whatever its row holds.
+ *   w_post  [N] bf16, or NULL: no output norm.  u = h * r_h * w_post (or h).
+ *   x       [T, N] bf16 or fp32 (x_dtype): the residual stream.
+ *   scale   finite: the residual scale.
+ *   eps     > 0, of both norms.
+ *   x_out   [T, N] of x's type, out; may be x: x_out = x + scale * u, rounded once.
+ *   w_next  [N] bf16, and
+ *   xn      [T, N] bf16 out, or both NULL: the norm of x_out as stored, the bits
+ *           that moe_norm(x_out, w_next) gives.
+ * A token with no routed slot keeps x_out = x.  One kernel launch; T = 0 returns
+ * MXFP4_OK and enqueues nothing.
+ */
+int moe_combine_norm(const void* proj, int proj_dtype, const float* gates, int T, int k, int N, const uint16_t* w_post,
+                     const void* x, int x_dtype, float scale, float eps, void* x_out, const uint16_t* w_next,
+                     uint16_t* xn, void* stream);
+
+/* Workspace bytes of moe_combine_norm_backward (both weights' gradients);
+ * (size_t)-1 for invalid sizes. */
+size_t moe_combine_norm_backward_workspace_size(int T, int N);
+
+/*
+ * The gradients of moe_combine_norm.
+ *
+ *   dx_out  [T, N] of x_dtype, or NULL (zero): the gradient of x_out along the
+ *           residual stream.
+ *   dxn     [T, N] bf16, or NULL: the gradient of xn.  With it x_out [T, N] of
+ *           x_dtype (as moe_combine_norm stored it) and w_next are read; at least
+ *           one of dx_out and dxn is given.
+ *   proj, proj_dtype, gates, k, w_post, x_dtype, scale, eps: as given to
+ *           moe_combine_norm.
+ *   Outputs, each NULL where it is not wanted:
+ *   dx      [T, N] of x_dtype; may be dx_out: G = dx_out + the gradient of the next
+ *           norm at x_out, the gradient of x.
+ *   dproj   [T, k, N] of proj_dtype: gates[t, s] * dh[t, :], where dh is the
+ *           gradient of the output norm at h for scale * G (or scale * G itself).
+ *           Exactly 0 for a slot with gate 0.
+ *   dgates  [T, k] fp32 (gates given): sum_n dh[t, n] * proj[t, s, n]; 0 for a slot
+ *           with gate 0, whose row is not read.
+ *   dw_post [N] fp32 (w_post given): sum_t scale * G * h * r_h.
+ *   dw_next [N] fp32 (dxn given): sum_t dxn * x_out * r.
+ *   All in fp32 with sums in a fixed order, each output rounded once.  T = 0 writes
+ *   zeros to dw_post and dw_next.
+ *   workspace, workspace_bytes: at least moe_combine_norm_backward_workspace_size(T,
+ *           N) bytes, 16-byte aligned; may be NULL where that is 0 or neither
+ *           dw_post nor dw_next is wanted.  Calls that share a workspace must be
+ *           ordered on one stream.
+ */
+int moe_combine_norm_backward(const void* dx_out, const uint16_t* dxn, const void* x_out, const uint16_t* w_next,
+                              const void* proj, int proj_dtype, const float* gates, int T, int k, int N,
+                              const uint16_t* w_post, int x_dtype, float scale, float eps, void* dx, void* dproj,
+                              float* dgates, float* dw_post, float* dw_next, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Workspace bytes of moe_balance; (size_t)-1 for invalid sizes. */
+size_t moe_balance_workspace_size(int T, int E, int S);
+
+/*
+ * The load of the experts: per-expert counts, the balance loss and the z loss
+ * of a batch of packed sequences.
+ *
+ *   logits  [T, E] bf16: the router logits; 0 <= T <= MOE_BALANCE_MAX_T,
+ *           1 <= E <= MXFP4_MAX_EXPERTS.
+ *   topk_ids [T, k] i32: the routing (mxfp4_moe_route_group);
+ *           1 <= k <= min(E, MXFP4_MAX_TOPK).
+ *   seq_offsets [S + 1] i32, ascending, or NULL (S = 1: all T tokens): sequence s
+ *           holds the tokens [seq_offsets[s], seq_offsets[s + 1]).  Sequences may
+ *           be empty; tokens before the first and behind the last are padding.
+ *           Values outside [0, T] are clamped.  1 <= S, S * E < 2^31.
+ *   A token is counted when it lies in a sequence, has a slot whose id lies in
+ *   [0, E), and a logit above -inf; another token's logits (NaN included) reach no
+ *   output.  A counted token's logits hold no NaN and no +inf.
+ *   counts  [S, E] i32 out: the slots of sequence s's counted tokens that chose
+ *           expert e.
+ *   tokens  [S + 2] i32 out: each sequence's counted tokens n_s, then their sum n
+ *           and the number S' of sequences with n_s > 0.
+ *   losses  [2] fp32 out: with p the softmax over all E logits,
+ *           losses[0] = (1 / S') sum_s E sum_e counts[s, e] / (k n_s) * mean p[., e],
+ *           losses[1] = the mean over the counted tokens of logsumexp(logits)^2;
+ *           0 where nothing is counted.  fp32, summed in a fixed order.
+ *   workspace, workspace_bytes: at least moe_balance_workspace_size(T, E, S) bytes,
+ *           16-byte aligned.  Calls that share a workspace must be ordered on one
+ *           stream.
+ * T = 0 writes zeros.
+ */
+int moe_balance(const uint16_t* logits, const int32_t* topk_ids, int T, int E, int k, const int32_t* seq_offsets,
+                int S, int32_t* counts, int32_t* tokens, float* losses, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * The gradient of the router's logits: through the gates (the softmax over the
+ * chosen logits), the balance loss and the z loss.
+ *
+ *   topk_ids, gates [T, k]: the routing; dgates [T, k] fp32, or NULL (none; gates
+ *           may then be NULL): the gates' gradient (moe_combine_norm_backward's).
+ *   dlosses [2] fp32 in device memory, or NULL (none): the gradients of
+ *           moe_balance's losses.  With it logits, seq_offsets, S, counts and tokens
+ *           are read, as given to and written by moe_balance; without it they may be
+ *           NULL and are not read.  At least one of dgates and dlosses is given.
+ *   T, E, k: as for moe_balance.
+ *   dlogits [T, E] fp32 or bf16 (dlogits_dtype), out, every element written:
+ *           sum over the slots s that chose e of g_s (dg_s - sum_r g_r dg_r)
+ *           + dlosses[0] E / (S' k n_s^2) p_e (counts_e - sum_j p_j counts_j)
+ *           + dlosses[1] (2 / n) logsumexp p_e,
+ *           in fp32, rounded once.  The counts carry no gradient.  A slot whose id
+ *           lies outside [0, E) or whose gate is 0 adds nothing.  With dlosses the
+ *           row of a token that moe_balance does not count is 0, without it the row
+ *           of a token with no valid slot.
+ * One kernel launch; T = 0 returns MXFP4_OK and enqueues nothing.
+ */
+int moe_route_backward(const uint16_t* logits, const int32_t* topk_ids, const float* gates, const float* dgates, int T,
+                       int E, int k, const int32_t* seq_offsets, int S, const int32_t* counts, const int32_t* tokens,
+                       const float* dlosses, void* dlogits, int dlogits_dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,9 @@ raises.
 __all__ = ["mxfp4_moe_route_group", "mxfp4_expert_proj", "mxfp4_expert_proj_workspace_size", "moe_combine",
            "mxfp4_expert_proj_swiglu", "mxfp4_expert_proj_combine", "mxfp4_moe_decode", "mxfp4_moe_decode_swiglu",
            "mxfp4_moe_router", "mxfp4_moe_dense_route", "mxfp4_dequantize", "mxfp4_expert_proj_noalloc",
+           "moe_norm", "moe_norm_backward", "moe_norm_backward_workspace_size", "moe_combine_norm",
+           "moe_combine_norm_backward", "moe_combine_norm_backward_workspace_size", "moe_balance",
+           "moe_balance_workspace_size", "moe_route_backward",
            "library_path"]
 
 

@@ -22,6 +22,8 @@ MXFP4_ROUTE_ERR_ID_RANGE, MXFP4_ROUTE_ERR_ID_DUP = 1, 2
 MXFP4_MAX_EXPERTS, MXFP4_MAX_TOPK = 512, 32
 MXFP4_DECODE_MAX_EXPERTS, MXFP4_DECODE_MAX_K, MXFP4_GEMM_MAX_K = 64, 3072, 8192
 MXFP4_NOALLOC_SCRATCH_BYTES = 128 << 20
+MXFP4_DTYPE_BF16, MXFP4_DTYPE_F32 = 0, 1
+MOE_NORM_MAX_N, MOE_BALANCE_MAX_T = 16384, 1 << 30
 
 #: the C entry points this binding uses (all declared in include/mxfp4_moe.h)
 ENTRY_POINTS = (
@@ -42,6 +44,15 @@ ENTRY_POINTS = (
     "mxfp4_expert_proj_combine_routed",
     "mxfp4_moe_decode_batch",
     "mxfp4_moe_decode_batch_swiglu",
+    "moe_norm",
+    "moe_norm_backward_workspace_size",
+    "moe_norm_backward",
+    "moe_combine_norm",
+    "moe_combine_norm_backward_workspace_size",
+    "moe_combine_norm_backward",
+    "moe_balance_workspace_size",
+    "moe_balance",
+    "moe_route_backward",
 )
 
 _lib_handle = None
@@ -107,6 +118,22 @@ def load_library():
     lib.mxfp4_expert_proj_combine_routed.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp,
                                                      vp, vp, i32, vp, sz, vp]
     lib.mxfp4_expert_proj_combine_routed.restype = i32
+    f32 = ctypes.c_float
+    lib.moe_norm.argtypes = [vp, i32, vp, i32, i32, f32, vp, vp]
+    lib.moe_norm_backward_workspace_size.argtypes = [i32, i32]
+    lib.moe_norm_backward.argtypes = [vp, vp, i32, vp, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.moe_combine_norm.argtypes = [vp, i32, vp, i32, i32, i32, vp, vp, i32, f32, f32, vp, vp, vp, vp]
+    lib.moe_combine_norm_backward_workspace_size.argtypes = [i32, i32]
+    lib.moe_combine_norm_backward.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, i32, f32, f32, vp, vp,
+                                              vp, vp, vp, vp, sz, vp]
+    lib.moe_balance_workspace_size.argtypes = [i32, i32, i32]
+    lib.moe_balance.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]
+    lib.moe_route_backward.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, i32, vp]
+    for name in ("moe_norm", "moe_norm_backward", "moe_combine_norm", "moe_combine_norm_backward", "moe_balance",
+                 "moe_route_backward"):
+        getattr(lib, name).restype = i32
+        if hasattr(lib, name + "_workspace_size"):
+            getattr(lib, name + "_workspace_size").restype = sz
     _lib_handle = lib
     return lib
 
@@ -370,3 +397,172 @@ def mxfp4_expert_proj_combine_routed(blocks, scales, bias, E: int, N: int, K: in
         _ptr(out, "out", _F32, dev), _ptr(y, "y", _F32, dev), int(path), ws_ptr, ctypes.c_size_t(ws_bytes),
         _stream(stream, dev))
     _check(st)
+
+
+# ---------------------------------------------------------------------------
+# The norms around the block and the routing's balance
+# ---------------------------------------------------------------------------
+
+# element types by dtype code (bf16 also as its bit patterns, as everywhere in this binding)
+_ELEMENTS = {MXFP4_DTYPE_BF16: _BF16, MXFP4_DTYPE_F32: _F32}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    for code, dtypes in _ELEMENTS.items():
+        if t.dtype in dtypes:
+            return code
+    raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16 + _F32}")
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtypes, count: int, device: int):
+    """A device pointer, or None: the tensor's type, its contiguous layout, its device (an
+    ordinal) and that it holds at least `count` elements."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected a device tensor on cuda:{device}")
+    if t.numel() < count:
+        raise ValueError(f"{name} holds {t.numel()} elements, {count} needed")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    return device
+
+
+def _run(entry, device: int, stream, *args):
+    """The C entry point on `device` (made current for the call) and its stream."""
+    if device == torch.cuda.current_device():
+        _check(entry(*args, _stream(stream, device)))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, _stream(stream, device)))
+
+
+def _size(n: int, what: str) -> int:
+    if n == ctypes.c_size_t(-1).value:
+        raise MXFP4Error(1, f"invalid sizes for the {what} workspace query")
+    return int(n)
+
+
+def _workspace(workspace, device: int):
+    if workspace is None:
+        return None, 0
+    return _arg(workspace, "workspace", _U8, 0, device), workspace.numel()
+
+
+def moe_norm(x, w, T: int, N: int, xn, eps: float = 1e-5, stream=None):
+    """The block's input norm (moe_norm): xn [T,N] bf16 = x * rsqrt(mean(x^2) + eps) * w of each row
+    of x [T,N] bf16 or f32; w [N] bf16."""
+    lib = load_library()
+    dev = _device_of(xn, "xn")
+    xt = _dtype(x, "x")
+    _run(lib.moe_norm, dev, stream, _arg(x, "x", _ELEMENTS[xt], T * N, dev), xt,
+         _arg(w, "w", _BF16, N, dev), T, N, eps, _arg(xn, "xn", _BF16, T * N, dev))
+
+
+def moe_norm_backward_workspace_size(T: int, N: int) -> int:
+    return _size(load_library().moe_norm_backward_workspace_size(T, N), "moe_norm_backward")
+
+
+def moe_norm_backward(dxn, x, w, T: int, N: int, dx, dw=None, dres=None, eps: float = 1e-5, workspace=None,
+                      stream=None):
+    """The gradients of moe_norm (moe_norm_backward): dx [T,N] of x's type (dres, the residual
+    stream's own gradient, added; dx may be dres) and dw [N] f32 (optional).  workspace: a uint8
+    device tensor of at least moe_norm_backward_workspace_size(T, N) bytes, for dw."""
+    lib = load_library()
+    dev = _device_of(dx, "dx")
+    ws, nbytes = _workspace(workspace, dev)
+    xt = _dtype(x, "x")
+    xs = _ELEMENTS[xt]
+    _run(lib.moe_norm_backward, dev, stream, _arg(dxn, "dxn", _BF16, T * N, dev), _arg(x, "x", xs, T * N, dev), xt,
+         _arg(w, "w", _BF16, N, dev), _arg(dres, "dres", xs, T * N, dev), T, N, eps, _arg(dx, "dx", xs, T * N, dev),
+         _arg(dw, "dw", _F32, N, dev), ws, nbytes)
+
+
+def moe_combine_norm(proj, gates, T: int, k: int, N: int, x, x_out, w_post=None, scale: float = 1.0, w_next=None,
+                     xn=None, eps: float = 1e-5, stream=None):
+    """The block's output (moe_combine_norm): the combine of proj [T,k,N] f32 or bf16 with gates
+    [T,k] f32 (None: every gate 1), the output norm (w_post [N] bf16, None: no norm), x_out [T,N] =
+    x + scale * that (of x's type, may be x), and with w_next [N] bf16 the next block's input
+    norm into xn [T,N] bf16."""
+    lib = load_library()
+    dev = _device_of(x_out, "x_out")
+    pt, xt = _dtype(proj, "proj"), _dtype(x, "x")
+    _run(lib.moe_combine_norm, dev, stream, _arg(proj, "proj", _ELEMENTS[pt], T * k * N, dev), pt,
+         _arg(gates, "gates", _F32, T * k, dev), T, k, N, _arg(w_post, "w_post", _BF16, N, dev),
+         _arg(x, "x", _ELEMENTS[xt], T * N, dev), xt, scale, eps, _arg(x_out, "x_out", _ELEMENTS[xt], T * N, dev),
+         _arg(w_next, "w_next", _BF16, N, dev), _arg(xn, "xn", _BF16, T * N, dev))
+
+
+def moe_combine_norm_backward_workspace_size(T: int, N: int) -> int:
+    return _size(load_library().moe_combine_norm_backward_workspace_size(T, N), "moe_combine_norm_backward")
+
+
+def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=None, dproj=None, dgates=None,
+                              w_post=None, dw_post=None, scale: float = 1.0, dxn=None, x_out=None, w_next=None,
+                              dw_next=None, eps: float = 1e-5, workspace=None, stream=None):
+    """The gradients of moe_combine_norm (moe_combine_norm_backward) for dx_out [T,N] (None: 0) and
+    dxn [T,N] bf16 (None: none; else with the stored x_out and w_next): dx [T,N] (may be dx_out),
+    dproj [T,k,N] of proj's type, dgates [T,k] f32, dw_post and dw_next [N] f32, each None where it is not
+    wanted.  workspace: a uint8 device tensor of at least
+    moe_combine_norm_backward_workspace_size(T, N) bytes, for the weights' gradients."""
+    lib = load_library()
+    dev = _device_of(proj, "proj")
+    stream_like = next((t for t in (dx_out, x_out, dx) if t is not None), None)
+    if stream_like is None:
+        raise ValueError("one of dx_out and dxn (with x_out) must be given")
+    pt, xt = _dtype(proj, "proj"), _dtype(stream_like, "the residual stream")
+    ps, xs = _ELEMENTS[pt], _ELEMENTS[xt]
+    ws, nbytes = _workspace(workspace, dev)
+    _run(lib.moe_combine_norm_backward, dev, stream, _arg(dx_out, "dx_out", xs, T * N, dev),
+         _arg(dxn, "dxn", _BF16, T * N, dev), _arg(x_out, "x_out", xs, T * N, dev),
+         _arg(w_next, "w_next", _BF16, N, dev), _arg(proj, "proj", ps, T * k * N, dev), pt,
+         _arg(gates, "gates", _F32, T * k, dev), T, k, N, _arg(w_post, "w_post", _BF16, N, dev), xt, scale, eps,
+         _arg(dx, "dx", xs, T * N, dev), _arg(dproj, "dproj", ps, T * k * N, dev),
+         _arg(dgates, "dgates", _F32, T * k, dev), _arg(dw_post, "dw_post", _F32, N, dev),
+         _arg(dw_next, "dw_next", _F32, N, dev), ws, nbytes)
+
+
+def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
+    return _size(load_library().moe_balance_workspace_size(T, E, S), "moe_balance")
+
+
+def moe_balance(logits, topk_ids, T: int, E: int, k: int, counts, tokens, losses, seq_offsets=None, S: int = 1,
+                workspace=None, stream=None):
+    """Per-expert counts, the balance loss and the z loss (moe_balance) of logits [T,E] bf16 and
+    topk_ids [T,k] i32: counts [S,E] i32, tokens [S+2] i32 (per sequence, their sum, the non-empty
+    sequences), losses [2] f32 (balance, z).  seq_offsets [S+1] i32: packed sequences (None: one of
+    all T tokens).  workspace: a uint8 device tensor of at least moe_balance_workspace_size(T, E, S)
+    bytes."""
+    lib = load_library()
+    dev = _device_of(counts, "counts")
+    ws, nbytes = _workspace(workspace, dev)
+    _run(lib.moe_balance, dev, stream, _arg(logits, "logits", _BF16, T * E, dev),
+         _arg(topk_ids, "topk_ids", _I32, T * k, dev), T, E, k,
+         _arg(seq_offsets, "seq_offsets", _I32, S + 1, dev), S, _arg(counts, "counts", _I32, S * E, dev),
+         _arg(tokens, "tokens", _I32, S + 2, dev), _arg(losses, "losses", _F32, 2, dev), ws, nbytes)
+
+
+def moe_route_backward(logits, topk_ids, gates, dgates, T: int, E: int, k: int, dlogits, seq_offsets=None, S: int = 1,
+                       counts=None, tokens=None, dlosses=None, stream=None):
+    """The gradient of the router logits (moe_route_backward) into dlogits [T,E] f32 or bf16: through
+    the gates [T,k] (dgates [T,k] f32, or None) and through moe_balance's losses (dlosses [2] f32 on
+    the device, or None; with it logits, seq_offsets, S, counts and tokens as given to and written by
+    moe_balance)."""
+    lib = load_library()
+    dev = _device_of(dlogits, "dlogits")
+    dt = _dtype(dlogits, "dlogits")
+    _run(lib.moe_route_backward, dev, stream, _arg(logits, "logits", _BF16, T * E, dev),
+         _arg(topk_ids, "topk_ids", _I32, T * k, dev), _arg(gates, "gates", _F32, T * k, dev),
+         _arg(dgates, "dgates", _F32, T * k, dev), T, E, k,
+         _arg(seq_offsets, "seq_offsets", _I32, S + 1, dev), S, _arg(counts, "counts", _I32, S * E, dev),
+         _arg(tokens, "tokens", _I32, S + 2, dev), _arg(dlosses, "dlosses", _F32, 2, dev),
+         _arg(dlogits, "dlogits", _ELEMENTS[dt], T * E, dev), dt)

@@ -422,4 +422,206 @@ int moe_combine(const float* proj, const float* gates, int T, int k, int N, floa
   return MXFP4_OK;
 }
 
+// ---------------------------------------------------------------------------
+// The norms around the block and the routing's balance
+// ---------------------------------------------------------------------------
+
+namespace {
+static_assert(mxfp4::kMaxTopK == MXFP4_MAX_TOPK && mxfp4::kNormMaxN == MOE_NORM_MAX_N, "one set of limits");
+
+bool known_dtype(int d) { return d == MXFP4_DTYPE_BF16 || d == MXFP4_DTYPE_F32; }
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned_elem(const void* p, int dtype) { return aligned_to(p, dtype == MXFP4_DTYPE_F32 ? 4 : 2); }
+
+int check_norm_sizes(int T, int k, int N, float eps) {
+  if (T < 0) return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be >= 0", T);
+  if (N < 1 || N > MOE_NORM_MAX_N) return fail(MXFP4_ERR_INVALID_ARG, "N = %d must be in [1, %d]", N, MOE_NORM_MAX_N);
+  if (k < 1 || k > MXFP4_MAX_TOPK) return fail(MXFP4_ERR_INVALID_ARG, "k = %d must be in [1, %d]", k, MXFP4_MAX_TOPK);
+  if ((long long)T * k > 0x7fffffffLL) return fail(MXFP4_ERR_INVALID_ARG, "T * k overflows int32");
+  if (!(eps > 0.f) || eps > 3.4e38f) return fail(MXFP4_ERR_INVALID_ARG, "eps = %g must be positive and finite", (double)eps);
+  return MXFP4_OK;
+}
+
+int check_workspace(const void* workspace, size_t given, size_t need) {
+  if (need == 0) return MXFP4_OK;
+  if (!workspace || given < need)
+    return fail(MXFP4_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? given : 0, need);
+  if (!aligned16(workspace)) return fail(MXFP4_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+  return MXFP4_OK;
+}
+
+int check_balance_sizes(int T, int E, int k, int S) {
+  if (T < 0 || T > MOE_BALANCE_MAX_T)
+    return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be in [0, %d]", T, MOE_BALANCE_MAX_T);
+  if (E < 1 || E > MXFP4_MAX_EXPERTS) return fail(MXFP4_ERR_INVALID_ARG, "E = %d must be in [1, %d]", E, MXFP4_MAX_EXPERTS);
+  if (k < 1 || k > E || k > MXFP4_MAX_TOPK)
+    return fail(MXFP4_ERR_INVALID_ARG, "k = %d must be in [1, min(E = %d, %d)]", k, E, MXFP4_MAX_TOPK);
+  if ((long long)T * k > 0x7fffffffLL) return fail(MXFP4_ERR_INVALID_ARG, "T * k overflows int32");
+  if (S < 1 || (long long)S * E > 0x7fffffffLL)
+    return fail(MXFP4_ERR_INVALID_ARG, "S = %d must be >= 1, with S * E within int32", S);
+  return MXFP4_OK;
+}
+}  // namespace
+
+int moe_norm(const void* x, int x_dtype, const uint16_t* w, int T, int N, float eps, uint16_t* xn, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_norm_sizes(T, 1, N, eps);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(x_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "x_dtype = %d unknown", x_dtype);
+  if (T == 0) return MXFP4_OK;
+  if (!x || !w || !xn) return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned_elem(x, x_dtype) || !aligned_to(w, 2) || !aligned_to(xn, 2))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if ((st = check_device()) != MXFP4_OK) return st;
+  hipError_t e = mxfp4::launch_norm(x, x_dtype == MXFP4_DTYPE_F32, w, T, N, eps, xn, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "norm launch");
+  return MXFP4_OK;
+}
+
+size_t moe_norm_backward_workspace_size(int T, int N) {
+  if (T < 0 || N < 1 || N > MOE_NORM_MAX_N) return (size_t)-1;
+  return mxfp4::norm_backward_workspace_bytes(T, N, 1);
+}
+
+int moe_norm_backward(const uint16_t* dxn, const void* x, int x_dtype, const uint16_t* w, const void* dres, int T,
+                      int N, float eps, void* dx, float* dw, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_norm_sizes(T, 1, N, eps);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(x_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "x_dtype = %d unknown", x_dtype);
+  if (T == 0 && !dw) return MXFP4_OK;
+  if (T > 0 && (!dxn || !x || !w || !dx)) return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned_to(dxn, 2) || !aligned_elem(x, x_dtype) || !aligned_to(w, 2) || !aligned_elem(dres, x_dtype) ||
+      !aligned_elem(dx, x_dtype) || !aligned_to(dw, 4))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if (dw && (st = check_workspace(workspace, workspace_bytes, mxfp4::norm_backward_workspace_bytes(T, N, 1))) != MXFP4_OK)
+    return st;
+  if ((st = check_device()) != MXFP4_OK) return st;
+  hipError_t e = mxfp4::launch_norm_backward(dxn, x, x_dtype == MXFP4_DTYPE_F32, w, dres, T, N, eps, dx, dw, workspace,
+                                             static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "norm_backward launch");
+  return MXFP4_OK;
+}
+
+int moe_combine_norm(const void* proj, int proj_dtype, const float* gates, int T, int k, int N, const uint16_t* w_post,
+                     const void* x, int x_dtype, float scale, float eps, void* x_out, const uint16_t* w_next,
+                     uint16_t* xn, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_norm_sizes(T, k, N, eps);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(proj_dtype) || !known_dtype(x_dtype))
+    return fail(MXFP4_ERR_INVALID_ARG, "proj_dtype = %d or x_dtype = %d unknown", proj_dtype, x_dtype);
+  if (!(scale - scale == 0.f)) return fail(MXFP4_ERR_INVALID_ARG, "scale must be finite");
+  if (T == 0) return MXFP4_OK;
+  if (!proj || !x || !x_out) return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!w_next != !xn) return fail(MXFP4_ERR_INVALID_ARG, "w_next and xn go together");
+  if (!aligned_elem(proj, proj_dtype) || !aligned_to(gates, 4) || !aligned_to(w_post, 2) ||
+      !aligned_elem(x, x_dtype) || !aligned_elem(x_out, x_dtype) || !aligned_to(w_next, 2) || !aligned_to(xn, 2))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if ((st = check_device()) != MXFP4_OK) return st;
+  mxfp4::CombineNormArgs a = {};
+  a.proj = proj, a.gates = gates, a.w_post = w_post, a.x = x, a.x_out = x_out, a.w_next = w_next, a.xn = xn;
+  a.k = k, a.N = N, a.scale = scale, a.eps = eps;
+  hipError_t e = mxfp4::launch_combine_norm(a, x_dtype == MXFP4_DTYPE_F32, proj_dtype == MXFP4_DTYPE_F32, T,
+                                            static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "combine_norm launch");
+  return MXFP4_OK;
+}
+
+size_t moe_combine_norm_backward_workspace_size(int T, int N) {
+  if (T < 0 || N < 1 || N > MOE_NORM_MAX_N) return (size_t)-1;
+  return mxfp4::norm_backward_workspace_bytes(T, N, 2);
+}
+
+int moe_combine_norm_backward(const void* dx_out, const uint16_t* dxn, const void* x_out, const uint16_t* w_next,
+                              const void* proj, int proj_dtype, const float* gates, int T, int k, int N,
+                              const uint16_t* w_post, int x_dtype, float scale, float eps, void* dx, void* dproj,
+                              float* dgates, float* dw_post, float* dw_next, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_norm_sizes(T, k, N, eps);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(proj_dtype) || !known_dtype(x_dtype))
+    return fail(MXFP4_ERR_INVALID_ARG, "proj_dtype = %d or x_dtype = %d unknown", proj_dtype, x_dtype);
+  if (!(scale - scale == 0.f)) return fail(MXFP4_ERR_INVALID_ARG, "scale must be finite");
+  if (dgates && !gates) return fail(MXFP4_ERR_INVALID_ARG, "dgates without gates");
+  if (dw_post && !w_post) return fail(MXFP4_ERR_INVALID_ARG, "dw_post without w_post");
+  if (T > 0) {
+    if (!dx_out && !dxn) return fail(MXFP4_ERR_INVALID_ARG, "one of dx_out and dxn must be given");
+    if (dxn && (!x_out || !w_next)) return fail(MXFP4_ERR_INVALID_ARG, "dxn needs x_out and w_next");
+    if (dw_next && !dxn) return fail(MXFP4_ERR_INVALID_ARG, "dw_next without dxn");
+    if (!proj) return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  }
+  if (!aligned_elem(dx_out, x_dtype) || !aligned_to(dxn, 2) || !aligned_elem(x_out, x_dtype) || !aligned_to(w_next, 2) ||
+      !aligned_elem(proj, proj_dtype) || !aligned_to(gates, 4) || !aligned_to(w_post, 2) || !aligned_elem(dx, x_dtype) ||
+      !aligned_elem(dproj, proj_dtype) || !aligned_to(dgates, 4) || !aligned_to(dw_post, 4) || !aligned_to(dw_next, 4))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if (!dw_post && !dw_next && (T == 0 || (!dx && !dproj && !dgates))) return MXFP4_OK;
+  if (dw_post || dw_next) {
+    st = check_workspace(workspace, workspace_bytes, mxfp4::norm_backward_workspace_bytes(T, N, 2));
+    if (st != MXFP4_OK) return st;
+  }
+  if ((st = check_device()) != MXFP4_OK) return st;
+  mxfp4::CombineNormBackwardArgs a = {};
+  a.dx_out = dx_out, a.dxn = dxn, a.x_out = x_out, a.w_next = w_next, a.proj = proj, a.gates = gates;
+  a.w_post = w_post, a.dx = dx, a.dproj = dproj, a.dgates = dgates;
+  a.T = T, a.k = k, a.N = N, a.scale = scale, a.eps = eps;
+  hipError_t e = mxfp4::launch_combine_norm_backward(a, x_dtype == MXFP4_DTYPE_F32, proj_dtype == MXFP4_DTYPE_F32,
+                                                     dw_post, dw_next, workspace, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "combine_norm_backward launch");
+  return MXFP4_OK;
+}
+
+size_t moe_balance_workspace_size(int T, int E, int S) {
+  if (T < 0 || T > MOE_BALANCE_MAX_T || E < 1 || E > MXFP4_MAX_EXPERTS || S < 1 || (long long)S * E > 0x7fffffffLL)
+    return (size_t)-1;
+  return mxfp4::balance_workspace_bytes(T, E, S);
+}
+
+int moe_balance(const uint16_t* logits, const int32_t* topk_ids, int T, int E, int k, const int32_t* seq_offsets,
+                int S, int32_t* counts, int32_t* tokens, float* losses, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_balance_sizes(T, E, k, S);
+  if (st != MXFP4_OK) return st;
+  if (!seq_offsets && S != 1) return fail(MXFP4_ERR_INVALID_ARG, "S = %d sequences need seq_offsets", S);
+  if ((T > 0 && (!logits || !topk_ids)) || !counts || !tokens || !losses)
+    return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned_to(logits, 2) || !aligned_to(topk_ids, 4) || !aligned_to(seq_offsets, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(tokens, 4) || !aligned_to(losses, 4))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  st = check_workspace(workspace, workspace_bytes, mxfp4::balance_workspace_bytes(T, E, S));
+  if (st != MXFP4_OK) return st;
+  if ((st = check_device()) != MXFP4_OK) return st;
+  hipError_t e = mxfp4::launch_balance(logits, topk_ids, T, E, k, seq_offsets, S, counts, tokens, losses, workspace,
+                                       static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "balance launch");
+  return MXFP4_OK;
+}
+
+int moe_route_backward(const uint16_t* logits, const int32_t* topk_ids, const float* gates, const float* dgates, int T,
+                       int E, int k, const int32_t* seq_offsets, int S, const int32_t* counts, const int32_t* tokens,
+                       const float* dlosses, void* dlogits, int dlogits_dtype, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_balance_sizes(T, E, k, dlosses ? S : 1);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(dlogits_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "dlogits_dtype = %d unknown", dlogits_dtype);
+  if (dlosses && !seq_offsets && S != 1)
+    return fail(MXFP4_ERR_INVALID_ARG, "S = %d sequences need seq_offsets", S);
+  if (T == 0) return MXFP4_OK;
+  if (!dgates && !dlosses) return fail(MXFP4_ERR_INVALID_ARG, "one of dgates and dlosses must be given");
+  if (!topk_ids || !dlogits || (dgates && !gates) || (dlosses && (!logits || !counts || !tokens)))
+    return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned_to(logits, 2) || !aligned_to(topk_ids, 4) || !aligned_to(gates, 4) || !aligned_to(dgates, 4) ||
+      !aligned_to(seq_offsets, 4) || !aligned_to(counts, 4) || !aligned_to(tokens, 4) || !aligned_to(dlosses, 4) ||
+      !aligned_elem(dlogits, dlogits_dtype))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if ((st = check_device()) != MXFP4_OK) return st;
+  hipError_t e = mxfp4::launch_route_backward(logits, topk_ids, gates, dgates, T, E, k, seq_offsets, S, counts, tokens,
+                                              dlosses, dlogits, dlogits_dtype == MXFP4_DTYPE_F32,
+                                              static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "route_backward launch");
+  return MXFP4_OK;
+}
+
 }  // extern "C"

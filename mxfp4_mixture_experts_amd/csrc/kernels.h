@@ -76,4 +76,61 @@ hipError_t launch_router(const uint16_t* x, const uint16_t* w, const uint16_t* b
 hipError_t launch_combine(const float* proj, const float* gates, int T, int k, int N, float* y,
                           hipStream_t stream, const int32_t* ids = nullptr, int E = 0);
 
+constexpr int kMaxTopK = 32;  // = MXFP4_MAX_TOPK
+
+// block_norm.hip: the norms before and after the block.  Element types of x,
+// x_out, dx_out, dx, dres (x_f32) and proj, dproj (proj_f32): fp32 or bf16.
+constexpr int kNormMaxN = 16384;  // = MOE_NORM_MAX_N: 512 threads x 4 chunks of 8
+hipError_t launch_norm(const void* x, bool x_f32, const uint16_t* w, int T, int N, float eps, uint16_t* xn,
+                       hipStream_t stream);
+// workspace: the workgroups' column sums of `weights` weight gradients
+size_t norm_backward_workspace_bytes(int T, int N, int weights);
+hipError_t launch_norm_backward(const uint16_t* dxn, const void* x, bool x_f32, const uint16_t* w, const void* dres,
+                                int T, int N, float eps, void* dx, float* dw, void* workspace, hipStream_t stream);
+
+struct CombineNormArgs {
+  const void* proj;     // [T, k, N]
+  const float* gates;   // [T, k], or NULL: all 1
+  const uint16_t* w_post;  // [N], or NULL: no output norm
+  const void* x;
+  void* x_out;
+  const uint16_t* w_next;  // [N], with xn
+  uint16_t* xn;            // [T, N], or NULL: no input norm of the next block
+  int k, N;
+  float scale, eps;
+  float inv_n;  // set by the launcher
+};
+hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, int T, hipStream_t stream);
+
+struct CombineNormBackwardArgs {
+  const void* dx_out;   // [T, N], or NULL: 0
+  const uint16_t* dxn;  // [T, N], or NULL: no gradient from the next norm (x_out, w_next are not read)
+  const void* x_out;
+  const uint16_t* w_next;
+  const void* proj;
+  const float* gates;
+  const uint16_t* w_post;
+  void* dx;       // each output may be NULL
+  void* dproj;
+  float* dgates;
+  int T, k, N;
+  float scale, eps;
+  float inv_n;       // these three set by the launcher
+  float* part_post;  // [groups, N] column sums of the weights' gradients
+  float* part_next;
+};
+hipError_t launch_combine_norm_backward(CombineNormBackwardArgs a, bool x_f32, bool proj_f32, float* dw_post,
+                                        float* dw_next, void* workspace, hipStream_t stream);
+
+// balance.hip: the routing's balance loss, counts and gradients
+size_t balance_workspace_bytes(int T, int E, int S);
+hipError_t launch_balance(const uint16_t* logits, const int32_t* ids, int T, int E, int k, const int32_t* seq, int S,
+                          int32_t* counts, int32_t* tokens, float* losses, void* workspace, hipStream_t stream);
+// dlosses == NULL: the gates' gradient only (seq, counts, tokens are not read);
+// dgates == NULL: the losses' only
+hipError_t launch_route_backward(const uint16_t* logits, const int32_t* ids, const float* gates, const float* dgates,
+                                 int T, int E, int k, const int32_t* seq, int S, const int32_t* counts,
+                                 const int32_t* tokens, const float* dlosses, void* dlogits, bool dlogits_f32,
+                                 hipStream_t stream);
+
 }  // namespace mxfp4
