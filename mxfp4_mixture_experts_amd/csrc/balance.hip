@@ -38,26 +38,23 @@ constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// sum and maximum over the L lanes of a group (every lane receives them; the
-// order is fixed)
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
-}
 template <int L>
 __device__ __forceinline__ bool group_any(bool p) {
   const uint64_t m = __ballot(p);
   if constexpr (L == 64) return m != 0;
   const int base = (threadIdx.x & 63) & ~(L - 1);
   return ((m >> base) & ((1ull << (L & 63)) - 1)) != 0;
+}
+
+// a lane's eight logits; -inf behind the last expert
+__device__ __forceinline__ void load_logits(const uint16_t* p, int valid, float (&v)[8]) {
+  Raw8<uint16_t> r;
+  fetch8(p, valid, r);
+  widen8(r, v);
+  if (valid < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = i < valid ? v[i] : -INFINITY;
+  }
 }
 
 // the softmax of a group's logits: v becomes the probabilities, z the
@@ -148,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void balance_pieces_kernel(const uint16_t
     int n = 0;
     for (int t = a + group; t < b; t += kGroups) {
       float v[8], z;
-      load8(logits + (size_t)t * E + e0, E - e0, v, -INFINITY);
+      load_logits(logits + (size_t)t * E + e0, E - e0, v);
       bool valid = false;
       for (int q = j; q < k; q += L) valid |= (unsigned)ids[(size_t)t * k + q] < (unsigned)E;
       const bool some = group_any<L>(valid);
@@ -318,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, z = 0.f;
     bool live = true;
     if constexpr (LOSSES) {
-      load8(logits + (size_t)t * E + e0, E - e0, v, -INFINITY);
+      load_logits(logits + (size_t)t * E + e0, E - e0, v);
       while (seq && t >= s_end && s < S) {
         s++;
         s_end = s < S ? seq[s + 1] : T;

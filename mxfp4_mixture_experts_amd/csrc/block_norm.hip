@@ -63,23 +63,26 @@ void with_row_type(bool f32, int N, F f) {
 }
 
 // Sums of M values over the workgroup, added lane by lane and then wave by
-// wave; every thread receives them.  `red` is free again after the barrier of
-// the next call with the other buffer (calls alternate between two).
+// wave; every thread receives them.  red[m] holds value m of each wave, 0
+// where the row has fewer waves (wave 0 writes those); a buffer is free again after the
+// barrier of the next call, so calls take turns between two.
 template <int M>
-__device__ __forceinline__ void row_sum(float (&v)[M], float* red) {
-  const int waves = blockDim.x >> 6;
+__device__ __forceinline__ void row_sum(float (&v)[M], float (&red)[M][kMaxWaves]) {
 #pragma unroll
-  for (int m = 0; m < M; m++) v[m] = wave_sum(v[m]);
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0) {
+  for (int m = 0; m < M; m++) v[m] = group_sum<64>(v[m]);
+  if (blockDim.x == 64) return;
+  const int lane = threadIdx.x & 63;
+  const bool spare = threadIdx.x < kMaxWaves && threadIdx.x >= (blockDim.x >> 6);
+  if (lane == 0 || spare) {
 #pragma unroll
-    for (int m = 0; m < M; m++) red[m * kMaxWaves + (threadIdx.x >> 6)] = v[m];
+    for (int m = 0; m < M; m++) red[m][spare ? lane : threadIdx.x >> 6] = spare ? 0.f : v[m];
   }
   __syncthreads();
 #pragma unroll
   for (int m = 0; m < M; m++) {
-    float s = red[m * kMaxWaves];
-    for (int w = 1; w < waves; w++) s += red[m * kMaxWaves + w];
+    float s = red[m][0];
+#pragma unroll
+    for (int w = 1; w < kMaxWaves; w++) s += red[m][w];
     v[m] = s;
   }
 }
@@ -88,31 +91,43 @@ __device__ __forceinline__ float rms_scale(float sum, float inv_n, float eps) {
   return rsqrtf(fmaf(sum, inv_n, eps));
 }
 
+// a thread's chunks of a row: c = 0 .. CH - 1 at element (thread + c * threads) * 8
+__device__ __forceinline__ int chunk_at(int c) { return (threadIdx.x + c * blockDim.x) * 8; }
+
+template <typename E, int CH>
+__device__ __forceinline__ void fetch_row(const E* row, int N, Raw8<E> (&r)[CH]) {
+#pragma unroll
+  for (int c = 0; c < CH; c++) fetch8(row + chunk_at(c), N - chunk_at(c), r[c]);
+}
+
 template <typename X, int CH>
 __global__ __launch_bounds__(kMaxRowThreads) void norm_kernel(const X* __restrict__ x, const uint16_t* __restrict__ w,
                                                               int N, float inv_n, float eps,
                                                               uint16_t* __restrict__ xn) {
-  __shared__ float red[kMaxWaves];
+  __shared__ __align__(16) float red[1][kMaxWaves];
   const size_t row = (size_t)blockIdx.x * N;
-  float v[CH][8], wv[CH][8], s[1] = {0.f};
+  Raw8<X> xr[CH];
+  Raw8<uint16_t> wr[CH];
+  fetch_row(x + row, N, xr);
+  fetch_row(w, N, wr);
+  float s[1] = {0.f};
 #pragma unroll
   for (int c = 0; c < CH; c++) {
-    const int i = (threadIdx.x + c * blockDim.x) * 8;
-    load8(x + row + i, N - i, v[c]);
-    load8(w + i, N - i, wv[c]);
+    float v[8];
+    widen8(xr[c], v);
+#pragma unroll
+    for (int j = 0; j < 8; j++) s[0] = fmaf(v[j], v[j], s[0]);
   }
-#pragma unroll
-  for (int c = 0; c < CH; c++)
-#pragma unroll
-    for (int j = 0; j < 8; j++) s[0] = fmaf(v[c][j], v[c][j], s[0]);
   row_sum(s, red);
   const float r = rms_scale(s[0], inv_n, eps);
 #pragma unroll
   for (int c = 0; c < CH; c++) {
-    const int i = (threadIdx.x + c * blockDim.x) * 8;
+    float v[8], wv[8];
+    widen8(xr[c], v);
+    widen8(wr[c], wv);
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[c][j] = v[c][j] * r * wv[c][j];
-    store8(xn + row + i, N - i, v[c]);
+    for (int j = 0; j < 8; j++) v[j] = v[j] * r * wv[j];
+    store8(xn + row + chunk_at(c), N - chunk_at(c), v);
   }
 }
 
@@ -120,27 +135,42 @@ __global__ __launch_bounds__(kMaxRowThreads) void norm_kernel(const X* __restric
 // by one thread, in this order.
 template <typename X, typename P, int CH>
 __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const CombineNormArgs a) {
-  __shared__ float red[2][kMaxWaves];
+  constexpr int kSlots = CH == 1 ? 4 : CH == 2 ? 2 : 1;  // slots whose rows are under way together
+  __shared__ __align__(16) float red[2][1][kMaxWaves];
   const int N = a.N, k = a.k;
   const size_t t = blockIdx.x, row = t * N;
   const X* x = static_cast<const X*>(a.x) + row;
   X* x_out = static_cast<X*>(a.x_out) + row;
   const P* proj = static_cast<const P*>(a.proj) + row * k;
+  Raw8<X> xr[CH];
+  Raw8<uint16_t> wp[CH], wn[CH];
+  fetch_row(x, N, xr);
+  if (a.w_post) fetch_row(a.w_post, N, wp);
+  if (a.xn) fetch_row(a.w_next, N, wn);
   float h[CH][8], s[1] = {0.f};
 #pragma unroll
   for (int c = 0; c < CH; c++)
 #pragma unroll
     for (int j = 0; j < 8; j++) h[c][j] = 0.f;
-  for (int q = 0; q < k; q++) {
-    const float g = a.gates ? a.gates[t * k + q] : 1.f;
-    if (g == 0.f) continue;
+  for (int q0 = 0; q0 < k; q0 += kSlots) {
+    Raw8<P> pr[kSlots][CH];
+    float g[kSlots];
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
-      const int i = (threadIdx.x + c * blockDim.x) * 8;
-      float p[8];
-      load8(proj + (size_t)q * N + i, N - i, p);
+    for (int u = 0; u < kSlots; u++) {
+      const int q = min(q0 + u, k - 1);
+      g[u] = q0 + u >= k ? 0.f : a.gates ? a.gates[t * k + q] : 1.f;
+      fetch_row(proj + (size_t)q * N, N, pr[u]);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; j++) h[c][j] = fmaf(g, p[j], h[c][j]);
+    for (int u = 0; u < kSlots; u++) {
+      if (g[u] == 0.f) continue;
+#pragma unroll
+      for (int c = 0; c < CH; c++) {
+        float p[8];
+        widen8(pr[u][c], p);
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[c][j] = fmaf(g[u], p[j], h[c][j]);
+      }
     }
   }
   if (a.w_post) {
@@ -152,9 +182,8 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const Comb
     const float r = rms_scale(s[0], a.inv_n, a.eps);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      const int i = (threadIdx.x + c * blockDim.x) * 8;
       float wv[8];
-      load8(a.w_post + i, N - i, wv);
+      widen8(wp[c], wv);
 #pragma unroll
       for (int j = 0; j < 8; j++) h[c][j] = h[c][j] * r * wv[j];
     }
@@ -162,85 +191,94 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const Comb
   s[0] = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; c++) {
-    const int i = (threadIdx.x + c * blockDim.x) * 8;
     float xv[8];
-    load8(x + i, N - i, xv);
+    widen8(xr[c], xv);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
       h[c][j] = rounded(fmaf(a.scale, h[c][j], xv[j]), x);
       s[0] = fmaf(h[c][j], h[c][j], s[0]);
     }
-    store8(x_out + i, N - i, h[c]);
+    store8(x_out + chunk_at(c), N - chunk_at(c), h[c]);
   }
   if (!a.xn) return;
   row_sum(s, red[1]);
   const float r = rms_scale(s[0], a.inv_n, a.eps);
 #pragma unroll
   for (int c = 0; c < CH; c++) {
-    const int i = (threadIdx.x + c * blockDim.x) * 8;
     float wv[8];
-    load8(a.w_next + i, N - i, wv);
+    widen8(wn[c], wv);
 #pragma unroll
     for (int j = 0; j < 8; j++) h[c][j] = h[c][j] * r * wv[j];
-    store8(a.xn + row + i, N - i, h[c]);
+    store8(a.xn + row + chunk_at(c), N - chunk_at(c), h[c]);
   }
 }
 
-// Gradients of moe_norm.  dx may be dres itself.
+// Gradients of moe_norm.  dx may be dres itself.  The loads of a workgroup's
+// next row are issued before the sums of this one.
 template <typename X, int CH>
 __global__ __launch_bounds__(kMaxRowThreads) void norm_backward_kernel(const uint16_t* dxn, const X* x,
                                                                        const uint16_t* w, const X* dres, int T, int N,
                                                                        float inv_n, float eps, X* dx, float* part) {
-  __shared__ float red[2][2 * kMaxWaves];
+  __shared__ __align__(16) float red[2][2][kMaxWaves];
   float dw[CH][8];
+  Raw8<uint16_t> wr[CH];
+  fetch_row(w, N, wr);
 #pragma unroll
   for (int c = 0; c < CH; c++)
 #pragma unroll
     for (int j = 0; j < 8; j++) dw[c][j] = 0.f;
+  Raw8<X> x_next[CH], r_next[CH];
+  Raw8<uint16_t> d_next[CH];
+  auto fetch = [&](int t) {
+    const size_t row = (size_t)t * N;
+    fetch_row(x + row, N, x_next);
+    fetch_row(dxn + row, N, d_next);
+    if (dres) fetch_row(dres + row, N, r_next);
+  };
+  fetch(blockIdx.x);
   int parity = 0;
   for (int t = blockIdx.x; t < T; t += gridDim.x, parity ^= 1) {
-    const size_t row = (size_t)t * N;
-    float v[CH][8], d[CH][8], g[CH][8], s[2] = {0.f, 0.f};
+    Raw8<X> rr[CH];
+    float v[CH][8], d[CH][8], s[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      const int i = (threadIdx.x + c * blockDim.x) * 8;
       float wv[8];
-      load8(x + row + i, N - i, v[c]);
-      load8(dxn + row + i, N - i, d[c]);
-      load8(w + i, N - i, wv);
+      widen8(x_next[c], v[c]);
+      widen8(d_next[c], d[c]);
+      widen8(wr[c], wv);
+      rr[c] = r_next[c];
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        g[c][j] = d[c][j] * wv[j];
         s[0] = fmaf(v[c][j], v[c][j], s[0]);
-        s[1] = fmaf(v[c][j], g[c][j], s[1]);
+        s[1] = fmaf(v[c][j], d[c][j] * wv[j], s[1]);
       }
     }
+    if (t + (int)gridDim.x < T) fetch(t + gridDim.x);
     row_sum(s, red[parity]);
     const float r = rms_scale(s[0], inv_n, eps);
     const float m = s[1] * inv_n * r;
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      const int i = (threadIdx.x + c * blockDim.x) * 8;
-      float o[8];
-      if (dres)
-        load8(dres + row + i, N - i, o);
-      else
+      float o[8], wv[8];
+      widen8(wr[c], wv);
+      if (dres) {
+        widen8(rr[c], o);
+      } else {
+#pragma unroll
         for (int j = 0; j < 8; j++) o[j] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const float unit = v[c][j] * r;
         dw[c][j] = fmaf(d[c][j], unit, dw[c][j]);
-        o[j] = fmaf(r, fmaf(-unit, m, g[c][j]), o[j]);
+        o[j] = fmaf(r, fmaf(-unit, m, d[c][j] * wv[j]), o[j]);
       }
-      store8(dx + row + i, N - i, o);
+      store8(dx + (size_t)t * N + chunk_at(c), N - chunk_at(c), o);
     }
   }
   if (part) {
 #pragma unroll
-    for (int c = 0; c < CH; c++) {
-      const int i = (threadIdx.x + c * blockDim.x) * 8;
-      store8(part + (size_t)blockIdx.x * N + i, N - i, dw[c]);
-    }
+    for (int c = 0; c < CH; c++) store8(part + (size_t)blockIdx.x * N + chunk_at(c), N - chunk_at(c), dw[c]);
   }
 }
 
@@ -250,10 +288,15 @@ __global__ __launch_bounds__(kMaxRowThreads) void norm_backward_kernel(const uin
 template <typename X, typename P, int CH, int KR>
 __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
   constexpr int KH = KR > 0 ? KR : 1;
-  __shared__ float red1[2][3 * kMaxWaves], red2[2][kMaxWaves], redg[2][kMaxTopK * kMaxWaves];
+  __shared__ __align__(16) float red1[2][3][kMaxWaves], red2[2][1][kMaxWaves], redg[2][kMaxTopK][kMaxWaves];
   const int N = a.N, k = a.k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const X* dx_out = static_cast<const X*>(a.dx_out);
+  const X* x_out = static_cast<const X*>(a.x_out);
   float dw_post[CH][8], dw_next[CH][8];
+  Raw8<uint16_t> wp[CH], wn[CH];
+  if (a.w_post) fetch_row(a.w_post, N, wp);
+  if (a.dxn) fetch_row(a.w_next, N, wn);
 #pragma unroll
   for (int c = 0; c < CH; c++)
 #pragma unroll
@@ -262,54 +305,62 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
     const size_t row = (size_t)t * N;
     const P* proj = static_cast<const P*>(a.proj) + row * k;
-    float p[KH][CH][8], h[CH][8], grad[CH][8], s[3] = {0.f, 0.f, 0.f};
+    const float* gates = a.gates ? a.gates + (size_t)t * k : nullptr;
+    Raw8<P> pr[KH][CH];
+    Raw8<X> gr[CH], xo[CH];
+    Raw8<uint16_t> dn[CH];
+    float h[CH][8], grad[CH][8], s[3] = {0.f, 0.f, 0.f};
+    if constexpr (KR > 0) {
+#pragma unroll
+      for (int q = 0; q < KR; q++)
+        if (q < k) fetch_row(proj + (size_t)q * N, N, pr[q]);
+    }
+    if (dx_out) fetch_row(dx_out + row, N, gr);
+    if (a.dxn) {
+      fetch_row(x_out + row, N, xo);
+      fetch_row(a.dxn + row, N, dn);
+    }
 #pragma unroll
     for (int c = 0; c < CH; c++)
 #pragma unroll
       for (int j = 0; j < 8; j++) h[c][j] = 0.f;
+    auto add_slot = [&](float g, const Raw8<P> (&rows)[CH]) {
+      if (g == 0.f) return;
+#pragma unroll
+      for (int c = 0; c < CH; c++) {
+        float p[8];
+        widen8(rows[c], p);
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[c][j] = fmaf(g, p[j], h[c][j]);
+      }
+    };
     if constexpr (KR > 0) {
 #pragma unroll
-      for (int q = 0; q < KR; q++) {
-        const float g = q < k ? (a.gates ? a.gates[(size_t)t * k + q] : 1.f) : 0.f;
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-          const int i = (threadIdx.x + c * blockDim.x) * 8;
-          load8(proj + (size_t)q * N + i, g == 0.f ? 0 : N - i, p[q][c]);
-#pragma unroll
-          for (int j = 0; j < 8; j++) h[c][j] = fmaf(g, p[q][c][j], h[c][j]);
-        }
-      }
+      for (int q = 0; q < KR; q++) add_slot(q < k ? (gates ? gates[q] : 1.f) : 0.f, pr[q]);
     } else {
       for (int q = 0; q < k; q++) {
-        const float g = a.gates ? a.gates[(size_t)t * k + q] : 1.f;
-        if (g == 0.f) continue;
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-          const int i = (threadIdx.x + c * blockDim.x) * 8;
-          load8(proj + (size_t)q * N + i, N - i, p[0][c]);
-#pragma unroll
-          for (int j = 0; j < 8; j++) h[c][j] = fmaf(g, p[0][c][j], h[c][j]);
-        }
+        fetch_row(proj + (size_t)q * N, N, pr[0]);
+        add_slot(gates ? gates[q] : 1.f, pr[0]);
       }
     }
     // the gradient at x_out: the stream's own and the next norm's
-    float xo[CH][8], dn[CH][8];
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      const int i = (threadIdx.x + c * blockDim.x) * 8;
-      if (a.dx_out)
-        load8(static_cast<const X*>(a.dx_out) + row + i, N - i, grad[c]);
-      else
+      if (dx_out) {
+        widen8(gr[c], grad[c]);
+      } else {
+#pragma unroll
         for (int j = 0; j < 8; j++) grad[c][j] = 0.f;
+      }
       if (a.dxn) {
-        float wv[8];
-        load8(static_cast<const X*>(a.x_out) + row + i, N - i, xo[c]);
-        load8(a.dxn + row + i, N - i, dn[c]);
-        load8(a.w_next + i, N - i, wv);
+        float wv[8], xv[8], dv[8];
+        widen8(xo[c], xv);
+        widen8(dn[c], dv);
+        widen8(wn[c], wv);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          s[0] = fmaf(xo[c][j], xo[c][j], s[0]);
-          s[1] = fmaf(xo[c][j], dn[c][j] * wv[j], s[1]);
+          s[0] = fmaf(xv[j], xv[j], s[0]);
+          s[1] = fmaf(xv[j], dv[j] * wv[j], s[1]);
         }
       }
 #pragma unroll
@@ -321,23 +372,22 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
       const float m = s[1] * a.inv_n * r;
 #pragma unroll
       for (int c = 0; c < CH; c++) {
-        const int i = (threadIdx.x + c * blockDim.x) * 8;
-        float wv[8];
-        load8(a.w_next + i, N - i, wv);
+        float wv[8], xv[8], dv[8];
+        widen8(xo[c], xv);
+        widen8(dn[c], dv);
+        widen8(wn[c], wv);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const float unit = xo[c][j] * r;
-          dw_next[c][j] = fmaf(dn[c][j], unit, dw_next[c][j]);
-          grad[c][j] = fmaf(r, fmaf(-unit, m, dn[c][j] * wv[j]), grad[c][j]);
+          const float unit = xv[j] * r;
+          dw_next[c][j] = fmaf(dv[j], unit, dw_next[c][j]);
+          grad[c][j] = fmaf(r, fmaf(-unit, m, dv[j] * wv[j]), grad[c][j]);
         }
       }
     }
     if (a.dx) {
 #pragma unroll
-      for (int c = 0; c < CH; c++) {
-        const int i = (threadIdx.x + c * blockDim.x) * 8;
-        store8(static_cast<X*>(a.dx) + row + i, N - i, grad[c]);
-      }
+      for (int c = 0; c < CH; c++)
+        store8(static_cast<X*>(a.dx) + row + chunk_at(c), N - chunk_at(c), grad[c]);
     }
     // through the residual scale and the output norm: grad becomes dh
 #pragma unroll
@@ -349,9 +399,8 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
       float d[1] = {0.f};
 #pragma unroll
       for (int c = 0; c < CH; c++) {
-        const int i = (threadIdx.x + c * blockDim.x) * 8;
         float wv[8];
-        load8(a.w_post + i, N - i, wv);
+        widen8(wp[c], wv);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
           const float unit = h[c][j] * r;
@@ -368,66 +417,63 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
         for (int j = 0; j < 8; j++) grad[c][j] = r * fmaf(-(h[c][j] * r), m, grad[c][j]);
     }
     // the slots: dproj = gate * dh, dgate = <dh, proj>
-    auto slot = [&](int q, const float (&pv)[CH][8], float g) {
+    auto slot = [&](int q, const Raw8<P> (&rows)[CH], float g) {
       if (a.dproj) {
 #pragma unroll
         for (int c = 0; c < CH; c++) {
-          const int i = (threadIdx.x + c * blockDim.x) * 8;
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) o[j] = g * grad[c][j];
-          store8(static_cast<P*>(a.dproj) + row * k + (size_t)q * N + i, N - i, o);
+          store8(static_cast<P*>(a.dproj) + row * k + (size_t)q * N + chunk_at(c), N - chunk_at(c), o);
         }
       }
       if (a.dgates) {
         float d = 0.f;
 #pragma unroll
-        for (int c = 0; c < CH; c++)
+        for (int c = 0; c < CH; c++) {
+          float p[8];
+          widen8(rows[c], p);
 #pragma unroll
-          for (int j = 0; j < 8; j++) d = fmaf(grad[c][j], pv[c][j], d);
-        d = wave_sum(d);
-        if (lane == 0) redg[parity][q * kMaxWaves + wave] = d;
+          for (int j = 0; j < 8; j++) d = fmaf(grad[c][j], p[j], d);
+        }
+        d = group_sum<64>(d);
+        if (lane == 0) redg[parity][q][wave] = d;
       }
     };
     if constexpr (KR > 0) {
 #pragma unroll
       for (int q = 0; q < KR; q++) {
-        if (q < k) slot(q, p[q], a.gates ? a.gates[(size_t)t * k + q] : 1.f);
+        if (q < k) slot(q, pr[q], gates ? gates[q] : 1.f);
       }
     } else {
       for (int q = 0; q < k; q++) {
-        const float g = a.gates ? a.gates[(size_t)t * k + q] : 1.f;
-        if (a.dgates) {
-#pragma unroll
-          for (int c = 0; c < CH; c++) {
-            const int i = (threadIdx.x + c * blockDim.x) * 8;
-            load8(proj + (size_t)q * N + i, g == 0.f ? 0 : N - i, p[0][c]);
-          }
-        }
-        slot(q, p[0], g);
+        if (a.dgates) fetch_row(proj + (size_t)q * N, N, pr[0]);
+        slot(q, pr[0], gates ? gates[q] : 1.f);
       }
     }
     if (a.dgates) {
       __syncthreads();
       if ((int)threadIdx.x < k) {
         float d = 0.f;
-        for (int w = 0; w < waves; w++) d += redg[parity][threadIdx.x * kMaxWaves + w];
-        a.dgates[(size_t)t * k + threadIdx.x] = a.gates[(size_t)t * k + threadIdx.x] == 0.f ? 0.f : d;
+        for (int w = 0; w < waves; w++) d += redg[parity][threadIdx.x][w];
+        a.dgates[(size_t)t * k + threadIdx.x] = gates[threadIdx.x] == 0.f ? 0.f : d;
       }
     }
   }
 #pragma unroll
   for (int c = 0; c < CH; c++) {
-    const int i = (threadIdx.x + c * blockDim.x) * 8;
-    if (a.part_post) store8(a.part_post + (size_t)blockIdx.x * N + i, N - i, dw_post[c]);
-    if (a.part_next) store8(a.part_next + (size_t)blockIdx.x * N + i, N - i, dw_next[c]);
+    const size_t at = (size_t)blockIdx.x * N + chunk_at(c);
+    if (a.part_post) store8(a.part_post + at, N - chunk_at(c), dw_post[c]);
+    if (a.part_next) store8(a.part_next + at, N - chunk_at(c), dw_next[c]);
   }
 }
 
-// out[n] = sum_g part[g][n], g ascending within 16 interleaved row groups that
-// are then added in order: 16 columns (64 bytes of a row) x 16 row groups.
+// out[n] = sum_g part[g][n]: 16 columns (64 bytes of a row) x 64 interleaved
+// groups of rows, each added in order (eight loads under way), then the groups
+// in order.
 constexpr int kSumCols = 16;
-constexpr int kSumGroups = 16;
+constexpr int kSumGroups = 64;
+constexpr int kSumDepth = 8;
 __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const float* __restrict__ part0, float* out0,
                                                                           const float* __restrict__ part1, float* out1,
                                                                           int G, int N) {
@@ -437,8 +483,18 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const 
   const int col = threadIdx.x % kSumCols, grp = threadIdx.x / kSumCols;
   const int n = blockIdx.x * kSumCols + col;
   float s = 0.f;
-  if (n < N)
-    for (int g = grp; g < G; g += kSumGroups) s += part[(size_t)g * N + n];
+  if (n < N) {
+    for (int g = grp; g < G; g += kSumGroups * kSumDepth) {
+      float v[kSumDepth];
+#pragma unroll
+      for (int u = 0; u < kSumDepth; u++) {
+        const int gu = g + u * kSumGroups;
+        v[u] = part[(size_t)min(gu, G - 1) * N + n];
+      }
+#pragma unroll
+      for (int u = 0; u < kSumDepth; u++) s += g + u * kSumGroups < G ? v[u] : 0.f;
+    }
+  }
   red[grp][col] = s;
   __syncthreads();
   if (grp == 0 && n < N) {
