@@ -285,14 +285,16 @@ __global__ __launch_bounds__(kMaxRowThreads) void norm_backward_kernel(const uin
 // Gradients of moe_combine_norm.  KR > 0: the k <= KR slots' rows stay in
 // registers between the combine and the gates' gradients; KR = 0: they are
 // read again.  dx may be dx_out itself.
+//
+// A workgroup's next row is fetched into the registers of this row as soon as
+// these have been used, ahead of this row's stores: loads and stores complete
+// in the order of their issue, so a load behind the stores would wait for them.
 template <typename X, typename P, int CH, int KR>
 __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
   constexpr int KH = KR > 0 ? KR : 1;
   __shared__ __align__(16) float red1[2][3][kMaxWaves], red2[2][1][kMaxWaves], redg[2][kMaxTopK][kMaxWaves];
   const int N = a.N, k = a.k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const X* dx_out = static_cast<const X*>(a.dx_out);
-  const X* x_out = static_cast<const X*>(a.x_out);
   float dw_post[CH][8], dw_next[CH][8];
   Raw8<uint16_t> wp[CH], wn[CH];
   if (a.w_post) fetch_row(a.w_post, N, wp);
@@ -301,25 +303,35 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
   for (int c = 0; c < CH; c++)
 #pragma unroll
     for (int j = 0; j < 8; j++) dw_post[c][j] = dw_next[c][j] = 0.f;
-  int parity = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
+  Raw8<P> pr[KH][CH];
+  Raw8<X> gr[CH], xo[CH];
+  Raw8<uint16_t> dn[CH];
+  auto fetch_stream = [&](int t) {
     const size_t row = (size_t)t * N;
-    const P* proj = static_cast<const P*>(a.proj) + row * k;
-    const float* gates = a.gates ? a.gates + (size_t)t * k : nullptr;
-    Raw8<P> pr[KH][CH];
-    Raw8<X> gr[CH], xo[CH];
-    Raw8<uint16_t> dn[CH];
-    float h[CH][8], grad[CH][8], s[3] = {0.f, 0.f, 0.f};
+    if (a.dx_out) fetch_row(static_cast<const X*>(a.dx_out) + row, N, gr);
+    if (a.dxn) {
+      fetch_row(static_cast<const X*>(a.x_out) + row, N, xo);
+      fetch_row(a.dxn + row, N, dn);
+    }
+  };
+  auto fetch_slot = [&](int t, int q, Raw8<P> (&rows)[CH]) {
+    fetch_row(static_cast<const P*>(a.proj) + ((size_t)t * k + q) * N, N, rows);
+  };
+  auto fetch_slots = [&](int t) {
     if constexpr (KR > 0) {
 #pragma unroll
       for (int q = 0; q < KR; q++)
-        if (q < k) fetch_row(proj + (size_t)q * N, N, pr[q]);
+        if (q < k) fetch_slot(t, q, pr[q]);
     }
-    if (dx_out) fetch_row(dx_out + row, N, gr);
-    if (a.dxn) {
-      fetch_row(x_out + row, N, xo);
-      fetch_row(a.dxn + row, N, dn);
-    }
+  };
+  fetch_slots(blockIdx.x);
+  fetch_stream(blockIdx.x);
+  int parity = 0;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
+    const bool more = t + (int)gridDim.x < a.T;
+    const size_t row = (size_t)t * N;
+    const float* gates = a.gates ? a.gates + (size_t)t * k : nullptr;
+    float h[CH][8], grad[CH][8], s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; c++)
 #pragma unroll
@@ -336,17 +348,18 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
     };
     if constexpr (KR > 0) {
 #pragma unroll
-      for (int q = 0; q < KR; q++) add_slot(q < k ? (gates ? gates[q] : 1.f) : 0.f, pr[q]);
+      for (int q = 0; q < KR; q++)
+        if (q < k) add_slot(gates ? gates[q] : 1.f, pr[q]);
     } else {
       for (int q = 0; q < k; q++) {
-        fetch_row(proj + (size_t)q * N, N, pr[0]);
+        fetch_slot(t, q, pr[0]);
         add_slot(gates ? gates[q] : 1.f, pr[0]);
       }
     }
     // the gradient at x_out: the stream's own and the next norm's
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      if (dx_out) {
+      if (a.dx_out) {
         widen8(gr[c], grad[c]);
       } else {
 #pragma unroll
@@ -384,6 +397,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
         }
       }
     }
+    if (more) fetch_stream(t + gridDim.x);
     if (a.dx) {
 #pragma unroll
       for (int c = 0; c < CH; c++)
@@ -416,39 +430,43 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
 #pragma unroll
         for (int j = 0; j < 8; j++) grad[c][j] = r * fmaf(-(h[c][j] * r), m, grad[c][j]);
     }
-    // the slots: dproj = gate * dh, dgate = <dh, proj>
-    auto slot = [&](int q, const Raw8<P> (&rows)[CH], float g) {
-      if (a.dproj) {
+    // the slots: dgate = <dh, proj>, dproj = gate * dh
+    auto dot_slot = [&](int q, const Raw8<P> (&rows)[CH]) {
+      float d = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; c++) {
+        float p[8];
+        widen8(rows[c], p);
+#pragma unroll
+        for (int j = 0; j < 8; j++) d = fmaf(grad[c][j], p[j], d);
+      }
+      d = group_sum<64>(d);
+      if (lane == 0) redg[parity][q][wave] = d;
+    };
+    if (a.dgates) {
+      if constexpr (KR > 0) {
+#pragma unroll
+        for (int q = 0; q < KR; q++)
+          if (q < k) dot_slot(q, pr[q]);
+      } else {
+        for (int q = 0; q < k; q++) {
+          fetch_slot(t, q, pr[0]);
+          dot_slot(q, pr[0]);
+        }
+      }
+    }
+    if (more) fetch_slots(t + gridDim.x);
+    if (a.dproj) {
+      for (int q = 0; q < k; q++) {
+        const float g = gates ? gates[q] : 1.f;
+        P* out = static_cast<P*>(a.dproj) + (row * k + (size_t)q * N);
 #pragma unroll
         for (int c = 0; c < CH; c++) {
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) o[j] = g * grad[c][j];
-          store8(static_cast<P*>(a.dproj) + row * k + (size_t)q * N + chunk_at(c), N - chunk_at(c), o);
+          store8(out + chunk_at(c), N - chunk_at(c), o);
         }
-      }
-      if (a.dgates) {
-        float d = 0.f;
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-          float p[8];
-          widen8(rows[c], p);
-#pragma unroll
-          for (int j = 0; j < 8; j++) d = fmaf(grad[c][j], p[j], d);
-        }
-        d = group_sum<64>(d);
-        if (lane == 0) redg[parity][q][wave] = d;
-      }
-    };
-    if constexpr (KR > 0) {
-#pragma unroll
-      for (int q = 0; q < KR; q++) {
-        if (q < k) slot(q, pr[q], gates ? gates[q] : 1.f);
-      }
-    } else {
-      for (int q = 0; q < k; q++) {
-        if (a.dgates) fetch_row(proj + (size_t)q * N, N, pr[0]);
-        slot(q, pr[0], gates ? gates[q] : 1.f);
       }
     }
     if (a.dgates) {
