@@ -67,7 +67,7 @@ typedef enum {
 #define MXFP4_DECODE_MAX_T 64        /* mxfp4_moe_decode_batch: tokens ranked one per lane */
 
 #define MOE_NORM_MAX_N 16384         /* the norms: a row stays in one workgroup's registers */
-#define MOE_BALANCE_MAX_T (1 << 30)  /* moe_balance, moe_route_backward */
+#define MOE_MAX_TOKENS (1 << 30)     /* the norms, moe_balance, moe_route_backward */
 
 /* Element types of the arguments that take one (`const void*` with a *_dtype). */
 #define MXFP4_DTYPE_BF16 0
@@ -465,7 +465,8 @@ int moe_combine(const float* proj, const float* gates, int T, int k, int N, floa
  * The block's input norm: the root-mean-square norm of each row of the
  * residual stream, the input of mxfp4_moe_router and of the experts.
  *
- *   x       [T, N] bf16 or fp32 (x_dtype), T >= 0, 1 <= N <= MOE_NORM_MAX_N.
+ *   x       [T, N] bf16 or fp32 (x_dtype), 0 <= T <= MOE_MAX_TOKENS,
+ *           1 <= N <= MOE_NORM_MAX_N.
  *   w       [N] bf16.
  *   eps     > 0.
  *   xn      [T, N] bf16 out: xn[t, n] = bf16(x[t, n] * r * w[n]) with
@@ -505,7 +506,7 @@ int moe_norm_backward(const uint16_t* dxn, const void* x, int x_dtype, const uin
  *   proj    [T, k, N] fp32 or bf16 (proj_dtype): the experts' outputs
  *           (mxfp4_expert_proj's out), or with k = 1 and gates NULL any block's
  *           output (moe_combine's or mxfp4_expert_proj_combine's y).
- *           T >= 0, 1 <= k <= MXFP4_MAX_TOPK, 1 <= N <= MOE_NORM_MAX_N.
+ *           0 <= T <= MOE_MAX_TOKENS, 1 <= k <= MXFP4_MAX_TOPK, 1 <= N <= MOE_NORM_MAX_N.
  *   gates   [T, k] fp32, or NULL: every gate 1.  h = sum_s gates[t, s] *
  *           proj[t, s, :] in slot order, the bits of moe_combine: a slot with gate 0
  *           adds nothing, whatever its row holds.
@@ -545,7 +546,7 @@ size_t moe_combine_norm_backward_workspace_size(int T, int N);
  *           gradient of the output norm at h for scale * G (or scale * G itself).
  *           Exactly 0 for a slot with gate 0.
  *   dgates  [T, k] fp32 (gates given): sum_n dh[t, n] * proj[t, s, n]; 0 for a slot
- *           with gate 0, whose row is not read.
+ *           with gate 0, whatever its row holds.
  *   dw_post [N] fp32 (w_post given): sum_t scale * G * h * r_h.
  *   dw_next [N] fp32 (dxn given): sum_t dxn * x_out * r.
  *   All in fp32 with sums in a fixed order, each output rounded once.  T = 0 writes
@@ -568,7 +569,7 @@ size_t moe_balance_workspace_size(int T, int E, int S);
  * The load of the experts: per-expert counts, the balance loss and the z loss
  * of a batch of packed sequences.
  *
- *   logits  [T, E] bf16: the router logits; 0 <= T <= MOE_BALANCE_MAX_T,
+ *   logits  [T, E] bf16: the router logits; 0 <= T <= MOE_MAX_TOKENS,
  *           1 <= E <= MXFP4_MAX_EXPERTS.
  *   topk_ids [T, k] i32: the routing (mxfp4_moe_route_group);
  *           1 <= k <= min(E, MXFP4_MAX_TOPK).

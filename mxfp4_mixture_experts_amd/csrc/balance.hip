@@ -46,14 +46,15 @@ __device__ __forceinline__ bool group_any(bool p) {
   return ((m >> base) & ((1ull << (L & 63)) - 1)) != 0;
 }
 
-// a lane's eight logits; -inf behind the last expert
-__device__ __forceinline__ void load_logits(const uint16_t* p, int valid, float (&v)[8]) {
+// a lane's eight logits (from expert e0); -inf behind the last expert
+__device__ __forceinline__ void load_logits(const uint16_t* row, int e0, int E, float (&v)[8]) {
   Raw8<uint16_t> r;
-  fetch8(p, valid, r);
+  fetch8(row, e0, E, E < 8, r);
+  if (ragged(E)) settle8(e0, E, r);
   widen8(r, v);
-  if (valid < 8) {
+  if (e0 + 8 > E) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = i < valid ? v[i] : -INFINITY;
+    for (int i = 0; i < 8; i++) v[i] = e0 + i < E ? v[i] : -INFINITY;
   }
 }
 
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void balance_pieces_kernel(const uint16_t
     int n = 0;
     for (int t = a + group; t < b; t += kGroups) {
       float v[8], z;
-      load_logits(logits + (size_t)t * E + e0, E - e0, v);
+      load_logits(logits + (size_t)t * E, e0, E, v);
       bool valid = false;
       for (int q = j; q < k; q += L) valid |= (unsigned)ids[(size_t)t * k + q] < (unsigned)E;
       const bool some = group_any<L>(valid);
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, z = 0.f;
     bool live = true;
     if constexpr (LOSSES) {
-      load_logits(logits + (size_t)t * E + e0, E - e0, v);
+      load_logits(logits + (size_t)t * E, e0, E, v);
       while (seq && t >= s_end && s < S) {
         s++;
         s_end = s < S ? seq[s + 1] : T;
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         }
       }
     }
-    store8(dlogits + (size_t)t * E + e0, E - e0, v);
+    store8(dlogits + (size_t)t * E, e0, E, v);
   }
 }
 

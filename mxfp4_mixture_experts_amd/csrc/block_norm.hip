@@ -13,17 +13,18 @@
 //
 // All of it is a stream through HBM with one to three row sums in the middle.
 // A row stays in registers between them, so each input is read once and each
-// output written once: a row belongs to a workgroup of NT threads (a multiple
-// of 64, at most 512), and thread i holds the chunks i, i + NT, ... of eight
-// elements (one or two 16-byte loads each).  NT follows the row's length alone
-// (row_threads), so every kernel here adds a row in the same order and the
-// norm of a stored row is the same bits whichever entry point takes it.
-// Sums are fp32: over the thread's elements, the wave's lanes, the waves.
+// output written once.  A row belongs to a team of threads, and thread i of it
+// holds the chunks i, i + team, ... of eight elements (one or two 16-byte loads
+// each): a power of two of lanes up to N = 512, then whole waves, at most eight
+// (and two or four chunks a thread beyond N = 4096).  The team follows the row's
+// length alone (team_threads), so every kernel here adds a row in the same
+// order and the norm of a stored row is the same bits whichever entry point
+// takes it.  Sums are fp32: over the thread's elements, the lanes, the waves.
 //
 // The weights' gradients add over the rows: each workgroup walks the rows
-// b, b + grid, ... and keeps its columns' sums in registers, writes them to
-// the workspace once, and a second launch adds the workgroups' sums in order
-// (no atomics: the same inputs give the same bits).
+// b, b + grid, ... and keeps its columns' sums in registers, adds its teams' and
+// writes them to the workspace once, and a second launch adds the workgroups'
+// sums in order (no atomics: the same inputs give the same bits).
 
 #include <type_traits>
 
@@ -33,27 +34,36 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kMaxRowThreads = 512;
-constexpr int kMaxWaves = kMaxRowThreads / 64;
+constexpr int kMaxTeam = 512;
+constexpr int kMaxWaves = kMaxTeam / 64;  // of a team
+constexpr int kMaxWaveTeams = 4;          // teams of several waves in a workgroup (of 128 threads each)
 
-// chunks of eight per thread, and the threads of a row
-int row_chunks_per_thread(int N) {
+// chunks of eight per thread, and the threads of a row's team
+int chunks_per_thread(int N) {
   const int chunks = (N + 7) / 8;
-  return chunks <= kMaxRowThreads ? 1 : chunks <= 2 * kMaxRowThreads ? 2 : 4;
+  return chunks <= kMaxTeam ? 1 : chunks <= 2 * kMaxTeam ? 2 : 4;
 }
-int row_threads(int N) {
-  const int chunks = (N + 7) / 8, ch = row_chunks_per_thread(N);
-  return ((chunks + ch - 1) / ch + 63) / 64 * 64;
+int team_threads(int N) {
+  const int chunks = (N + 7) / 8, ch = chunks_per_thread(N);
+  if (chunks > 64) return ((chunks + ch - 1) / ch + 63) / 64 * 64;
+  int t = 1;
+  while (t < chunks) t *= 2;
+  return t;
 }
 
-// f(an element of the row type, the chunks per thread as a constant)
+// f(an element of the row type, the chunks per thread as a constant, whether
+// the team is a part of a wave as a constant)
 template <typename F>
 void with_row_type(bool f32, int N, F f) {
   auto with_chunks = [&](auto elem) {
-    switch (row_chunks_per_thread(N)) {
-      case 1: f(elem, std::integral_constant<int, 1>{}); break;
-      case 2: f(elem, std::integral_constant<int, 2>{}); break;
-      default: f(elem, std::integral_constant<int, 4>{}); break;
+    if (team_threads(N) < 64) {
+      f(elem, std::integral_constant<int, 1>{}, std::true_type{});
+      return;
+    }
+    switch (chunks_per_thread(N)) {
+      case 1: f(elem, std::integral_constant<int, 1>{}, std::false_type{}); break;
+      case 2: f(elem, std::integral_constant<int, 2>{}, std::false_type{}); break;
+      default: f(elem, std::integral_constant<int, 4>{}, std::false_type{}); break;
     }
   };
   if (f32)
@@ -62,27 +72,59 @@ void with_row_type(bool f32, int N, F f) {
     with_chunks(uint16_t{});
 }
 
-// Sums of M values over the workgroup, added lane by lane and then wave by
-// wave; every thread receives them.  red[m] holds value m of each wave, 0
-// where the row has fewer waves (wave 0 writes those); a buffer is free again after the
-// barrier of the next call, so calls take turns between two.
-template <int M>
-__device__ __forceinline__ void row_sum(float (&v)[M], float (&red)[M][kMaxWaves]) {
+// The teams of a workgroup: blockDim = (threads of a team, teams).  PART: a team
+// is a part of a wave (else its number is the same for a whole wave).
+template <bool PART>
+struct Team {
+  int threads, count;  // of a team; teams
+  int id, me;          // this thread's team and its place there
+  bool tiny;           // rows of fewer than eight elements
+  __device__ __forceinline__ explicit Team(int N) : threads(blockDim.x), count(blockDim.y), me(threadIdx.x) {
+    id = PART ? (int)threadIdx.y : __builtin_amdgcn_readfirstlane(threadIdx.y);
+    tiny = PART && N < 8;
+  }
+  // the thread's chunk c starts at this element
+  __device__ __forceinline__ int at(int c) const { return (me + c * threads) * 8; }
+};
+
+template <typename E, bool PART, int CH>
+__device__ __forceinline__ void fetch_row(const Team<PART>& team, const E* row, int N, Raw8<E> (&r)[CH]) {
 #pragma unroll
-  for (int m = 0; m < M; m++) v[m] = group_sum<64>(v[m]);
-  if (blockDim.x == 64) return;
-  const int lane = threadIdx.x & 63;
-  const bool spare = threadIdx.x < kMaxWaves && threadIdx.x >= (blockDim.x >> 6);
-  if (lane == 0 || spare) {
+  for (int c = 0; c < CH; c++) fetch8(row, team.at(c), N, team.tiny, r[c]);
+}
+template <typename E, bool PART, int CH>
+__device__ __forceinline__ void settle_row(const Team<PART>& team, int N, Raw8<E> (&r)[CH]) {
 #pragma unroll
-    for (int m = 0; m < M; m++) red[m][spare ? lane : threadIdx.x >> 6] = spare ? 0.f : v[m];
+  for (int c = 0; c < CH; c++) settle8(team.at(c), N, r[c]);
+}
+
+// the sum over a team's lanes within a wave; every lane receives it
+template <bool PART>
+__device__ __forceinline__ float lane_sum(const Team<PART>& team, float v) {
+  if constexpr (PART) return group_sum_up_to_32(v, team.threads);
+  return group_sum<64>(v);
+}
+
+// Sums of M values over each team, added lane by lane and then wave by wave;
+// every thread receives its team's.  red[.][m] holds value m of each wave, 0
+// where the team has fewer waves (its first wave writes those); a buffer is free
+// again after the barrier of the next call, so calls take turns between two.
+template <bool PART, int M>
+__device__ __forceinline__ void row_sum(const Team<PART>& team, float (&v)[M], float (&red)[kMaxWaveTeams][M][kMaxWaves]) {
+#pragma unroll
+  for (int m = 0; m < M; m++) v[m] = lane_sum(team, v[m]);
+  if (PART || team.threads == 64) return;
+  const bool spare = team.me < kMaxWaves && team.me >= (team.threads >> 6);
+  if ((team.me & 63) == 0 || spare) {
+#pragma unroll
+    for (int m = 0; m < M; m++) red[team.id][m][spare ? team.me : team.me >> 6] = spare ? 0.f : v[m];
   }
   __syncthreads();
 #pragma unroll
   for (int m = 0; m < M; m++) {
-    float s = red[m][0];
+    float s = red[team.id][m][0];
 #pragma unroll
-    for (int w = 1; w < kMaxWaves; w++) s += red[m][w];
+    for (int w = 1; w < kMaxWaves; w++) s += red[team.id][m][w];
     v[m] = s;
   }
 }
@@ -91,25 +133,22 @@ __device__ __forceinline__ float rms_scale(float sum, float inv_n, float eps) {
   return rsqrtf(fmaf(sum, inv_n, eps));
 }
 
-// a thread's chunks of a row: c = 0 .. CH - 1 at element (thread + c * threads) * 8
-__device__ __forceinline__ int chunk_at(int c) { return (threadIdx.x + c * blockDim.x) * 8; }
-
-template <typename E, int CH>
-__device__ __forceinline__ void fetch_row(const E* row, int N, Raw8<E> (&r)[CH]) {
-#pragma unroll
-  for (int c = 0; c < CH; c++) fetch8(row + chunk_at(c), N - chunk_at(c), r[c]);
-}
-
-template <typename X, int CH>
-__global__ __launch_bounds__(kMaxRowThreads) void norm_kernel(const X* __restrict__ x, const uint16_t* __restrict__ w,
-                                                              int N, float inv_n, float eps,
-                                                              uint16_t* __restrict__ xn) {
-  __shared__ __align__(16) float red[1][kMaxWaves];
-  const size_t row = (size_t)blockIdx.x * N;
+template <typename X, int CH, bool PART>
+__global__ __launch_bounds__(kMaxTeam) void norm_kernel(const X* __restrict__ x, const uint16_t* __restrict__ w, int T,
+                                                        int N, float inv_n, float eps, uint16_t* __restrict__ xn) {
+  __shared__ __align__(16) float red[kMaxWaveTeams][1][kMaxWaves];
+  const Team<PART> team(N);
+  const int t = blockIdx.x * team.count + team.id;
+  const size_t row = (size_t)t * N;
+  const int Nt = t < T ? N : 0;
   Raw8<X> xr[CH];
   Raw8<uint16_t> wr[CH];
-  fetch_row(x + row, N, xr);
-  fetch_row(w, N, wr);
+  fetch_row(team, x + row, Nt, xr);
+  fetch_row(team, w, N, wr);
+  if (ragged(N)) {
+    settle_row(team, Nt, xr);
+    settle_row(team, N, wr);
+  }
   float s[1] = {0.f};
 #pragma unroll
   for (int c = 0; c < CH; c++) {
@@ -118,7 +157,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void norm_kernel(const X* __restric
 #pragma unroll
     for (int j = 0; j < 8; j++) s[0] = fmaf(v[j], v[j], s[0]);
   }
-  row_sum(s, red);
+  row_sum(team, s, red);
   const float r = rms_scale(s[0], inv_n, eps);
 #pragma unroll
   for (int c = 0; c < CH; c++) {
@@ -127,26 +166,29 @@ __global__ __launch_bounds__(kMaxRowThreads) void norm_kernel(const X* __restric
     widen8(wr[c], wv);
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] = v[j] * r * wv[j];
-    store8(xn + row + chunk_at(c), N - chunk_at(c), v);
+    store8(xn + row, team.at(c), Nt, v);
   }
 }
 
 // The block's output.  x_out may be x itself: each element is read and written
 // by one thread, in this order.
-template <typename X, typename P, int CH>
-__global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const CombineNormArgs a) {
+template <typename X, typename P, int CH, bool PART>
+__global__ __launch_bounds__(kMaxTeam) void combine_norm_kernel(const CombineNormArgs a) {
   constexpr int kSlots = CH == 1 ? 4 : CH == 2 ? 2 : 1;  // slots whose rows are under way together
-  __shared__ __align__(16) float red[2][1][kMaxWaves];
+  __shared__ __align__(16) float red[2][kMaxWaveTeams][1][kMaxWaves];
   const int N = a.N, k = a.k;
-  const size_t t = blockIdx.x, row = t * N;
+  const Team<PART> team(N);
+  const int t = blockIdx.x * team.count + team.id;
+  const int Nt = t < a.T ? N : 0;
+  const size_t row = (size_t)t * N;
   const X* x = static_cast<const X*>(a.x) + row;
   X* x_out = static_cast<X*>(a.x_out) + row;
   const P* proj = static_cast<const P*>(a.proj) + row * k;
   Raw8<X> xr[CH];
   Raw8<uint16_t> wp[CH], wn[CH];
-  fetch_row(x, N, xr);
-  if (a.w_post) fetch_row(a.w_post, N, wp);
-  if (a.xn) fetch_row(a.w_next, N, wn);
+  fetch_row(team, x, Nt, xr);
+  if (a.w_post) fetch_row(team, a.w_post, N, wp);
+  if (a.xn) fetch_row(team, a.w_next, N, wn);
   float h[CH][8], s[1] = {0.f};
 #pragma unroll
   for (int c = 0; c < CH; c++)
@@ -158,8 +200,12 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const Comb
 #pragma unroll
     for (int u = 0; u < kSlots; u++) {
       const int q = min(q0 + u, k - 1);
-      g[u] = q0 + u >= k ? 0.f : a.gates ? a.gates[t * k + q] : 1.f;
-      fetch_row(proj + (size_t)q * N, N, pr[u]);
+      g[u] = q0 + u >= k || Nt == 0 ? 0.f : a.gates ? a.gates[(size_t)t * k + q] : 1.f;
+      fetch_row(team, proj + (size_t)q * N, Nt, pr[u]);
+    }
+    if (ragged(N)) {
+#pragma unroll
+      for (int u = 0; u < kSlots; u++) settle_row(team, Nt, pr[u]);
     }
 #pragma unroll
     for (int u = 0; u < kSlots; u++) {
@@ -173,12 +219,17 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const Comb
       }
     }
   }
+  if (ragged(N)) {
+    settle_row(team, Nt, xr);
+    if (a.w_post) settle_row(team, N, wp);
+    if (a.xn) settle_row(team, N, wn);
+  }
   if (a.w_post) {
 #pragma unroll
     for (int c = 0; c < CH; c++)
 #pragma unroll
       for (int j = 0; j < 8; j++) s[0] = fmaf(h[c][j], h[c][j], s[0]);
-    row_sum(s, red[0]);
+    row_sum(team, s, red[0]);
     const float r = rms_scale(s[0], a.inv_n, a.eps);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
@@ -198,10 +249,13 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const Comb
       h[c][j] = rounded(fmaf(a.scale, h[c][j], xv[j]), x);
       s[0] = fmaf(h[c][j], h[c][j], s[0]);
     }
-    store8(x_out + chunk_at(c), N - chunk_at(c), h[c]);
+    if (a.stream)
+      store8<true>(x_out, team.at(c), Nt, h[c]);
+    else
+      store8(x_out, team.at(c), Nt, h[c]);
   }
   if (!a.xn) return;
-  row_sum(s, red[1]);
+  row_sum(team, s, red[1]);
   const float r = rms_scale(s[0], a.inv_n, a.eps);
 #pragma unroll
   for (int c = 0; c < CH; c++) {
@@ -209,96 +263,128 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_kernel(const Comb
     widen8(wn[c], wv);
 #pragma unroll
     for (int j = 0; j < 8; j++) h[c][j] = h[c][j] * r * wv[j];
-    store8(a.xn + row + chunk_at(c), N - chunk_at(c), h[c]);
+    store8(a.xn + row, team.at(c), Nt, h[c]);
   }
 }
 
-// Gradients of moe_norm.  dx may be dres itself.  The loads of a workgroup's
-// next row are issued before the sums of this one.
-template <typename X, int CH>
-__global__ __launch_bounds__(kMaxRowThreads) void norm_backward_kernel(const uint16_t* dxn, const X* x,
-                                                                       const uint16_t* w, const X* dres, int T, int N,
-                                                                       float inv_n, float eps, X* dx, float* part) {
-  __shared__ __align__(16) float red[2][2][kMaxWaves];
+// A workgroup's column sums to row blockIdx.x of part: the teams' in order.
+template <bool PART, int CH>
+__device__ __forceinline__ void store_columns(const Team<PART>& team, float (&dw)[CH][8], float* buf, int N, float* part) {
+  if (CH == 1 && team.count > 1) {
+    float* mine = buf + (size_t)(team.id * team.threads + team.me) * 8;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; j++) mine[j] = dw[0][j];
+    __syncthreads();
+    if (team.id > 0) return;
+    for (int q = 1; q < team.count; q++) {
+      mine += team.threads * 8;
+#pragma unroll
+      for (int j = 0; j < 8; j++) dw[0][j] += mine[j];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; c++) store8(part + (size_t)blockIdx.x * N, team.at(c), N, dw[c]);
+}
+
+// Gradients of moe_norm.  dx may be dres itself.
+//
+// A team's next row is fetched ahead of this row's stores: loads and stores
+// complete in the order of their issue, so a load behind the stores would wait
+// for them.
+template <typename X, int CH, bool PART>
+__global__ __launch_bounds__(kMaxTeam) void norm_backward_kernel(const uint16_t* dxn, const X* x, const uint16_t* w,
+                                                                 const X* dres, int T, int N, float inv_n, float eps,
+                                                                 X* dx, float* part) {
+  __shared__ __align__(16) float red[2][kMaxWaveTeams][2][kMaxWaves];
+  __shared__ __align__(16) float cols[CH == 1 ? kMaxTeam * 8 : 8];
+  const Team<PART> team(N);
+  const int step = gridDim.x * team.count;
   float dw[CH][8];
   Raw8<uint16_t> wr[CH];
-  fetch_row(w, N, wr);
+  fetch_row(team, w, N, wr);
 #pragma unroll
   for (int c = 0; c < CH; c++)
 #pragma unroll
     for (int j = 0; j < 8; j++) dw[c][j] = 0.f;
-  Raw8<X> x_next[CH], r_next[CH];
-  Raw8<uint16_t> d_next[CH];
+  Raw8<X> xr[CH], rr[CH];
+  Raw8<uint16_t> dr[CH];
   auto fetch = [&](int t) {
     const size_t row = (size_t)t * N;
-    fetch_row(x + row, N, x_next);
-    fetch_row(dxn + row, N, d_next);
-    if (dres) fetch_row(dres + row, N, r_next);
+    const int Nt = t < T ? N : 0;
+    fetch_row(team, x + row, Nt, xr);
+    fetch_row(team, dxn + row, Nt, dr);
+    if (dres) fetch_row(team, dres + row, Nt, rr);
   };
-  fetch(blockIdx.x);
+  fetch(blockIdx.x * team.count + team.id);
+  if (ragged(N)) settle_row(team, N, wr);
   int parity = 0;
-  for (int t = blockIdx.x; t < T; t += gridDim.x, parity ^= 1) {
-    Raw8<X> rr[CH];
-    float v[CH][8], d[CH][8], s[2] = {0.f, 0.f};
+  for (int t0 = blockIdx.x * team.count; t0 < T; t0 += step, parity ^= 1) {
+    const int t = t0 + team.id;
+    const int Nt = t < T ? N : 0;
+    float v[CH][8], d[CH][8], o[CH][8], s[2] = {0.f, 0.f};
+    if (ragged(N)) {
+      settle_row(team, Nt, xr);
+      settle_row(team, Nt, dr);
+      if (dres) settle_row(team, Nt, rr);
+    }
 #pragma unroll
     for (int c = 0; c < CH; c++) {
       float wv[8];
-      widen8(x_next[c], v[c]);
-      widen8(d_next[c], d[c]);
+      widen8(xr[c], v[c]);
+      widen8(dr[c], d[c]);
       widen8(wr[c], wv);
-      rr[c] = r_next[c];
+      if (dres) {
+        widen8(rr[c], o[c]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) o[c][j] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         s[0] = fmaf(v[c][j], v[c][j], s[0]);
         s[1] = fmaf(v[c][j], d[c][j] * wv[j], s[1]);
       }
     }
-    if (t + (int)gridDim.x < T) fetch(t + gridDim.x);
-    row_sum(s, red[parity]);
+    if (t0 + step < T) fetch(t + step);
+    row_sum(team, s, red[parity]);
     const float r = rms_scale(s[0], inv_n, eps);
     const float m = s[1] * inv_n * r;
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      float o[8], wv[8];
+      float wv[8];
       widen8(wr[c], wv);
-      if (dres) {
-        widen8(rr[c], o);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) o[j] = 0.f;
-      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const float unit = v[c][j] * r;
         dw[c][j] = fmaf(d[c][j], unit, dw[c][j]);
-        o[j] = fmaf(r, fmaf(-unit, m, d[c][j] * wv[j]), o[j]);
+        o[c][j] = fmaf(r, fmaf(-unit, m, d[c][j] * wv[j]), o[c][j]);
       }
-      store8(dx + (size_t)t * N + chunk_at(c), N - chunk_at(c), o);
+      store8(dx + (size_t)t * N, team.at(c), Nt, o[c]);
     }
   }
-  if (part) {
-#pragma unroll
-    for (int c = 0; c < CH; c++) store8(part + (size_t)blockIdx.x * N + chunk_at(c), N - chunk_at(c), dw[c]);
-  }
+  if (part) store_columns(team, dw, cols, N, part);
 }
 
 // Gradients of moe_combine_norm.  KR > 0: the k <= KR slots' rows stay in
 // registers between the combine and the gates' gradients; KR = 0: they are
-// read again.  dx may be dx_out itself.
-//
-// A workgroup's next row is fetched into the registers of this row as soon as
-// these have been used, ahead of this row's stores: loads and stores complete
-// in the order of their issue, so a load behind the stores would wait for them.
-template <typename X, typename P, int CH, int KR>
-__global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
+// read again.  dx may be dx_out itself.  A team's next row is fetched into the
+// registers of this row as soon as these have been used, ahead of this row's
+// stores (as in norm_backward_kernel); so are its gates.
+template <typename X, typename P, int CH, bool PART, int KR>
+__global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
   constexpr int KH = KR > 0 ? KR : 1;
-  __shared__ __align__(16) float red1[2][3][kMaxWaves], red2[2][1][kMaxWaves], redg[2][kMaxTopK][kMaxWaves];
-  const int N = a.N, k = a.k;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  __shared__ __align__(16) float red1[2][kMaxWaveTeams][3][kMaxWaves], red2[2][kMaxWaveTeams][1][kMaxWaves];
+  __shared__ __align__(16) float redg[2][kMaxWaveTeams][kMaxTopK][kMaxWaves];
+  __shared__ __align__(16) float cols[CH == 1 ? kMaxTeam * 8 : 8];
+  const int N = a.N, k = a.k, T = a.T;
+  const Team<PART> team(N);
+  const int step = gridDim.x * team.count;
+  const bool one_wave = PART || team.threads == 64;
   float dw_post[CH][8], dw_next[CH][8];
   Raw8<uint16_t> wp[CH], wn[CH];
-  if (a.w_post) fetch_row(a.w_post, N, wp);
-  if (a.dxn) fetch_row(a.w_next, N, wn);
+  if (a.w_post) fetch_row(team, a.w_post, N, wp);
+  if (a.dxn) fetch_row(team, a.w_next, N, wn);
 #pragma unroll
   for (int c = 0; c < CH; c++)
 #pragma unroll
@@ -306,32 +392,53 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
   Raw8<P> pr[KH][CH];
   Raw8<X> gr[CH], xo[CH];
   Raw8<uint16_t> dn[CH];
+  float gate_next[KH];
   auto fetch_stream = [&](int t) {
     const size_t row = (size_t)t * N;
-    if (a.dx_out) fetch_row(static_cast<const X*>(a.dx_out) + row, N, gr);
+    const int Nt = t < T ? N : 0;
+    if (a.dx_out) fetch_row(team, static_cast<const X*>(a.dx_out) + row, Nt, gr);
     if (a.dxn) {
-      fetch_row(static_cast<const X*>(a.x_out) + row, N, xo);
-      fetch_row(a.dxn + row, N, dn);
+      fetch_row(team, static_cast<const X*>(a.x_out) + row, Nt, xo);
+      fetch_row(team, a.dxn + row, Nt, dn);
     }
   };
   auto fetch_slot = [&](int t, int q, Raw8<P> (&rows)[CH]) {
-    fetch_row(static_cast<const P*>(a.proj) + ((size_t)t * k + q) * N, N, rows);
+    fetch_row(team, static_cast<const P*>(a.proj) + ((size_t)t * k + q) * N, t < T ? N : 0, rows);
   };
+  auto gate_of = [&](int t, int q) { return t >= T ? 0.f : a.gates ? a.gates[(size_t)t * k + q] : 1.f; };
   auto fetch_slots = [&](int t) {
     if constexpr (KR > 0) {
 #pragma unroll
-      for (int q = 0; q < KR; q++)
+      for (int q = 0; q < KR; q++) {
+        gate_next[q] = q < k ? gate_of(t, q) : 0.f;
         if (q < k) fetch_slot(t, q, pr[q]);
+      }
     }
   };
-  fetch_slots(blockIdx.x);
-  fetch_stream(blockIdx.x);
+  fetch_slots(blockIdx.x * team.count + team.id);
+  fetch_stream(blockIdx.x * team.count + team.id);
+  if (ragged(N)) {
+    if (a.w_post) settle_row(team, N, wp);
+    if (a.dxn) settle_row(team, N, wn);
+  }
   int parity = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
-    const bool more = t + (int)gridDim.x < a.T;
+  for (int t0 = blockIdx.x * team.count; t0 < T; t0 += step, parity ^= 1) {
+    const int t = t0 + team.id;
+    const int Nt = t < T ? N : 0;
     const size_t row = (size_t)t * N;
-    const float* gates = a.gates ? a.gates + (size_t)t * k : nullptr;
-    float h[CH][8], grad[CH][8], s[3] = {0.f, 0.f, 0.f};
+    float h[CH][8], grad[CH][8], gate[KH], s[3] = {0.f, 0.f, 0.f};
+    if (ragged(N)) {
+      if constexpr (KR > 0) {
+#pragma unroll
+        for (int q = 0; q < KR; q++)
+          if (q < k) settle_row(team, Nt, pr[q]);
+      }
+      if (a.dx_out) settle_row(team, Nt, gr);
+      if (a.dxn) {
+        settle_row(team, Nt, xo);
+        settle_row(team, Nt, dn);
+      }
+    }
 #pragma unroll
     for (int c = 0; c < CH; c++)
 #pragma unroll
@@ -348,12 +455,15 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
     };
     if constexpr (KR > 0) {
 #pragma unroll
-      for (int q = 0; q < KR; q++)
-        if (q < k) add_slot(gates ? gates[q] : 1.f, pr[q]);
+      for (int q = 0; q < KR; q++) {
+        gate[q] = gate_next[q];
+        if (q < k) add_slot(gate[q], pr[q]);
+      }
     } else {
       for (int q = 0; q < k; q++) {
         fetch_slot(t, q, pr[0]);
-        add_slot(gates ? gates[q] : 1.f, pr[0]);
+        if (ragged(N)) settle_row(team, Nt, pr[0]);
+        add_slot(gate_of(t, q), pr[0]);
       }
     }
     // the gradient at x_out: the stream's own and the next norm's
@@ -379,7 +489,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
 #pragma unroll
       for (int j = 0; j < 8; j++) s[2] = fmaf(h[c][j], h[c][j], s[2]);
     }
-    if (a.dxn || a.w_post) row_sum(s, red1[parity]);
+    if (a.dxn || a.w_post) row_sum(team, s, red1[parity]);
     if (a.dxn) {
       const float r = rms_scale(s[0], a.inv_n, a.eps);
       const float m = s[1] * a.inv_n * r;
@@ -397,11 +507,10 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
         }
       }
     }
-    if (more) fetch_stream(t + gridDim.x);
+    if (t0 + step < T) fetch_stream(t + step);
     if (a.dx) {
 #pragma unroll
-      for (int c = 0; c < CH; c++)
-        store8(static_cast<X*>(a.dx) + row + chunk_at(c), N - chunk_at(c), grad[c]);
+      for (int c = 0; c < CH; c++) store8(static_cast<X*>(a.dx) + row, team.at(c), Nt, grad[c]);
     }
     // through the residual scale and the output norm: grad becomes dh
 #pragma unroll
@@ -423,7 +532,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
           d[0] = fmaf(grad[c][j], unit, d[0]);
         }
       }
-      row_sum(d, red2[parity]);
+      row_sum(team, d, red2[parity]);
       const float m = d[0] * a.inv_n;
 #pragma unroll
       for (int c = 0; c < CH; c++)
@@ -431,7 +540,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
         for (int j = 0; j < 8; j++) grad[c][j] = r * fmaf(-(h[c][j] * r), m, grad[c][j]);
     }
     // the slots: dgate = <dh, proj>, dproj = gate * dh
-    auto dot_slot = [&](int q, const Raw8<P> (&rows)[CH]) {
+    auto dot_slot = [&](int q, float g, const Raw8<P> (&rows)[CH]) {
       float d = 0.f;
 #pragma unroll
       for (int c = 0; c < CH; c++) {
@@ -440,50 +549,60 @@ __global__ __launch_bounds__(kMaxRowThreads) void combine_norm_backward_kernel(c
 #pragma unroll
         for (int j = 0; j < 8; j++) d = fmaf(grad[c][j], p[j], d);
       }
-      d = group_sum<64>(d);
-      if (lane == 0) redg[parity][q][wave] = d;
+      d = g == 0.f ? 0.f : lane_sum(team, d);
+      if (one_wave) {
+        if (team.me == 0 && Nt > 0) a.dgates[(size_t)t * k + q] = d;
+      } else if ((team.me & 63) == 0) {
+        redg[parity][team.id][q][team.me >> 6] = d;
+      }
     };
     if (a.dgates) {
       if constexpr (KR > 0) {
 #pragma unroll
         for (int q = 0; q < KR; q++)
-          if (q < k) dot_slot(q, pr[q]);
+          if (q < k) dot_slot(q, gate[q], pr[q]);
       } else {
         for (int q = 0; q < k; q++) {
           fetch_slot(t, q, pr[0]);
-          dot_slot(q, pr[0]);
+          if (ragged(N)) settle_row(team, Nt, pr[0]);
+          dot_slot(q, gate_of(t, q), pr[0]);
         }
       }
     }
-    if (more) fetch_slots(t + gridDim.x);
+    if (t0 + step < T) fetch_slots(t + step);
     if (a.dproj) {
-      for (int q = 0; q < k; q++) {
-        const float g = gates ? gates[q] : 1.f;
+      auto store_slot = [&](int q, float g) {
         P* out = static_cast<P*>(a.dproj) + (row * k + (size_t)q * N);
 #pragma unroll
         for (int c = 0; c < CH; c++) {
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) o[j] = g * grad[c][j];
-          store8(out + chunk_at(c), N - chunk_at(c), o);
+          if (a.stream)
+            store8<true>(out, team.at(c), Nt, o);
+          else
+            store8(out, team.at(c), Nt, o);
         }
-      }
-    }
-    if (a.dgates) {
-      __syncthreads();
-      if ((int)threadIdx.x < k) {
-        float d = 0.f;
-        for (int w = 0; w < waves; w++) d += redg[parity][threadIdx.x][w];
-        a.dgates[(size_t)t * k + threadIdx.x] = gates[threadIdx.x] == 0.f ? 0.f : d;
-      }
-    }
-  }
+      };
+      if constexpr (KR > 0) {
 #pragma unroll
-  for (int c = 0; c < CH; c++) {
-    const size_t at = (size_t)blockIdx.x * N + chunk_at(c);
-    if (a.part_post) store8(a.part_post + at, N - chunk_at(c), dw_post[c]);
-    if (a.part_next) store8(a.part_next + at, N - chunk_at(c), dw_next[c]);
+        for (int q = 0; q < KR; q++)
+          if (q < k) store_slot(q, gate[q]);
+      } else {
+        for (int q = 0; q < k; q++) store_slot(q, gate_of(t, q));
+      }
+    }
+    if (a.dgates && !one_wave) {
+      __syncthreads();
+      if (team.me < k && Nt > 0) {
+        float d = 0.f;
+        for (int w = 0; w < team.threads >> 6; w++) d += redg[parity][team.id][team.me][w];
+        a.dgates[(size_t)t * k + team.me] = d;
+      }
+    }
   }
+  if (a.part_post) store_columns(team, dw_post, cols, N, a.part_post);
+  if (a.part_next) store_columns(team, dw_next, cols, N, a.part_next);
 }
 
 // out[n] = sum_g part[g][n]: 16 columns (64 bytes of a row) x 64 interleaved
@@ -523,10 +642,23 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const 
   }
 }
 
-// The workgroups of a backward launch, by the rows alone: enough to fill the
-// 256 CUs twice, few enough that their column sums stay small beside the rows.
+// Teams and workgroups of a launch, by the rows' number and length alone.
+// Forward: workgroups of up to 256 threads, a row a team.  Backward: workgroups
+// of up to 512 threads, few enough that their column sums stay small beside the
+// rows, enough to fill the 256 CUs twice.
+constexpr int kForwardThreads = 256;
 constexpr int kBackwardGroups = 512;
-int backward_groups(int T) { return T < kBackwardGroups ? T : kBackwardGroups; }
+dim3 team_block(int N, int threads) {
+  const int team = team_threads(N);
+  const int count = threads / team > 1 ? threads / team : 1;
+  return dim3(team, count);
+}
+int backward_groups(int T, int N) {
+  const int teams = team_block(N, kMaxTeam).y;
+  const int groups = (int)(((long long)T + teams - 1) / teams);
+  return groups < kBackwardGroups ? groups : kBackwardGroups;
+}
+dim3 forward_grid(int T, dim3 block) { return dim3((unsigned)(((long long)T + block.y - 1) / block.y)); }
 
 // the outputs that are wanted (not NULL); G = 0 rows of sums: zeros
 hipError_t launch_column_sums(const float* part0, float* out0, const float* part1, float* out1, int G, int N,
@@ -544,76 +676,89 @@ hipError_t launch_column_sums(const float* part0, float* out0, const float* part
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int T, int N, int weights) {
-  return T > 1 ? (size_t)backward_groups(T) * N * 4 * weights : 0;
+  // a row of column sums for each workgroup, of which there are at most T
+  return T > 1 ? (size_t)(T < kBackwardGroups ? T : kBackwardGroups) * N * 4 * weights : 0;
 }
 
 hipError_t launch_norm(const void* x, bool x_f32, const uint16_t* w, int T, int N, float eps, uint16_t* xn,
                        hipStream_t stream) {
-  const dim3 grid(T), block(row_threads(N));
+  const dim3 block = team_block(N, kForwardThreads), grid = forward_grid(T, block);
   const float inv_n = 1.0f / (float)N;
-  with_row_type(x_f32, N, [&](auto elem, auto ch) {
+  with_row_type(x_f32, N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
-    hipLaunchKernelGGL((norm_kernel<X, decltype(ch)::value>), grid, block, 0, stream, static_cast<const X*>(x), w, N,
-                       inv_n, eps, xn);
+    hipLaunchKernelGGL((norm_kernel<X, decltype(ch)::value, decltype(part)::value>), grid, block, 0, stream,
+                       static_cast<const X*>(x), w, T, N, inv_n, eps, xn);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_norm_backward(const uint16_t* dxn, const void* x, bool x_f32, const uint16_t* w, const void* dres,
                                 int T, int N, float eps, void* dx, float* dw, void* workspace, hipStream_t stream) {
-  const int G = backward_groups(T);
+  const int G = backward_groups(T, N);
   if (G == 0) return launch_column_sums(nullptr, dw, nullptr, nullptr, 0, N, stream);
-  float* part = !dw ? nullptr : G == 1 ? dw : static_cast<float*>(workspace);
-  const dim3 grid(G), block(row_threads(N));
+  float* sums = !dw ? nullptr : G == 1 ? dw : static_cast<float*>(workspace);
   const float inv_n = 1.0f / (float)N;
-  with_row_type(x_f32, N, [&](auto elem, auto ch) {
+  with_row_type(x_f32, N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
-    hipLaunchKernelGGL((norm_backward_kernel<X, decltype(ch)::value>), grid, block, 0, stream, dxn,
-                       static_cast<const X*>(x), w, static_cast<const X*>(dres), T, N, inv_n, eps,
-                       static_cast<X*>(dx), part);
+    hipLaunchKernelGGL((norm_backward_kernel<X, decltype(ch)::value, decltype(part)::value>), dim3(G),
+                       team_block(N, kMaxTeam), 0, stream, dxn, static_cast<const X*>(x), w,
+                       static_cast<const X*>(dres), T, N, inv_n, eps, static_cast<X*>(dx), sums);
   });
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || G == 1 || !dw) return e;
-  return launch_column_sums(part, dw, nullptr, nullptr, G, N, stream);
+  if (e != hipSuccess || G == 1) return e;
+  return launch_column_sums(sums, dw, nullptr, nullptr, G, N, stream);
 }
 
-hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, int T, hipStream_t stream) {
-  const dim3 grid(T), block(row_threads(a.N));
+// Whether the experts' outputs alone pass the 256 MB cache in front of the HBM:
+// then what is not read again at once (x_out, dproj) is stored non-temporally.
+// 8192 x 4 x 2880: 95 -> 90 us and 205 -> 200 us; xn and dx are read by the next
+// launch and stay ordinary (a router behind a norm of 16384 rows takes 35 us
+// after ordinary stores, 41 us after non-temporal ones).
+bool streams(int T, int k, int N, bool proj_f32) {
+  return (size_t)T * k * N * (proj_f32 ? 4 : 2) > ((size_t)256 << 20);
+}
+
+hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, hipStream_t stream) {
+  a.stream = streams(a.T, a.k, a.N, proj_f32);
   a.inv_n = 1.0f / (float)a.N;
-  with_row_type(x_f32, a.N, [&](auto elem, auto ch) {
+  const dim3 block = team_block(a.N, kForwardThreads), grid = forward_grid(a.T, block);
+  with_row_type(x_f32, a.N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
     if (proj_f32)
-      hipLaunchKernelGGL((combine_norm_kernel<X, float, decltype(ch)::value>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((combine_norm_kernel<X, float, decltype(ch)::value, decltype(part)::value>), grid, block, 0,
+                         stream, a);
     else
-      hipLaunchKernelGGL((combine_norm_kernel<X, uint16_t, decltype(ch)::value>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((combine_norm_kernel<X, uint16_t, decltype(ch)::value, decltype(part)::value>), grid, block,
+                         0, stream, a);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_combine_norm_backward(CombineNormBackwardArgs a, bool x_f32, bool proj_f32, float* dw_post,
                                         float* dw_next, void* workspace, hipStream_t stream) {
-  const int G = backward_groups(a.T);
+  const int G = backward_groups(a.T, a.N);
   if (G == 0) return launch_column_sums(nullptr, dw_post, nullptr, dw_next, 0, a.N, stream);
-  const size_t part = (size_t)G * a.N;
+  a.stream = streams(a.T, a.k, a.N, proj_f32);
   float* ws = static_cast<float*>(workspace);
   a.part_post = !dw_post ? nullptr : G == 1 ? dw_post : ws;
-  a.part_next = !dw_next ? nullptr : G == 1 ? dw_next : ws + part;
+  a.part_next = !dw_next ? nullptr : G == 1 ? dw_next : ws + (size_t)G * a.N;
   a.inv_n = 1.0f / (float)a.N;
-  const dim3 grid(G), block(row_threads(a.N));
-  with_row_type(x_f32, a.N, [&](auto elem, auto ch) {
+  const dim3 grid(G), block = team_block(a.N, kMaxTeam);
+  with_row_type(x_f32, a.N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
     constexpr int CH = decltype(ch)::value;
+    constexpr bool PART = decltype(part)::value;
     // the slots' rows held in registers: at most 64 values a thread
     constexpr int KR = CH == 1 ? 8 : CH == 2 ? 4 : 0;
     constexpr int KS = CH == 1 ? 4 : CH == 2 ? 2 : 0;
     auto with_proj = [&](auto pelem) {
       using P = decltype(pelem);
       if (a.k <= KS)
-        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, KS>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, KS>), grid, block, 0, stream, a);
       else if (a.k <= KR)
-        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, KR>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, KR>), grid, block, 0, stream, a);
       else
-        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, 0>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, 0>), grid, block, 0, stream, a);
     };
     if (proj_f32)
       with_proj(float{});

@@ -434,7 +434,7 @@ bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 bool aligned_elem(const void* p, int dtype) { return aligned_to(p, dtype == MXFP4_DTYPE_F32 ? 4 : 2); }
 
 int check_norm_sizes(int T, int k, int N, float eps) {
-  if (T < 0) return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be >= 0", T);
+  if (T < 0 || T > MOE_MAX_TOKENS) return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be in [0, %d]", T, MOE_MAX_TOKENS);
   if (N < 1 || N > MOE_NORM_MAX_N) return fail(MXFP4_ERR_INVALID_ARG, "N = %d must be in [1, %d]", N, MOE_NORM_MAX_N);
   if (k < 1 || k > MXFP4_MAX_TOPK) return fail(MXFP4_ERR_INVALID_ARG, "k = %d must be in [1, %d]", k, MXFP4_MAX_TOPK);
   if ((long long)T * k > 0x7fffffffLL) return fail(MXFP4_ERR_INVALID_ARG, "T * k overflows int32");
@@ -451,8 +451,8 @@ int check_workspace(const void* workspace, size_t given, size_t need) {
 }
 
 int check_balance_sizes(int T, int E, int k, int S) {
-  if (T < 0 || T > MOE_BALANCE_MAX_T)
-    return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be in [0, %d]", T, MOE_BALANCE_MAX_T);
+  if (T < 0 || T > MOE_MAX_TOKENS)
+    return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be in [0, %d]", T, MOE_MAX_TOKENS);
   if (E < 1 || E > MXFP4_MAX_EXPERTS) return fail(MXFP4_ERR_INVALID_ARG, "E = %d must be in [1, %d]", E, MXFP4_MAX_EXPERTS);
   if (k < 1 || k > E || k > MXFP4_MAX_TOPK)
     return fail(MXFP4_ERR_INVALID_ARG, "k = %d must be in [1, min(E = %d, %d)]", k, E, MXFP4_MAX_TOPK);
@@ -479,7 +479,7 @@ int moe_norm(const void* x, int x_dtype, const uint16_t* w, int T, int N, float 
 }
 
 size_t moe_norm_backward_workspace_size(int T, int N) {
-  if (T < 0 || N < 1 || N > MOE_NORM_MAX_N) return (size_t)-1;
+  if (T < 0 || T > MOE_MAX_TOKENS || N < 1 || N > MOE_NORM_MAX_N) return (size_t)-1;
   return mxfp4::norm_backward_workspace_bytes(T, N, 1);
 }
 
@@ -521,15 +521,15 @@ int moe_combine_norm(const void* proj, int proj_dtype, const float* gates, int T
   if ((st = check_device()) != MXFP4_OK) return st;
   mxfp4::CombineNormArgs a = {};
   a.proj = proj, a.gates = gates, a.w_post = w_post, a.x = x, a.x_out = x_out, a.w_next = w_next, a.xn = xn;
-  a.k = k, a.N = N, a.scale = scale, a.eps = eps;
-  hipError_t e = mxfp4::launch_combine_norm(a, x_dtype == MXFP4_DTYPE_F32, proj_dtype == MXFP4_DTYPE_F32, T,
+  a.T = T, a.k = k, a.N = N, a.scale = scale, a.eps = eps;
+  hipError_t e = mxfp4::launch_combine_norm(a, x_dtype == MXFP4_DTYPE_F32, proj_dtype == MXFP4_DTYPE_F32,
                                             static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "combine_norm launch");
   return MXFP4_OK;
 }
 
 size_t moe_combine_norm_backward_workspace_size(int T, int N) {
-  if (T < 0 || N < 1 || N > MOE_NORM_MAX_N) return (size_t)-1;
+  if (T < 0 || T > MOE_MAX_TOKENS || N < 1 || N > MOE_NORM_MAX_N) return (size_t)-1;
   return mxfp4::norm_backward_workspace_bytes(T, N, 2);
 }
 
@@ -573,7 +573,7 @@ int moe_combine_norm_backward(const void* dx_out, const uint16_t* dxn, const voi
 }
 
 size_t moe_balance_workspace_size(int T, int E, int S) {
-  if (T < 0 || T > MOE_BALANCE_MAX_T || E < 1 || E > MXFP4_MAX_EXPERTS || S < 1 || (long long)S * E > 0x7fffffffLL)
+  if (T < 0 || T > MOE_MAX_TOKENS || E < 1 || E > MXFP4_MAX_EXPERTS || S < 1 || (long long)S * E > 0x7fffffffLL)
     return (size_t)-1;
   return mxfp4::balance_workspace_bytes(T, E, S);
 }

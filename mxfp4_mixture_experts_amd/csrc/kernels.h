@@ -96,11 +96,12 @@ struct CombineNormArgs {
   void* x_out;
   const uint16_t* w_next;  // [N], with xn
   uint16_t* xn;            // [T, N], or NULL: no input norm of the next block
-  int k, N;
+  int T, k, N;
   float scale, eps;
-  float inv_n;  // set by the launcher
+  float inv_n;  // these set by the launcher
+  bool stream;  // x_out stored non-temporally
 };
-hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, int T, hipStream_t stream);
+hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, hipStream_t stream);
 
 struct CombineNormBackwardArgs {
   const void* dx_out;   // [T, N], or NULL: 0
@@ -115,7 +116,8 @@ struct CombineNormBackwardArgs {
   float* dgates;
   int T, k, N;
   float scale, eps;
-  float inv_n;       // these three set by the launcher
+  float inv_n;       // these set by the launcher
+  bool stream;       // dproj stored non-temporally
   float* part_post;  // [groups, N] column sums of the weights' gradients
   float* part_next;
 };

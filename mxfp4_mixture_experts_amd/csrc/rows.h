@@ -49,29 +49,54 @@ __device__ __forceinline__ void fetch8_full(const float* p, Raw8<float>& r) {
   r.a = *reinterpret_cast<const f32x4_a4*>(p);
   r.b = *reinterpret_cast<const f32x4_a4*>(p + 4);
 }
-// the first `valid` of the eight elements at p; 0 in the others
-__device__ __forceinline__ void fetch8_part(const uint16_t* p, int valid, Raw8<uint16_t>& r) {
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const uint32_t lo = 2 * i < valid ? p[2 * i] : 0u, hi = 2 * i + 1 < valid ? p[2 * i + 1] : 0u;
-    r.d[i] = lo | (hi << 16);
+// r moved down by n elements (0 <= n < 8), zeros behind
+__device__ __forceinline__ void shift_down(Raw8<uint16_t>& r, int n) {
+  if (n & 4) r.d = u32x4_t{r.d[2], r.d[3], 0u, 0u};
+  if (n & 2) r.d = u32x4_t{r.d[1], r.d[2], r.d[3], 0u};
+  if (n & 1) {
+    r.d[0] = __builtin_amdgcn_alignbit(r.d[1], r.d[0], 16);
+    r.d[1] = __builtin_amdgcn_alignbit(r.d[2], r.d[1], 16);
+    r.d[2] = __builtin_amdgcn_alignbit(r.d[3], r.d[2], 16);
+    r.d[3] >>= 16;
   }
 }
-__device__ __forceinline__ void fetch8_part(const float* p, int valid, Raw8<float>& r) {
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    r.a[i] = i < valid ? p[i] : 0.f;
-    r.b[i] = 4 + i < valid ? p[4 + i] : 0.f;
-  }
+__device__ __forceinline__ void shift_down(Raw8<float>& r, int n) {
+  if (n & 4) r.a = r.b, r.b = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (n & 2) r.a = f32x4_t{r.a[2], r.a[3], r.b[0], r.b[1]}, r.b = f32x4_t{r.b[2], r.b[3], 0.f, 0.f};
+  if (n & 1) r.a = f32x4_t{r.a[1], r.a[2], r.a[3], r.b[0]}, r.b = f32x4_t{r.b[1], r.b[2], r.b[3], 0.f};
 }
-template <typename E>
-__device__ __forceinline__ void fetch8(const E* p, int valid, Raw8<E>& r) {
-  if (valid >= 8)
-    fetch8_full(p, r);
-  else if (valid > 0)
-    fetch8_part(p, valid, r);
+__device__ __forceinline__ void set8(Raw8<uint16_t>& r, int i, uint16_t v) {
+  r.d[i >> 1] |= (uint32_t)v << (16 * (i & 1));
+}
+__device__ __forceinline__ void set8(Raw8<float>& r, int i, float v) {
+  if (i < 4)
+    r.a[i] = v;
   else
-    r = Raw8<E>{};
+    r.b[i - 4] = v;
+}
+
+// Elements i .. i + 7 of a row of N (0 where i >= N).  A row's last, partial
+// chunk is fetched as the row's last eight elements, so it is the same single
+// load; settle8 moves it into place.  The two are apart because the move has to
+// wait for the load.  tiny: the row has fewer than eight elements, read one by
+// one; a launch-wide value, so that the choice is a scalar branch (as a lane's
+// own choice it makes each wide load wait for the element loads).
+template <typename E>
+__device__ __forceinline__ void fetch8(const E* row, int i, int N, bool tiny, Raw8<E>& r) {
+  r = Raw8<E>{};
+  if (tiny) {
+#pragma unroll
+    for (int j = 0; j < 7; j++)
+      if (i == 0 && j < N) set8(r, j, row[j]);
+  } else if (i < N) {
+    fetch8_full(row + min(i, N - 8), r);
+  }
+}
+// whether a row of N has a partial last chunk that settle8 has to move
+__device__ __forceinline__ bool ragged(int N) { return N > 8 && (N & 7) != 0; }
+template <typename E>
+__device__ __forceinline__ void settle8(int i, int N, Raw8<E>& r) {
+  if (i < N && i + 8 > N) shift_down(r, i + 8 - N);
 }
 
 __device__ __forceinline__ void widen8(const Raw8<uint16_t>& r, float (&v)[8]) {
@@ -86,28 +111,40 @@ __device__ __forceinline__ void widen8(const Raw8<float>& r, float (&v)[8]) {
   for (int i = 0; i < 4; i++) v[i] = r.a[i], v[4 + i] = r.b[i];
 }
 
+// STREAM: marked non-temporal
+template <bool STREAM = false>
 __device__ __forceinline__ void store8_full(uint16_t* p, const float (&v)[8]) {
-  u32x4_a2 d;
+  u32x4_t d;
 #pragma unroll
   for (int i = 0; i < 4; i++) d[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  *reinterpret_cast<u32x4_a2*>(p) = d;
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(d, reinterpret_cast<u32x4_a2*>(p));
+  else
+    *reinterpret_cast<u32x4_a2*>(p) = d;
 }
+template <bool STREAM = false>
 __device__ __forceinline__ void store8_full(float* p, const float (&v)[8]) {
-  f32x4_a4 a, b;
+  f32x4_t a, b;
 #pragma unroll
   for (int i = 0; i < 4; i++) a[i] = v[i], b[i] = v[4 + i];
-  *reinterpret_cast<f32x4_a4*>(p) = a;
-  *reinterpret_cast<f32x4_a4*>(p + 4) = b;
+  if constexpr (STREAM) {
+    __builtin_nontemporal_store(a, reinterpret_cast<f32x4_a4*>(p));
+    __builtin_nontemporal_store(b, reinterpret_cast<f32x4_a4*>(p + 4));
+  } else {
+    *reinterpret_cast<f32x4_a4*>(p) = a;
+    *reinterpret_cast<f32x4_a4*>(p + 4) = b;
+  }
 }
 
-template <typename E>
-__device__ __forceinline__ void store8(E* p, int valid, const float (&v)[8]) {
-  if (valid >= 8) {
-    store8_full(p, v);
-  } else if (valid > 0) {
+// elements i .. i + 7 of a row of N, those that it has
+template <bool STREAM = false, typename E>
+__device__ __forceinline__ void store8(E* row, int i, int N, const float (&v)[8]) {
+  if (i + 8 <= N) {
+    store8_full<STREAM>(row + i, v);
+  } else if (i < N) {
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-      if (i < valid) from_f32(v[i], p + i);
+    for (int j = 0; j < 7; j++)
+      if (i + j < N) from_f32(v[j], row + i + j);
   }
 }
 
@@ -139,6 +176,18 @@ __device__ __forceinline__ float group_reduce(float v, Op op) {
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+// the same for a group size known at the call only (uniform, at most 32)
+__device__ __forceinline__ float group_sum_up_to_32(float v, int L) {
+  if (L >= 2) v += dpp<0xB1>(v);
+  if (L >= 4) v += dpp<0x4E>(v);
+  if (L >= 8) v += dpp<0x141>(v);
+  if (L >= 16) v += dpp<0x140>(v);
+  if (L >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return v;
 }
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
