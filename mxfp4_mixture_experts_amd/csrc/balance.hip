@@ -24,7 +24,8 @@
 //
 // Layout: a token belongs to a group of L lanes (a power of two), each holding
 // eight neighbouring experts (one 16-byte load), so 64 / L tokens run in a wave
-// and a token's maximum and sum take log2(L) lane exchanges.
+// and a token's maximum and sums take log2(L) register moves.  A group fetches
+// its next token's logits and slots before it works on this one's.
 
 #include <type_traits>
 
@@ -34,7 +35,6 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -47,9 +47,7 @@ __device__ __forceinline__ bool group_any(bool p) {
 }
 
 // a lane's eight logits (from expert e0); -inf behind the last expert
-__device__ __forceinline__ void load_logits(const uint16_t* row, int e0, int E, float (&v)[8]) {
-  Raw8<uint16_t> r;
-  fetch8(row, e0, E, E < 8, r);
+__device__ __forceinline__ void settle_logits(Raw8<uint16_t> r, int e0, int E, float (&v)[8]) {
   if (ragged(E)) settle8(e0, E, r);
   widen8(r, v);
   if (e0 + 8 > E) {
@@ -58,26 +56,29 @@ __device__ __forceinline__ void load_logits(const uint16_t* row, int e0, int E, 
   }
 }
 
-// the softmax of a group's logits: v becomes the probabilities, z the
-// log-sum-exp.  False where no logit is above -inf (or one is a NaN).
+// The exponentials of a group's logits against their maximum, in place, and the
+// maximum m.  One rounding each: exp2(l log2 e - m log2 e), whose common second
+// term cancels in the probabilities; a maximum so low that it would pass fp32's
+// range there is taken off first.
 template <int L>
-__device__ __forceinline__ bool group_softmax(float (&v)[8], float& z) {
-  float m = v[0];
+__device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
+  m = v[0];
 #pragma unroll
   for (int j = 1; j < 8; j++) m = fmaxf(m, v[j]);
   m = group_max<L>(m);
-  float s = 0.f;
+  float base = m;
+  if (m < -1e38f) {
 #pragma unroll
-  for (int j = 0; j < 8; j++) {
-    v[j] = __builtin_amdgcn_exp2f((v[j] - m) * kLog2e);
-    s += v[j];
+    for (int j = 0; j < 8; j++) v[j] -= m;
+    base = 0.f;
   }
-  s = group_sum<L>(s);
-  const float r = 1.0f / s;
+  base *= -kLog2e;
 #pragma unroll
-  for (int j = 0; j < 8; j++) v[j] *= r;
-  z = fmaf(__builtin_amdgcn_logf(s), kLn2, m);
-  return m > -INFINITY;
+  for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f(fmaf(v[j], kLog2e, base));
+}
+// the log-sum-exp from the maximum and the sum of the exponentials
+__device__ __forceinline__ float log_sum(float m, float sum) {
+  return fmaf(__builtin_amdgcn_logf(sum), kLn2, m);
 }
 
 __device__ __forceinline__ int clamped(int v, int T) { return min(max(v, 0), T); }
@@ -97,38 +98,46 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int t) {
 
 // Workspace of a balance call: a workgroup's chunk of tokens is cut at the
 // sequences' borders into pieces; piece (chunk c, sequence s) has the slot
-// c + s (distinct, since both only rise along the tokens).
+// c + s (distinct, since both only rise along the tokens).  Chunks of 64 tokens
+// fill the chip from 16384 tokens on; beyond 32768 they grow, so that there are
+// never more than 512 to add up.
+constexpr int kSumCols = 64;  // experts per workgroup of the second launch
 struct BalanceLayout {
-  int chunk, chunks, slots;
+  int chunk, chunks, slots, blocks;
   size_t p, c, zn, part, total;  // byte offsets
 };
-__host__ __device__ inline BalanceLayout balance_layout(int T, int E, int S) {
+BalanceLayout balance_layout(int T, int E, int S) {
   BalanceLayout b;
-  const int per = (T + 1023) / 1024;
+  const int per = (T + 511) / 512;
   b.chunk = per > 64 ? per : 64;
   b.chunks = T > 0 ? (T + b.chunk - 1) / b.chunk : 0;
   b.slots = b.chunks + S;
+  b.blocks = (E + kSumCols - 1) / kSumCols;
   const size_t cell = (size_t)b.slots * E * 4;
-  b.p = 0;
+  b.zn = 0;
+  b.p = b.zn + (size_t)b.slots * 8;
   b.c = b.p + cell;
-  b.zn = b.c + cell;
-  b.part = b.zn + (size_t)b.slots * 8;
-  b.total = b.part + (size_t)S * ((E + 15) / 16) * 4 + (size_t)S * 8;
+  b.part = b.c + cell;
+  b.total = b.part + (size_t)S * b.blocks * 4 + (size_t)S * 4;
   return b;
 }
 
+// The threads of a piece's workgroup: more where a wave holds few tokens.
 template <int L>
-__global__ __launch_bounds__(kThreads) void balance_pieces_kernel(const uint16_t* __restrict__ logits,
-                                                                  const int32_t* __restrict__ ids, int T, int E, int k,
-                                                                  const int32_t* __restrict__ seq, int S, int chunk,
-                                                                  float* __restrict__ part_p,
-                                                                  int32_t* __restrict__ part_c,
-                                                                  float2* __restrict__ part_zn) {
+constexpr int kPieceThreads = L >= 16 ? 512 : 256;
+
+template <int L>
+__global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
+    const uint16_t* __restrict__ logits, const int32_t* __restrict__ ids, int T, int E, int k,
+    const int32_t* __restrict__ seq, int S, int chunk, float* __restrict__ part_p, int32_t* __restrict__ part_c,
+    float2* __restrict__ part_zn) {
+  constexpr int kThreads = kPieceThreads<L>;
   constexpr int kGroups = kThreads / L;
+  constexpr int kWaves = kThreads / 64;
   __shared__ int hist[L * 8];
-  __shared__ float red[kThreads / 64][L * 8];
-  __shared__ float redz[kThreads / 64];
-  __shared__ int redn[kThreads / 64];
+  __shared__ float red[kWaves][L * 8];
+  __shared__ float redz[kWaves];
+  __shared__ int redn[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int j = threadIdx.x % L, group = threadIdx.x / L;
   const int e0 = j * 8;
@@ -144,20 +153,35 @@ __global__ __launch_bounds__(kThreads) void balance_pieces_kernel(const uint16_t
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     float z2 = 0.f;
     int n = 0;
+    Raw8<uint16_t> next;
+    int id_next = -1;
+    auto fetch = [&](int t) {
+      fetch8(logits + (size_t)t * E, e0, E, E < 8, next);
+      id_next = j < k ? ids[(size_t)t * k + j] : -1;
+    };
+    if (a + group < b) fetch(a + group);
     for (int t = a + group; t < b; t += kGroups) {
-      float v[8], z;
-      load_logits(logits + (size_t)t * E, e0, E, v);
-      bool valid = false;
-      for (int q = j; q < k; q += L) valid |= (unsigned)ids[(size_t)t * k + q] < (unsigned)E;
+      float v[8], m;
+      settle_logits(next, e0, E, v);
+      const int id = id_next;
+      if (t + kGroups < b) fetch(t + kGroups);
+      bool valid = (unsigned)id < (unsigned)E;
+      for (int q = j + L; q < k; q += L) valid |= (unsigned)ids[(size_t)t * k + q] < (unsigned)E;
       const bool some = group_any<L>(valid);
-      const bool live = group_softmax<L>(v, z) && some;
-      if (live) {
-        for (int q = j; q < k; q += L) {
-          const int id = ids[(size_t)t * k + q];
-          if ((unsigned)id < (unsigned)E) atomicAdd(&hist[id], 1);
-        }
+      group_exp<L>(v, m);
+      float sum = v[0];
 #pragma unroll
-        for (int i = 0; i < 8; i++) acc[i] += v[i];
+      for (int i = 1; i < 8; i++) sum += v[i];
+      sum = group_sum<L>(sum);
+      if (some && m > -INFINITY) {
+        for (int q = j; q < k; q += L) {
+          const int at = q == j ? id : ids[(size_t)t * k + q];
+          if ((unsigned)at < (unsigned)E) atomicAdd(&hist[at], 1);
+        }
+        const float r = __builtin_amdgcn_rcpf(sum);
+        const float z = log_sum(m, sum);
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] = fmaf(v[i], r, acc[i]);
         z2 = fmaf(z, z, z2);
         n++;
       }
@@ -180,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void balance_pieces_kernel(const uint16_t
     for (int e = threadIdx.x; e < E; e += kThreads) {
       float v = red[0][e];
 #pragma unroll
-      for (int w = 1; w < kThreads / 64; w++) v += red[w][e];
+      for (int w = 1; w < kWaves; w++) v += red[w][e];
       part_p[slot * E + e] = v;
       part_c[slot * E + e] = hist[e];
     }
@@ -188,90 +212,115 @@ __global__ __launch_bounds__(kThreads) void balance_pieces_kernel(const uint16_t
       float zz = redz[0];
       int nn = redn[0];
 #pragma unroll
-      for (int w = 1; w < kThreads / 64; w++) zz += redz[w], nn += redn[w];
+      for (int w = 1; w < kWaves; w++) zz += redz[w], nn += redn[w];
       part_zn[slot] = make_float2(zz, __int_as_float(nn));
     }
     __syncthreads();
   }
 }
 
-// One sequence's pieces: 16 experts x 64 piece groups per workgroup.
+// a sequence's share of the balance loss, from sum_e counts p and its n tokens
+__device__ __forceinline__ float sequence_loss(float cp, int n, int E, int k) {
+  return cp * ((float)E / (float)k) / ((float)n * (float)n);
+}
+
+// One sequence's pieces: 64 experts x 16 piece groups per workgroup, the pieces
+// of a group in order (four loads under way), then the groups in order.  The
+// only workgroup of a launch writes the losses too.
 constexpr int kSumThreads = 1024;
-constexpr int kSumCols = 16;
+constexpr int kSumDepth = 4;
 __global__ __launch_bounds__(kSumThreads) void balance_sequences_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c, const float2* __restrict__ part_zn, int T,
-    int E, const int32_t* __restrict__ seq, int chunk, int32_t* __restrict__ counts, int32_t* __restrict__ tokens,
-    float* __restrict__ part, float* __restrict__ seq_z) {
+    int E, int k, const int32_t* __restrict__ seq, int S, int chunk, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens, float* __restrict__ losses, float* __restrict__ part, float* __restrict__ seq_z) {
   constexpr int kRows = kSumThreads / kSumCols;
-  __shared__ float redp[kRows][kSumCols + 1];
-  __shared__ int redc[kRows][kSumCols + 1];
+  __shared__ float redp[kRows][kSumCols];
+  __shared__ int redc[kRows][kSumCols];
+  __shared__ float cp_all;
   const int s = blockIdx.x;
-  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;
+  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;  // a wave is one row
   const int e = blockIdx.y * kSumCols + col;
   const int a = seq ? clamped(seq[s], T) : 0, b = seq ? clamped(seq[s + 1], T) : T;
-  float p = 0.f;
-  int c = 0;
   const int first = b > a ? a / chunk : 0, last = b > a ? (b - 1) / chunk : -1;
+  float p = 0.f, z = 0.f;
+  int c = 0, n = 0;
   if (e < E) {
-    for (int i = first + row; i <= last; i += kRows) {
-      const size_t slot = (size_t)i + s;
-      p += part_p[slot * E + e];
-      c += part_c[slot * E + e];
+    for (int i = first + row; i <= last; i += kRows * kSumDepth) {
+      float pv[kSumDepth];
+      int cv[kSumDepth];
+#pragma unroll
+      for (int u = 0; u < kSumDepth; u++) {
+        const size_t slot = (size_t)min(i + u * kRows, last) + s;
+        pv[u] = part_p[slot * E + e];
+        cv[u] = part_c[slot * E + e];
+      }
+#pragma unroll
+      for (int u = 0; u < kSumDepth; u++) {
+        const bool in = i + u * kRows <= last;
+        p += in ? pv[u] : 0.f;
+        c += in ? cv[u] : 0;
+      }
     }
   }
-  redp[row][col] = p;
-  redc[row][col] = c;
-  __syncthreads();
-  if (threadIdx.x < 64) {  // wave 0: columns, then the sum of c * p over them
-    float cp = 0.f;
-    if (threadIdx.x < kSumCols && e < E) {
-      p = 0.f;
-      c = 0;
-      for (int i = 0; i < kRows; i++) p += redp[i][col], c += redc[i][col];
-      counts[(size_t)s * E + e] = c;
-      cp = (float)c * p;
-    }
-    cp = wave_sum(cp);
-    if (threadIdx.x == 0) part[(size_t)s * gridDim.y + blockIdx.y] = cp;
-  } else if (blockIdx.y == 0 && threadIdx.x < 128) {  // wave 1: tokens and z
-    float z = 0.f;
-    int n = 0;
-    for (int i = first + (int)threadIdx.x - 64; i <= last; i += 64) {
+  if (row == 1) {  // wave 1 adds the tokens and z^2 beside
+    for (int i = first + col; i <= last; i += 64) {
       const float2 zn = part_zn[(size_t)i + s];
       z += zn.x;
       n += __float_as_int(zn.y);
     }
-    z = wave_sum(z);
+    z = group_sum<64>(z);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
-    if (threadIdx.x == 64) {
-      seq_z[s] = z;
-      tokens[s] = n;
+  }
+  redp[row][col] = p;
+  redc[row][col] = c;
+  __syncthreads();
+  if (row == 0) {
+#pragma unroll
+    for (int i = 1; i < kRows; i++) p += redp[i][col], c += redc[i][col];
+    if (e < E) counts[(size_t)s * E + e] = c;
+    const float cp = group_sum<64>((float)c * p);
+    if (col == 0) {
+      part[(size_t)s * gridDim.y + blockIdx.y] = cp;
+      cp_all = cp;
+    }
+  }
+  const bool alone = gridDim.x == 1 && gridDim.y == 1;
+  if (alone) __syncthreads();
+  if (row == 1 && col == 0 && blockIdx.y == 0) {
+    seq_z[s] = z;
+    tokens[s] = n;
+    if (alone) {
+      tokens[1] = n;
+      tokens[2] = n > 0;
+      losses[0] = n > 0 ? sequence_loss(cp_all, n, E, k) : 0.f;
+      losses[1] = n > 0 ? z / (float)n : 0.f;
     }
   }
 }
 
-__global__ __launch_bounds__(kThreads) void balance_losses_kernel(const float* __restrict__ part,
-                                                                  const float* __restrict__ seq_z, int E, int k, int S,
-                                                                  int blocks, int32_t* __restrict__ tokens,
-                                                                  float* __restrict__ losses) {
-  __shared__ float redb[kThreads / 64], redz[kThreads / 64];
-  __shared__ int redn[kThreads / 64], redu[kThreads / 64];
+// The losses of several sequences or blocks of experts.
+constexpr int kLossThreads = 512;
+__global__ __launch_bounds__(kLossThreads) void balance_losses_kernel(const float* __restrict__ part,
+                                                                      const float* __restrict__ seq_z, int E, int k,
+                                                                      int S, int blocks, int32_t* __restrict__ tokens,
+                                                                      float* __restrict__ losses) {
+  constexpr int kWaves = kLossThreads / 64;
+  __shared__ float redb[kWaves], redz[kWaves];
+  __shared__ int redn[kWaves], redu[kWaves];
   float loss = 0.f, z = 0.f;
   int n = 0, used = 0;
-  for (int s = threadIdx.x; s < S; s += kThreads) {
+  for (long long i = threadIdx.x; i < (long long)S * blocks; i += kLossThreads) {
+    const int s = (int)(i / blocks);
     const int ns = tokens[s];
-    if (ns > 0) {
-      float cp = 0.f;
-      for (int i = 0; i < blocks; i++) cp += part[(size_t)s * blocks + i];
-      loss += cp * ((float)E / (float)k) / ((float)ns * (float)ns);
-      z += seq_z[s];
-      n += ns;
-      used++;
-    }
+    if (ns > 0) loss += sequence_loss(part[i], ns, E, k);
   }
-  loss = wave_sum(loss);
-  z = wave_sum(z);
+  for (int s = threadIdx.x; s < S; s += kLossThreads) {
+    const int ns = tokens[s];
+    if (ns > 0) z += seq_z[s], n += ns, used++;
+  }
+  loss = group_sum<64>(loss);
+  z = group_sum<64>(z);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64), used += __shfl_xor(used, o, 64);
   if ((threadIdx.x & 63) == 0) {
@@ -281,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void balance_losses_kernel(const float* _
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int w = 1; w < kThreads / 64; w++) loss += redb[w], z += redz[w], n += redn[w], used += redu[w];
+    for (int w = 1; w < kWaves; w++) loss += redb[w], z += redz[w], n += redn[w], used += redu[w];
     tokens[S] = n;
     tokens[S + 1] = used;
     losses[0] = used > 0 ? loss / (float)used : 0.f;
@@ -289,18 +338,48 @@ __global__ __launch_bounds__(kThreads) void balance_losses_kernel(const float* _
   }
 }
 
+constexpr int kRouteThreads = 256;
+// tokens of a workgroup: each group has one at least
+template <int L>
+constexpr int kRouteChunk = kRouteThreads / L > 64 ? kRouteThreads / L : 64;
+
 // dlogits.  LOSSES: the balance and z losses' part (else the gates' alone, and
 // logits, seq, counts and tokens are not read).
+//
+// The slots' values meet their experts' lanes through a wave's own LDS row: one
+// write and one read a token, where comparing every slot with every lane's eight
+// experts takes 3 x 8 k vector instructions.  A token's slots normally hold
+// distinct experts; the lowest slot of a repeated one goes first, the others in
+// further rounds, so the order of their sum is fixed.
 template <int L, typename O, bool LOSSES>
-__global__ __launch_bounds__(kThreads) void route_backward_kernel(
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
     const uint16_t* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ gates,
     const float* __restrict__ dgates, int T, int E, int k, const int32_t* __restrict__ seq, int S,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens, const float* __restrict__ dlosses,
-    int chunk, O* __restrict__ dlogits) {
-  constexpr int kGroups = kThreads / L;
+    O* __restrict__ dlogits) {
+  constexpr int kGroups = kRouteThreads / L;
+  constexpr int kNone = 0x7fffffff;
+  __shared__ __align__(16) float slot_value[kRouteThreads * 8];
+  __shared__ __align__(16) int slot_owner[kRouteThreads * 8];
   const int j = threadIdx.x % L, group = threadIdx.x / L;
   const int e0 = j * 8;
-  const int c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
+  float* value = slot_value + group * (L * 8);  // a group's experts; other groups never touch them
+  int* owner = slot_owner + group * (L * 8);
+#pragma unroll
+  for (int i = 0; i < 8; i++) value[e0 + i] = 0.f, owner[e0 + i] = kNone;
+  const int c0 = blockIdx.x * kRouteChunk<L>, c1 = min(c0 + kRouteChunk<L>, T);
+  Raw8<uint16_t> l_next;
+  int id_next = -1;
+  float g_next = 0.f, dg_next = 0.f;
+  auto fetch = [&](int t) {
+    if constexpr (LOSSES) fetch8(logits + (size_t)t * E, e0, E, E < 8, l_next);
+    if (j < k) {
+      const size_t r = (size_t)t * k + j;
+      id_next = ids[r];
+      if (dgates) g_next = gates[r], dg_next = dgates[r];
+    }
+  };
+  if (c0 + group < c1) fetch(c0 + group);
   float da = 0.f, b = 0.f;
   int s = 0, s_end = T, s_have = -1;
   float c[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -313,75 +392,100 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     }
   }
   for (int t = c0 + group; t < c1; t += kGroups) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, z = 0.f;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int id = id_next;
+    const bool ok = j < k && (unsigned)id < (unsigned)E;
+    const float g = ok ? g_next : 0.f;
+    const float dg = g != 0.f ? dg_next : 0.f;
     bool live = true;
     if constexpr (LOSSES) {
-      load_logits(logits + (size_t)t * E, e0, E, v);
+      settle_logits(l_next, e0, E, v);
       while (seq && t >= s_end && s < S) {
         s++;
         s_end = s < S ? seq[s + 1] : T;
       }
       live = s >= 0 && s < S;
     }
-    // the slots: lane j takes the slots j, j + L, ...
-    bool valid = false;
-    float qd = 0.f;
-    for (int q = j; q < k; q += L) {
+    if (t + kGroups < c1) fetch(t + kGroups);
+    // lane j takes the slots j, j + L, ...; one each where k <= L
+    bool valid = ok;
+    float qd = g * dg;
+    for (int q = j + L; q < k; q += L) {
       const size_t r = (size_t)t * k + q;
-      const bool ok = (unsigned)ids[r] < (unsigned)E;
-      valid |= ok;
+      const bool okq = (unsigned)ids[r] < (unsigned)E;
+      valid |= okq;
       if (dgates) {
-        const float g = ok ? gates[r] : 0.f;
-        if (g != 0.f) qd = fmaf(g, dgates[r], qd);
+        const float gq = okq ? gates[r] : 0.f;
+        if (gq != 0.f) qd = fmaf(gq, dgates[r], qd);
       }
     }
     live = group_any<L>(valid) && live;
     if constexpr (LOSSES) {
-      live = group_softmax<L>(v, z) && live;
-      float pc = 0.f;
-      if (live) {
-        if (s != s_have) {
-          float sum = 0.f;
+      float m;
+      group_exp<L>(v, m);
+      live = m > -INFINITY && live;
+      if (live && s != s_have) {
+        float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            c[i] = e0 + i < E ? (float)counts[(size_t)s * E + e0 + i] : 0.f;
-            sum += c[i];
-          }
-          sum = group_sum<L>(sum);
-          const float n = (float)max(tokens[s], 1);
-          const float a = da / (n * n), mean = sum / (float)E;
-#pragma unroll
-          for (int i = 0; i < 8; i++) c[i] = (c[i] - mean) * a;
-          s_have = s;
+        for (int i = 0; i < 8; i++) {
+          c[i] = e0 + i < E ? (float)counts[(size_t)s * E + e0 + i] : 0.f;
+          sum += c[i];
         }
+        sum = group_sum<L>(sum);
+        const float n = (float)max(tokens[s], 1);
+        const float a = da / (n * n), mean = sum / (float)E;
 #pragma unroll
-        for (int i = 0; i < 8; i++) pc = fmaf(v[i], c[i], pc);
+        for (int i = 0; i < 8; i++) c[i] = (c[i] - mean) * a;
+        s_have = s;
       }
-      pc = group_sum<L>(pc);
-      const float bz = b == 0.f ? 0.f : b * z;
+      float sum = 0.f, pc = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = live ? v[i] * (c[i] - pc + bz) : 0.f;
+      for (int i = 0; i < 8; i++) {
+        sum += v[i];
+        pc = fmaf(v[i], c[i], pc);
+      }
+      sum = group_sum<L>(sum);
+      pc = group_sum<L>(pc);
+      const float r = __builtin_amdgcn_rcpf(sum);
+      const float bz = (b == 0.f ? 0.f : b * log_sum(m, sum)) - pc * r;
+#pragma unroll
+      for (int i = 0; i < 8; i++) v[i] = live ? v[i] * r * (c[i] + bz) : 0.f;
     }
     if (dgates) {
       qd = group_sum<L>(qd);
       for (int q0 = 0; q0 < k; q0 += L) {
-        int id = -1;
-        float d = 0.f;
-        if (q0 + j < k) {
-          const size_t r = (size_t)t * k + q0 + j;
-          id = ids[r];
-          const float g = (unsigned)id < (unsigned)E ? gates[r] : 0.f;
-          if (g != 0.f) d = g * (dgates[r] - qd);
+        int at = id;
+        float d = g != 0.f ? g * (dg - qd) : 0.f;
+        bool pending = ok && live;
+        if (q0 > 0) {
+          pending = false;
+          if (q0 + j < k) {
+            const size_t r = (size_t)t * k + q0 + j;
+            at = ids[r];
+            pending = live && (unsigned)at < (unsigned)E;
+            const float gq = pending ? gates[r] : 0.f;
+            d = gq != 0.f ? gq * (dgates[r] - qd) : 0.f;
+          }
         }
-        const int m = min(L, k - q0);
-        for (int q = 0; q < m; q++) {
-          const int src = ((threadIdx.x & 63) & ~(L - 1)) + q;
-          const int at = __shfl(id, src, 64) - e0;
-          const float dq = __shfl(d, src, 64);
-#pragma unroll
-          for (int i = 0; i < 8; i++) v[i] += at == i && live ? dq : 0.f;
+        while (__ballot(pending)) {
+          if (pending) atomicMin(&owner[at], q0 + j);
+          __builtin_amdgcn_wave_barrier();  // a wave's LDS accesses complete in order
+          if (pending && owner[at] == q0 + j) {
+            value[at] += d;  // one lane per address
+            owner[at] = kNone;
+            pending = false;
+          }
+          __builtin_amdgcn_wave_barrier();
         }
       }
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(value + e0);
+      const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(value + e0 + 4);
+      __builtin_amdgcn_wave_barrier();
+      *reinterpret_cast<f32x4_t*>(value + e0) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      *reinterpret_cast<f32x4_t*>(value + e0 + 4) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[i] += lo[i], v[4 + i] += hi[i];
     }
     store8(dlogits + (size_t)t * E, e0, E, v);
   }
@@ -418,24 +522,24 @@ hipError_t launch_balance(const uint16_t* logits, const int32_t* ids, int T, int
   float* part_p = reinterpret_cast<float*>(ws + b.p);
   int32_t* part_c = reinterpret_cast<int32_t*>(ws + b.c);
   float2* part_zn = reinterpret_cast<float2*>(ws + b.zn);
-  const int blocks = (E + kSumCols - 1) / kSumCols;
   float* part = reinterpret_cast<float*>(ws + b.part);
-  float* seq_z = part + (size_t)S * blocks;
+  float* seq_z = part + (size_t)S * b.blocks;
   hipError_t e = hipSuccess;
   if (b.chunks > 0) {
     with_lanes(E, [&](auto lanes) {
-      hipLaunchKernelGGL((balance_pieces_kernel<decltype(lanes)::value>), dim3(b.chunks), dim3(kThreads), 0, stream,
-                         logits, ids, T, E, k, seq, S, b.chunk, part_p, part_c, part_zn);
+      constexpr int L = decltype(lanes)::value;
+      hipLaunchKernelGGL((balance_pieces_kernel<L>), dim3(b.chunks), dim3(kPieceThreads<L>), 0, stream, logits, ids, T,
+                         E, k, seq, S, b.chunk, part_p, part_c, part_zn);
     });
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(balance_sequences_kernel, dim3(S, blocks), dim3(kSumThreads), 0, stream, part_p, part_c, part_zn,
-                     T, E, seq, b.chunk, counts, tokens, part, seq_z);
+  hipLaunchKernelGGL(balance_sequences_kernel, dim3(S, b.blocks), dim3(kSumThreads), 0, stream, part_p, part_c,
+                     part_zn, T, E, k, seq, S, b.chunk, counts, tokens, losses, part, seq_z);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_losses_kernel, dim3(1), dim3(kThreads), 0, stream, part, seq_z, E, k, S, blocks, tokens,
-                     losses);
+  if (e != hipSuccess || (S == 1 && b.blocks == 1)) return e;
+  hipLaunchKernelGGL(balance_losses_kernel, dim3(1), dim3(kLossThreads), 0, stream, part, seq_z, E, k, S, b.blocks,
+                     tokens, losses);
   return hipGetLastError();
 }
 
@@ -443,17 +547,17 @@ hipError_t launch_route_backward(const uint16_t* logits, const int32_t* ids, con
                                  int T, int E, int k, const int32_t* seq, int S, const int32_t* counts,
                                  const int32_t* tokens, const float* dlosses, void* dlogits, bool dlogits_f32,
                                  hipStream_t stream) {
-  const int chunk = 64, chunks = (T + chunk - 1) / chunk;
   with_lanes(E, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
+    const dim3 grid((T + kRouteChunk<L> - 1) / kRouteChunk<L>);
     auto with_out = [&](auto elem) {
       using O = decltype(elem);
       if (dlosses)
-        hipLaunchKernelGGL((route_backward_kernel<L, O, true>), dim3(chunks), dim3(kThreads), 0, stream, logits, ids,
-                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, chunk, static_cast<O*>(dlogits));
+        hipLaunchKernelGGL((route_backward_kernel<L, O, true>), grid, dim3(kRouteThreads), 0, stream, logits, ids,
+                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, static_cast<O*>(dlogits));
       else
-        hipLaunchKernelGGL((route_backward_kernel<L, O, false>), dim3(chunks), dim3(kThreads), 0, stream, logits, ids,
-                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, chunk, static_cast<O*>(dlogits));
+        hipLaunchKernelGGL((route_backward_kernel<L, O, false>), grid, dim3(kRouteThreads), 0, stream, logits, ids,
+                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, static_cast<O*>(dlogits));
     };
     if (dlogits_f32)
       with_out(float{});
