@@ -46,37 +46,69 @@ __device__ __forceinline__ bool group_any(bool p) {
   return ((m >> base) & ((1ull << (L & 63)) - 1)) != 0;
 }
 
-// a lane's eight logits (from expert e0); -inf behind the last expert
+// A lane's eight logits (from expert e0) of a token's row; -inf behind the last
+// expert.  Every lane loads eight that the row has, whatever part of them is its
+// own: settle_logits sorts that out, where E is not 8 L.
+template <int L>
+__device__ __forceinline__ void fetch_logits(const uint16_t* row, int e0, int E, Raw8<uint16_t>& r) {
+  if (L == 1 && E < 8)
+    fetch8(row, e0, E, true, r);
+  else
+    fetch8_full(row + min(e0, E - 8), r);
+}
+template <int L>
 __device__ __forceinline__ void settle_logits(Raw8<uint16_t> r, int e0, int E, float (&v)[8]) {
-  if (ragged(E)) settle8(e0, E, r);
+  if (E != 8 * L && E > 8) settle8(e0, E, r);
   widen8(r, v);
-  if (e0 + 8 > E) {
+  if (E != 8 * L) {
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] = e0 + i < E ? v[i] : -INFINITY;
   }
 }
 
-// The exponentials of a group's logits against their maximum, in place, and the
-// maximum m.  One rounding each: exp2(l log2 e - m log2 e), whose common second
-// term cancels in the probabilities; a maximum so low that it would pass fp32's
-// range there is taken off first.
+// a lane's eight counts of a sequence's row; 0 behind the last expert
+template <int L>
+__device__ __forceinline__ void load_counts(const int32_t* row, int e0, int E, int (&c)[8]) {
+  const float* words = reinterpret_cast<const float*>(row);  // moved as they are
+  Raw8<float> r = {};
+  if (L == 1 && E < 8) {
+    fetch8(words, e0, E, true, r);
+  } else if (e0 < E) {
+    fetch8_full(words + min(e0, E - 8), r);
+    settle8(e0, E, r);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) c[i] = __float_as_int(r.a[i]), c[4 + i] = __float_as_int(r.b[i]);
+}
+
+// The exponentials of a group's logits against a common m, in place; m is -inf
+// where no logit is above that.  While every token of the wave has its largest
+// logit in [-64, 64], m is 0 and no maximum over the lanes is needed: no
+// exponential passes fp32's range, and a sum of them is at least e^-64.  (Router
+// logits lie there; of the 125 instructions a token of 512 experts takes, 20 are
+// saved.)  Otherwise m is the row's maximum, taken off first where it is so low
+// that its product with log2 e would pass fp32's range.  One rounding before
+// the exponential either way; that of m log2 e is common to the row and cancels
+// in the probabilities.
 template <int L>
 __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
-  m = v[0];
+  float top = v[0];
 #pragma unroll
-  for (int j = 1; j < 8; j++) m = fmaxf(m, v[j]);
-  m = group_max<L>(m);
-  float base = m;
-  if (m < -1e38f) {
+  for (int j = 1; j < 8; j++) top = fmaxf(top, v[j]);
+  const bool near = group_any<L>(top >= -64.f) && top <= 64.f;
+  if (__ballot(!near) == 0) {
+    m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] -= m;
-    base = 0.f;
+    for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f(v[j] * kLog2e);
+    return;
   }
-  base *= -kLog2e;
+  m = group_max<L>(top);
+  const float off = m < -1e38f ? m : 0.f;
+  const float base = (off - m) * kLog2e;
 #pragma unroll
-  for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f(fmaf(v[j], kLog2e, base));
+  for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f(fmaf(v[j] - off, kLog2e, base));
 }
-// the log-sum-exp from the maximum and the sum of the exponentials
+// the log-sum-exp from m and the sum of the exponentials
 __device__ __forceinline__ float log_sum(float m, float sum) {
   return fmaf(__builtin_amdgcn_logf(sum), kLn2, m);
 }
@@ -98,9 +130,11 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int t) {
 
 // Workspace of a balance call: a workgroup's chunk of tokens is cut at the
 // sequences' borders into pieces; piece (chunk c, sequence s) has the slot
-// c + s (distinct, since both only rise along the tokens).  Chunks of 64 tokens
-// fill the chip from 16384 tokens on; beyond 32768 they grow, so that there are
-// never more than 512 to add up.
+// c + s (distinct, since both only rise along the tokens).  A workgroup takes
+// its pieces one after another, about 0.7 us each, so chunks are no longer than
+// the mean sequence, from 64 tokens (which fill the chip from 16384 tokens on)
+// down to 4; beyond 32768 tokens they grow, so that there are never more than
+// 512 to add up.
 constexpr int kSumCols = 64;  // experts per workgroup of the second launch
 struct BalanceLayout {
   int chunk, chunks, slots, blocks;
@@ -108,8 +142,9 @@ struct BalanceLayout {
 };
 BalanceLayout balance_layout(int T, int E, int S) {
   BalanceLayout b;
-  const int per = (T + 511) / 512;
-  b.chunk = per > 64 ? per : 64;
+  const int per = (T + 511) / 512, mean = T / S;
+  b.chunk = mean > 64 ? 64 : mean > 4 ? mean : 4;
+  if (b.chunk < per) b.chunk = per;
   b.chunks = T > 0 ? (T + b.chunk - 1) / b.chunk : 0;
   b.slots = b.chunks + S;
   b.blocks = (E + kSumCols - 1) / kSumCols;
@@ -124,7 +159,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
 
 // The threads of a piece's workgroup: more where a wave holds few tokens.
 template <int L>
-constexpr int kPieceThreads = L >= 16 ? 512 : 256;
+constexpr int kPieceThreads = L >= 16 ? 1024 : 256;
 
 template <int L>
 __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
@@ -156,17 +191,18 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
     Raw8<uint16_t> next;
     int id_next = -1;
     auto fetch = [&](int t) {
-      fetch8(logits + (size_t)t * E, e0, E, E < 8, next);
+      fetch_logits<L>(logits + (size_t)t * E, e0, E, next);
       id_next = j < k ? ids[(size_t)t * k + j] : -1;
     };
     if (a + group < b) fetch(a + group);
     for (int t = a + group; t < b; t += kGroups) {
       float v[8], m;
-      settle_logits(next, e0, E, v);
+      settle_logits<L>(next, e0, E, v);
       const int id = id_next;
       if (t + kGroups < b) fetch(t + kGroups);
       bool valid = (unsigned)id < (unsigned)E;
-      for (int q = j + L; q < k; q += L) valid |= (unsigned)ids[(size_t)t * k + q] < (unsigned)E;
+      if constexpr (L < kMaxTopK)
+        for (int q = j + L; q < k; q += L) valid |= (unsigned)ids[(size_t)t * k + q] < (unsigned)E;
       const bool some = group_any<L>(valid);
       group_exp<L>(v, m);
       float sum = v[0];
@@ -174,10 +210,12 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
       for (int i = 1; i < 8; i++) sum += v[i];
       sum = group_sum<L>(sum);
       if (some && m > -INFINITY) {
-        for (int q = j; q < k; q += L) {
-          const int at = q == j ? id : ids[(size_t)t * k + q];
-          if ((unsigned)at < (unsigned)E) atomicAdd(&hist[at], 1);
-        }
+        if ((unsigned)id < (unsigned)E) atomicAdd(&hist[id], 1);
+        if constexpr (L < kMaxTopK)
+          for (int q = j + L; q < k; q += L) {
+            const int at = ids[(size_t)t * k + q];
+            if ((unsigned)at < (unsigned)E) atomicAdd(&hist[at], 1);
+          }
         const float r = __builtin_amdgcn_rcpf(sum);
         const float z = log_sum(m, sum);
 #pragma unroll
@@ -339,9 +377,10 @@ __global__ __launch_bounds__(kLossThreads) void balance_losses_kernel(const floa
 }
 
 constexpr int kRouteThreads = 256;
-// tokens of a workgroup: each group has one at least
+// tokens of a workgroup: each group has one at least, and at most eight (65536
+// tokens of 512 experts then fill every wave slot of the chip)
 template <int L>
-constexpr int kRouteChunk = kRouteThreads / L > 64 ? kRouteThreads / L : 64;
+constexpr int kRouteChunk = L >= 32 ? 8 * kRouteThreads / L : kRouteThreads / L > 64 ? kRouteThreads / L : 64;
 
 // dlogits.  LOSSES: the balance and z losses' part (else the gates' alone, and
 // logits, seq, counts and tokens are not read).
@@ -352,7 +391,7 @@ constexpr int kRouteChunk = kRouteThreads / L > 64 ? kRouteThreads / L : 64;
 // distinct experts; the lowest slot of a repeated one goes first, the others in
 // further rounds, so the order of their sum is fixed.
 template <int L, typename O, bool LOSSES>
-__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
+__global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward_kernel(
     const uint16_t* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ gates,
     const float* __restrict__ dgates, int T, int E, int k, const int32_t* __restrict__ seq, int S,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens, const float* __restrict__ dlosses,
@@ -372,7 +411,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
   int id_next = -1;
   float g_next = 0.f, dg_next = 0.f;
   auto fetch = [&](int t) {
-    if constexpr (LOSSES) fetch8(logits + (size_t)t * E, e0, E, E < 8, l_next);
+    if constexpr (LOSSES) fetch_logits<L>(logits + (size_t)t * E, e0, E, l_next);
     if (j < k) {
       const size_t r = (size_t)t * k + j;
       id_next = ids[r];
@@ -399,7 +438,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
     const float dg = g != 0.f ? dg_next : 0.f;
     bool live = true;
     if constexpr (LOSSES) {
-      settle_logits(l_next, e0, E, v);
+      settle_logits<L>(l_next, e0, E, v);
       while (seq && t >= s_end && s < S) {
         s++;
         s_end = s < S ? seq[s + 1] : T;
@@ -410,13 +449,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
     // lane j takes the slots j, j + L, ...; one each where k <= L
     bool valid = ok;
     float qd = g * dg;
-    for (int q = j + L; q < k; q += L) {
-      const size_t r = (size_t)t * k + q;
-      const bool okq = (unsigned)ids[r] < (unsigned)E;
-      valid |= okq;
-      if (dgates) {
-        const float gq = okq ? gates[r] : 0.f;
-        if (gq != 0.f) qd = fmaf(gq, dgates[r], qd);
+    if constexpr (L < kMaxTopK) {
+      for (int q = j + L; q < k; q += L) {
+        const size_t r = (size_t)t * k + q;
+        const bool okq = (unsigned)ids[r] < (unsigned)E;
+        valid |= okq;
+        if (dgates) {
+          const float gq = okq ? gates[r] : 0.f;
+          if (gq != 0.f) qd = fmaf(gq, dgates[r], qd);
+        }
       }
     }
     live = group_any<L>(valid) && live;
@@ -426,9 +467,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
       live = m > -INFINITY && live;
       if (live && s != s_have) {
         float sum = 0.f;
+        int cv[8];
+        load_counts<L>(counts + (size_t)s * E, e0, E, cv);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          c[i] = e0 + i < E ? (float)counts[(size_t)s * E + e0 + i] : 0.f;
+          c[i] = (float)cv[i];
           sum += c[i];
         }
         sum = group_sum<L>(sum);
@@ -447,13 +490,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
       sum = group_sum<L>(sum);
       pc = group_sum<L>(pc);
       const float r = __builtin_amdgcn_rcpf(sum);
-      const float bz = (b == 0.f ? 0.f : b * log_sum(m, sum)) - pc * r;
+      const float bz = ((b == 0.f ? 0.f : b * log_sum(m, sum)) - pc * r) * r;
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = live ? v[i] * r * (c[i] + bz) : 0.f;
+      for (int i = 0; i < 8; i++) v[i] = live ? v[i] * fmaf(c[i], r, bz) : 0.f;
     }
     if (dgates) {
       qd = group_sum<L>(qd);
-      for (int q0 = 0; q0 < k; q0 += L) {
+      for (int q0 = 0; q0 < (L < kMaxTopK ? k : 1); q0 += L) {
         int at = id;
         float d = g != 0.f ? g * (dg - qd) : 0.f;
         bool pending = ok && live;

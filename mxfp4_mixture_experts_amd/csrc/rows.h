@@ -154,28 +154,51 @@ __device__ __forceinline__ void store8(E* row, int i, int N, const float (&v)[8]
 // them): about 8 cycles a step, where a lane exchange through the LDS takes over
 // a hundred.  Lanes of other groups may be inactive.
 template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
 }
-template <int L, typename Op>
-__device__ __forceinline__ float group_reduce(float v, Op op) {
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(dpp<CTRL>(__float_as_int(v)));
+}
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits(int v) { return (uint32_t)v; }
+__device__ __forceinline__ void from_bits(uint32_t b, float& v) { v = __uint_as_float(b); }
+__device__ __forceinline__ void from_bits(uint32_t b, int& v) { v = (int)b; }
+
+template <int L, typename V, typename Op>
+__device__ __forceinline__ V group_reduce(V v, Op op) {
   if constexpr (L >= 2) v = op(v, dpp<0xB1>(v));    // quad_perm [1, 0, 3, 2]
   if constexpr (L >= 4) v = op(v, dpp<0x4E>(v));    // quad_perm [2, 3, 0, 1]
   if constexpr (L >= 8) v = op(v, dpp<0x141>(v));   // the other quad of eight lanes (mirrored)
   if constexpr (L >= 16) v = op(v, dpp<0x140>(v));  // the other half of sixteen (mirrored)
+  V x, y;
   if constexpr (L >= 32) {
-    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto p = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+    from_bits(p[0], x);
+    from_bits(p[1], y);
+    v = op(x, y);
   }
   if constexpr (L >= 64) {
-    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto p = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+    from_bits(p[0], x);
+    from_bits(p[1], y);
+    v = op(x, y);
   }
   return v;
 }
+template <int L, typename V>
+__device__ __forceinline__ V group_sum(V v) {
+  return group_reduce<L>(v, [](V a, V b) { return a + b; });
+}
+// The maximum, compared as integers in the floats' order: an integer maximum
+// takes its moved operand in the same instruction, a float one first quiets it.
 template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-  return group_reduce<L>(v, [](float a, float b) { return a + b; });
+__device__ __forceinline__ float group_max(float v) {
+  int key = __float_as_int(v);
+  key ^= (key >> 31) & 0x7fffffff;
+  key = group_reduce<L>(key, [](int a, int b) { return a > b ? a : b; });
+  return __int_as_float(key ^ ((key >> 31) & 0x7fffffff));
 }
 // the same for a group size known at the call only (uniform, at most 32)
 __device__ __forceinline__ float group_sum_up_to_32(float v, int L) {
@@ -188,10 +211,6 @@ __device__ __forceinline__ float group_sum_up_to_32(float v, int L) {
     v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   }
   return v;
-}
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-  return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 }  // namespace mxfp4
