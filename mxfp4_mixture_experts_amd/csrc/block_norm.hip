@@ -35,8 +35,9 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kMaxTeam = 512;
-constexpr int kMaxWaves = kMaxTeam / 64;  // of a team
-constexpr int kMaxWaveTeams = 4;          // teams of several waves in a workgroup (of 128 threads each)
+constexpr int kMaxWaves = kMaxTeam / 64;          // of a team
+constexpr int kMaxThreads = 1024;                 // of a workgroup, where a thread has one chunk and few registers
+constexpr int kMaxWaveTeams = kMaxThreads / 128;  // teams of several waves in a workgroup
 
 // chunks of eight per thread, and the threads of a row's team
 int chunks_per_thread(int N) {
@@ -293,11 +294,11 @@ __device__ __forceinline__ void store_columns(const Team<PART>& team, float (&dw
 // complete in the order of their issue, so a load behind the stores would wait
 // for them.
 template <typename X, int CH, bool PART>
-__global__ __launch_bounds__(kMaxTeam) void norm_backward_kernel(const uint16_t* dxn, const X* x, const uint16_t* w,
-                                                                 const X* dres, int T, int N, float inv_n, float eps,
-                                                                 X* dx, float* part) {
+__global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backward_kernel(
+    const uint16_t* dxn, const X* x, const uint16_t* w, const X* dres, int T, int N, float inv_n, float eps, X* dx,
+    float* part) {
   __shared__ __align__(16) float red[2][kMaxWaveTeams][2][kMaxWaves];
-  __shared__ __align__(16) float cols[CH == 1 ? kMaxTeam * 8 : 8];
+  __shared__ __align__(16) float cols[CH == 1 ? kMaxThreads * 8 : 8];
   const Team<PART> team(N);
   const int step = gridDim.x * team.count;
   float dw[CH][8];
@@ -421,8 +422,17 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const C
     if (a.w_post) settle_row(team, N, wp);
     if (a.dxn) settle_row(team, N, wn);
   }
-  int parity = 0;
-  for (int t0 = blockIdx.x * team.count; t0 < T; t0 += step, parity ^= 1) {
+  // a row's gates' gradients, from its waves' sums behind a barrier
+  auto store_dgates = [&](int t, int parity) {
+    if (team.me < k && t < T) {
+      float d = 0.f;
+      for (int w = 0; w < team.threads >> 6; w++) d += redg[parity][team.id][team.me][w];
+      a.dgates[(size_t)t * k + team.me] = d;
+    }
+  };
+  const bool sums = a.dxn || a.w_post, shared_dgates = a.dgates && !one_wave;
+  int parity = 0, t0 = blockIdx.x * team.count;
+  for (; t0 < T; t0 += step, parity ^= 1) {
     const int t = t0 + team.id;
     const int Nt = t < T ? N : 0;
     const size_t row = (size_t)t * N;
@@ -489,7 +499,13 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const C
 #pragma unroll
       for (int j = 0; j < 8; j++) s[2] = fmaf(h[c][j], h[c][j], s[2]);
     }
-    if (a.dxn || a.w_post) row_sum(team, s, red1[parity]);
+    // the first barrier of this row is also the one behind the last row's
+    // dgates
+    if (sums)
+      row_sum(team, s, red1[parity]);
+    else if (shared_dgates)
+      __syncthreads();
+    if (shared_dgates && t0 >= step) store_dgates(t - step, parity ^ 1);
     if (a.dxn) {
       const float r = rms_scale(s[0], a.inv_n, a.eps);
       const float m = s[1] * a.inv_n * r;
@@ -592,14 +608,10 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const C
         for (int q = 0; q < k; q++) store_slot(q, gate_of(t, q));
       }
     }
-    if (a.dgates && !one_wave) {
-      __syncthreads();
-      if (team.me < k && Nt > 0) {
-        float d = 0.f;
-        for (int w = 0; w < team.threads >> 6; w++) d += redg[parity][team.id][team.me][w];
-        a.dgates[(size_t)t * k + team.me] = d;
-      }
-    }
+  }
+  if (shared_dgates) {
+    __syncthreads();
+    store_dgates(t0 - step + team.id, parity ^ 1);
   }
   if (a.part_post) store_columns(team, dw_post, cols, N, a.part_post);
   if (a.part_next) store_columns(team, dw_next, cols, N, a.part_next);
@@ -643,19 +655,25 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const 
 }
 
 // Teams and workgroups of a launch, by the rows' number and length alone.
-// Forward: workgroups of up to 256 threads, a row a team.  Backward: workgroups
-// of up to 512 threads, few enough that their column sums stay small beside the
-// rows, enough to fill the 256 CUs twice.
+// Forward: workgroups of up to 256 threads.  Backward: 256 workgroups, one a CU
+// (their column sums are a small part of the traffic then; with the next row
+// fetched ahead, one row under way on a CU keeps up with two: 8192 x 4 x 2880,
+// block output, 191 us against 193 with 512 workgroups and 197 with 768), then
+// more teams in each.
 constexpr int kForwardThreads = 256;
-constexpr int kBackwardGroups = 512;
-dim3 team_block(int N, int threads) {
+constexpr int kBackwardGroups = 256;
+dim3 forward_block(int N) {
   const int team = team_threads(N);
-  const int count = threads / team > 1 ? threads / team : 1;
-  return dim3(team, count);
+  return dim3(team, kForwardThreads > team ? kForwardThreads / team : 1);
 }
-int backward_groups(int T, int N) {
-  const int teams = team_block(N, kMaxTeam).y;
-  const int groups = (int)(((long long)T + teams - 1) / teams);
+dim3 backward_block(int T, int N, int threads) {
+  const int team = team_threads(N);
+  const int most = threads > team ? threads / team : 1;
+  const int want = (int)(((long long)T + kBackwardGroups - 1) / kBackwardGroups);
+  return dim3(team, want < 1 ? 1 : want < most ? want : most);
+}
+int backward_groups(int T, dim3 block) {
+  const int groups = (int)(((long long)T + block.y - 1) / block.y);
   return groups < kBackwardGroups ? groups : kBackwardGroups;
 }
 dim3 forward_grid(int T, dim3 block) { return dim3((unsigned)(((long long)T + block.y - 1) / block.y)); }
@@ -682,7 +700,7 @@ size_t norm_backward_workspace_bytes(int T, int N, int weights) {
 
 hipError_t launch_norm(const void* x, bool x_f32, const uint16_t* w, int T, int N, float eps, uint16_t* xn,
                        hipStream_t stream) {
-  const dim3 block = team_block(N, kForwardThreads), grid = forward_grid(T, block);
+  const dim3 block = forward_block(N), grid = forward_grid(T, block);
   const float inv_n = 1.0f / (float)N;
   with_row_type(x_f32, N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
@@ -694,15 +712,16 @@ hipError_t launch_norm(const void* x, bool x_f32, const uint16_t* w, int T, int 
 
 hipError_t launch_norm_backward(const uint16_t* dxn, const void* x, bool x_f32, const uint16_t* w, const void* dres,
                                 int T, int N, float eps, void* dx, float* dw, void* workspace, hipStream_t stream) {
-  const int G = backward_groups(T, N);
+  const dim3 block = backward_block(T, N, chunks_per_thread(N) == 1 ? kMaxThreads : kMaxTeam);
+  const int G = backward_groups(T, block);
   if (G == 0) return launch_column_sums(nullptr, dw, nullptr, nullptr, 0, N, stream);
   float* sums = !dw ? nullptr : G == 1 ? dw : static_cast<float*>(workspace);
   const float inv_n = 1.0f / (float)N;
   with_row_type(x_f32, N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
     hipLaunchKernelGGL((norm_backward_kernel<X, decltype(ch)::value, decltype(part)::value>), dim3(G),
-                       team_block(N, kMaxTeam), 0, stream, dxn, static_cast<const X*>(x), w,
-                       static_cast<const X*>(dres), T, N, inv_n, eps, static_cast<X*>(dx), sums);
+                       block, 0, stream, dxn, static_cast<const X*>(x), w, static_cast<const X*>(dres), T, N, inv_n,
+                       eps, static_cast<X*>(dx), sums);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || G == 1) return e;
@@ -721,7 +740,7 @@ bool streams(int T, int k, int N, bool proj_f32) {
 hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, hipStream_t stream) {
   a.stream = streams(a.T, a.k, a.N, proj_f32);
   a.inv_n = 1.0f / (float)a.N;
-  const dim3 block = team_block(a.N, kForwardThreads), grid = forward_grid(a.T, block);
+  const dim3 block = forward_block(a.N), grid = forward_grid(a.T, block);
   with_row_type(x_f32, a.N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
     if (proj_f32)
@@ -736,14 +755,15 @@ hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, hip
 
 hipError_t launch_combine_norm_backward(CombineNormBackwardArgs a, bool x_f32, bool proj_f32, float* dw_post,
                                         float* dw_next, void* workspace, hipStream_t stream) {
-  const int G = backward_groups(a.T, a.N);
+  const dim3 block = backward_block(a.T, a.N, kMaxTeam);
+  const int G = backward_groups(a.T, block);
   if (G == 0) return launch_column_sums(nullptr, dw_post, nullptr, dw_next, 0, a.N, stream);
   a.stream = streams(a.T, a.k, a.N, proj_f32);
   float* ws = static_cast<float*>(workspace);
   a.part_post = !dw_post ? nullptr : G == 1 ? dw_post : ws;
   a.part_next = !dw_next ? nullptr : G == 1 ? dw_next : ws + (size_t)G * a.N;
   a.inv_n = 1.0f / (float)a.N;
-  const dim3 grid(G), block = team_block(a.N, kMaxTeam);
+  const dim3 grid(G);
   with_row_type(x_f32, a.N, [&](auto elem, auto ch, auto part) {
     using X = decltype(elem);
     constexpr int CH = decltype(ch)::value;
