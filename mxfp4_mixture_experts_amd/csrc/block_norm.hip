@@ -250,10 +250,7 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_kernel(const CombineNor
       h[c][j] = rounded(fmaf(a.scale, h[c][j], xv[j]), x);
       s[0] = fmaf(h[c][j], h[c][j], s[0]);
     }
-    if (a.stream)
-      store8<true>(x_out, team.at(c), Nt, h[c]);
-    else
-      store8(x_out, team.at(c), Nt, h[c]);
+    store8(x_out, team.at(c), Nt, h[c], a.stream);
   }
   if (!a.xn) return;
   row_sum(team, s, red[1]);
@@ -594,10 +591,7 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const C
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) o[j] = g * grad[c][j];
-          if (a.stream)
-            store8<true>(out, team.at(c), Nt, o);
-          else
-            store8(out, team.at(c), Nt, o);
+          store8(out, team.at(c), Nt, o, a.stream);
         }
       };
       if constexpr (KR > 0) {

@@ -20,10 +20,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
-__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ void from_f32(float f, uint16_t* p) { *p = to_bf16(f); }
-__device__ __forceinline__ void from_f32(float f, float* p) { *p = f; }
 // f as the element type stores it
 __device__ __forceinline__ float rounded(float f, const uint16_t*) { return bf16_bits_to_f32(to_bf16(f)); }
 __device__ __forceinline__ float rounded(float f, const float*) { return f; }
@@ -112,7 +108,7 @@ __device__ __forceinline__ void widen8(const Raw8<float>& r, float (&v)[8]) {
 }
 
 // STREAM: marked non-temporal
-template <bool STREAM = false>
+template <bool STREAM>
 __device__ __forceinline__ void store8_full(uint16_t* p, const float (&v)[8]) {
   u32x4_t d;
 #pragma unroll
@@ -122,7 +118,7 @@ __device__ __forceinline__ void store8_full(uint16_t* p, const float (&v)[8]) {
   else
     *reinterpret_cast<u32x4_a2*>(p) = d;
 }
-template <bool STREAM = false>
+template <bool STREAM>
 __device__ __forceinline__ void store8_full(float* p, const float (&v)[8]) {
   f32x4_t a, b;
 #pragma unroll
@@ -136,15 +132,58 @@ __device__ __forceinline__ void store8_full(float* p, const float (&v)[8]) {
   }
 }
 
-// elements i .. i + 7 of a row of N, those that it has
-template <bool STREAM = false, typename E>
-__device__ __forceinline__ void store8(E* row, int i, int N, const float (&v)[8]) {
-  if (i + 8 <= N) {
-    store8_full<STREAM>(row + i, v);
-  } else if (i < N) {
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+
+// the first n (under 8) elements, as pieces of four, two and one
+__device__ __forceinline__ void store8_part(uint16_t* p, int n, const float (&v)[8]) {
+  uint32_t d[4];
 #pragma unroll
-    for (int j = 0; j < 7; j++)
-      if (i + j < N) from_f32(v[j], row + i + j);
+  for (int i = 0; i < 4; i++) d[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  if (n & 4) {
+    *reinterpret_cast<u32x2_a2*>(p) = u32x2_a2{d[0], d[1]};
+    d[0] = d[2], d[1] = d[3];
+    p += 4;
+  }
+  if (n & 2) {
+    *reinterpret_cast<u32_a2*>(p) = d[0];
+    d[0] = d[1];
+    p += 2;
+  }
+  if (n & 1) *p = (uint16_t)d[0];
+}
+__device__ __forceinline__ void store8_part(float* p, int n, const float (&v)[8]) {
+  float d[4] = {v[0], v[1], v[2], v[3]};
+  if (n & 4) {
+    *reinterpret_cast<f32x4_a4*>(p) = f32x4_a4{d[0], d[1], d[2], d[3]};
+    d[0] = v[4], d[1] = v[5], d[2] = v[6];
+    p += 4;
+  }
+  if (n & 2) {
+    *reinterpret_cast<f32x2_a4*>(p) = f32x2_a4{d[0], d[1]};
+    d[0] = d[2];
+    p += 2;
+  }
+  if (n & 1) *p = d[0];
+}
+
+// elements i .. i + 7 of a row of N, those that it has; stream: whole chunks
+// marked non-temporal
+template <typename E>
+__device__ __forceinline__ void store8(E* row, int i, int N, const float (&v)[8], bool stream = false) {
+  if (i + 8 <= N) {
+    if (stream) {
+      // the empty statements keep the two branches' stores from being moved out
+      // of them as one, which drops the mark
+      asm volatile("");
+      store8_full<true>(row + i, v);
+      asm volatile("");
+    } else {
+      store8_full<false>(row + i, v);
+    }
+  } else if (i < N) {
+    store8_part(row + i, N - i, v);
   }
 }
 
