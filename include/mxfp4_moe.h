@@ -68,6 +68,7 @@ typedef enum {
 
 #define MOE_NORM_MAX_N 16384         /* the norms: a row stays in one workgroup's registers */
 #define MOE_MAX_TOKENS (1 << 30)     /* the norms, moe_balance, moe_route_backward */
+#define MOE_MAX_SEQUENCES (1 << 20)  /* moe_balance, moe_route_backward */
 
 /* Element types of the arguments that take one (`const void*` with a *_dtype). */
 #define MXFP4_DTYPE_BF16 0
@@ -576,7 +577,7 @@ size_t moe_balance_workspace_size(int T, int E, int S);
  *   seq_offsets [S + 1] i32, ascending, or NULL (S = 1: all T tokens): sequence s
  *           holds the tokens [seq_offsets[s], seq_offsets[s + 1]).  Sequences may
  *           be empty; tokens before the first and behind the last are padding.
- *           Values outside [0, T] are clamped.  1 <= S, S * E < 2^31.
+ *           Values outside [0, T] are clamped.  1 <= S <= MOE_MAX_SEQUENCES.
  *   A token is counted when it lies in a sequence, has a slot whose id lies in
  *   [0, E), and a logit above -inf; another token's logits (NaN included) reach no
  *   output.  A counted token's logits hold no NaN and no +inf.

@@ -23,7 +23,7 @@ MXFP4_MAX_EXPERTS, MXFP4_MAX_TOPK = 512, 32
 MXFP4_DECODE_MAX_EXPERTS, MXFP4_DECODE_MAX_K, MXFP4_GEMM_MAX_K = 64, 3072, 8192
 MXFP4_NOALLOC_SCRATCH_BYTES = 128 << 20
 MXFP4_DTYPE_BF16, MXFP4_DTYPE_F32 = 0, 1
-MOE_NORM_MAX_N, MOE_MAX_TOKENS = 16384, 1 << 30
+MOE_NORM_MAX_N, MOE_MAX_TOKENS, MOE_MAX_SEQUENCES = 16384, 1 << 30, 1 << 20
 
 #: the C entry points this binding uses (all declared in include/mxfp4_moe.h)
 ENTRY_POINTS = (

@@ -115,17 +115,21 @@ __device__ __forceinline__ float log_sum(float m, float sum) {
 
 __device__ __forceinline__ int clamped(int v, int T) { return min(max(v, 0), T); }
 
-// the last sequence that starts at or before token t (-1: none)
+// The last sequence that starts at or before token t (-1: none).  A whole wave
+// looks for it, 64 starts at a time: one load's latency up to 64 sequences.
+// Whatever seq holds, the result lies in [-1, S).
 __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int t) {
-  int lo = 0, hi = S;  // the first of [0, S) that starts behind t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq[mid] <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+  const int lane = threadIdx.x & 63;
+  int lo = -1, hi = S;  // starts up to lo lie at or before t; those from hi on are not looked at
+  while (hi - lo > 1) {
+    const int stride = (hi - lo - 1 + 63) / 64;
+    const int at = lo + 1 + lane * stride;
+    const int n = __popcll(__ballot(at < hi && seq[min(at, hi - 1)] <= t));
+    if (n == 0) break;
+    lo += 1 + (n - 1) * stride;
+    hi = min(lo + stride, hi);
   }
-  return lo - 1;
+  return lo;
 }
 
 // Workspace of a balance call: a workgroup's chunk of tokens is cut at the
@@ -395,7 +399,7 @@ __global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward
     const uint16_t* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ gates,
     const float* __restrict__ dgates, int T, int E, int k, const int32_t* __restrict__ seq, int S,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens, const float* __restrict__ dlosses,
-    O* __restrict__ dlogits) {
+    int chunk, O* __restrict__ dlogits) {
   constexpr int kGroups = kRouteThreads / L;
   constexpr int kNone = 0x7fffffff;
   __shared__ __align__(16) float slot_value[kRouteThreads * 8];
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward
   int* owner = slot_owner + group * (L * 8);
 #pragma unroll
   for (int i = 0; i < 8; i++) value[e0 + i] = 0.f, owner[e0 + i] = kNone;
-  const int c0 = blockIdx.x * kRouteChunk<L>, c1 = min(c0 + kRouteChunk<L>, T);
+  const int c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
   Raw8<uint16_t> l_next;
   int id_next = -1;
   float g_next = 0.f, dg_next = 0.f;
@@ -592,15 +596,19 @@ hipError_t launch_route_backward(const uint16_t* logits, const int32_t* ids, con
                                  hipStream_t stream) {
   with_lanes(E, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const dim3 grid((T + kRouteChunk<L> - 1) / kRouteChunk<L>);
+    const int least = (T + (1 << 21) - 1) >> 21;  // a grid holds under 2^32 threads
+    const int chunk = kRouteChunk<L> > least ? kRouteChunk<L> : least;
+    const dim3 grid((T + chunk - 1) / chunk);
     auto with_out = [&](auto elem) {
       using O = decltype(elem);
       if (dlosses)
         hipLaunchKernelGGL((route_backward_kernel<L, O, true>), grid, dim3(kRouteThreads), 0, stream, logits, ids,
-                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, static_cast<O*>(dlogits));
+                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, chunk,
+                           static_cast<O*>(dlogits));
       else
         hipLaunchKernelGGL((route_backward_kernel<L, O, false>), grid, dim3(kRouteThreads), 0, stream, logits, ids,
-                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, static_cast<O*>(dlogits));
+                           gates, dgates, T, E, k, seq, S, counts, tokens, dlosses, chunk,
+                           static_cast<O*>(dlogits));
     };
     if (dlogits_f32)
       with_out(float{});

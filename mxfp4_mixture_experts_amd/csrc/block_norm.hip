@@ -172,7 +172,8 @@ __global__ __launch_bounds__(kMaxTeam) void norm_kernel(const X* __restrict__ x,
 }
 
 // The block's output.  x_out may be x itself: each element is read and written
-// by one thread, in this order.
+// by one thread, in this order (what the row's last chunk reads beside its own
+// elements, it drops).
 template <typename X, typename P, int CH, bool PART>
 __global__ __launch_bounds__(kMaxTeam) void combine_norm_kernel(const CombineNormArgs a) {
   constexpr int kSlots = CH == 1 ? 4 : CH == 2 ? 2 : 1;  // slots whose rows are under way together
@@ -670,6 +671,8 @@ int backward_groups(int T, dim3 block) {
   const int groups = (int)(((long long)T + block.y - 1) / block.y);
   return groups < kBackwardGroups ? groups : kBackwardGroups;
 }
+// rows of one forward launch: a grid holds under 2^32 threads
+constexpr int kForwardRows = 1 << 22;
 dim3 forward_grid(int T, dim3 block) { return dim3((unsigned)(((long long)T + block.y - 1) / block.y)); }
 
 // the outputs that are wanted (not NULL); G = 0 rows of sums: zeros
@@ -694,14 +697,20 @@ size_t norm_backward_workspace_bytes(int T, int N, int weights) {
 
 hipError_t launch_norm(const void* x, bool x_f32, const uint16_t* w, int T, int N, float eps, uint16_t* xn,
                        hipStream_t stream) {
-  const dim3 block = forward_block(N), grid = forward_grid(T, block);
+  const dim3 block = forward_block(N);
   const float inv_n = 1.0f / (float)N;
-  with_row_type(x_f32, N, [&](auto elem, auto ch, auto part) {
-    using X = decltype(elem);
-    hipLaunchKernelGGL((norm_kernel<X, decltype(ch)::value, decltype(part)::value>), grid, block, 0, stream,
-                       static_cast<const X*>(x), w, T, N, inv_n, eps, xn);
-  });
-  return hipGetLastError();
+  hipError_t e = hipSuccess;
+  for (int t = 0; t < T && e == hipSuccess; t += kForwardRows) {
+    const int rows = T - t < kForwardRows ? T - t : kForwardRows;
+    const size_t at = (size_t)t * N;
+    with_row_type(x_f32, N, [&](auto elem, auto ch, auto part) {
+      using X = decltype(elem);
+      hipLaunchKernelGGL((norm_kernel<X, decltype(ch)::value, decltype(part)::value>), forward_grid(rows, block),
+                         block, 0, stream, static_cast<const X*>(x) + at, w, rows, N, inv_n, eps, xn + at);
+    });
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 hipError_t launch_norm_backward(const uint16_t* dxn, const void* x, bool x_f32, const uint16_t* w, const void* dres,
@@ -734,17 +743,33 @@ bool streams(int T, int k, int N, bool proj_f32) {
 hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, hipStream_t stream) {
   a.stream = streams(a.T, a.k, a.N, proj_f32);
   a.inv_n = 1.0f / (float)a.N;
-  const dim3 block = forward_block(a.N), grid = forward_grid(a.T, block);
-  with_row_type(x_f32, a.N, [&](auto elem, auto ch, auto part) {
-    using X = decltype(elem);
-    if (proj_f32)
-      hipLaunchKernelGGL((combine_norm_kernel<X, float, decltype(ch)::value, decltype(part)::value>), grid, block, 0,
-                         stream, a);
-    else
-      hipLaunchKernelGGL((combine_norm_kernel<X, uint16_t, decltype(ch)::value, decltype(part)::value>), grid, block,
-                         0, stream, a);
-  });
-  return hipGetLastError();
+  const dim3 block = forward_block(a.N);
+  const int T = a.T;
+  hipError_t e = hipSuccess;
+  for (int t = 0; t < T && e == hipSuccess; t += kForwardRows) {
+    CombineNormArgs r = a;
+    const size_t at = (size_t)t * a.N;
+    r.T = T - t < kForwardRows ? T - t : kForwardRows;
+    if (r.gates) r.gates += (size_t)t * a.k;
+    if (r.xn) r.xn += at;
+    const dim3 grid = forward_grid(r.T, block);
+    with_row_type(x_f32, a.N, [&](auto elem, auto ch, auto part) {
+      using X = decltype(elem);
+      constexpr int CH = decltype(ch)::value;
+      constexpr bool PART = decltype(part)::value;
+      r.x = static_cast<const X*>(a.x) + at;
+      r.x_out = static_cast<X*>(a.x_out) + at;
+      if (proj_f32) {
+        r.proj = static_cast<const float*>(a.proj) + at * a.k;
+        hipLaunchKernelGGL((combine_norm_kernel<X, float, CH, PART>), grid, block, 0, stream, r);
+      } else {
+        r.proj = static_cast<const uint16_t*>(a.proj) + at * a.k;
+        hipLaunchKernelGGL((combine_norm_kernel<X, uint16_t, CH, PART>), grid, block, 0, stream, r);
+      }
+    });
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 hipError_t launch_combine_norm_backward(CombineNormBackwardArgs a, bool x_f32, bool proj_f32, float* dw_post,

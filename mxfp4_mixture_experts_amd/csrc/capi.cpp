@@ -457,8 +457,8 @@ int check_balance_sizes(int T, int E, int k, int S) {
   if (k < 1 || k > E || k > MXFP4_MAX_TOPK)
     return fail(MXFP4_ERR_INVALID_ARG, "k = %d must be in [1, min(E = %d, %d)]", k, E, MXFP4_MAX_TOPK);
   if ((long long)T * k > 0x7fffffffLL) return fail(MXFP4_ERR_INVALID_ARG, "T * k overflows int32");
-  if (S < 1 || (long long)S * E > 0x7fffffffLL)
-    return fail(MXFP4_ERR_INVALID_ARG, "S = %d must be >= 1, with S * E within int32", S);
+  if (S < 1 || S > MOE_MAX_SEQUENCES)
+    return fail(MXFP4_ERR_INVALID_ARG, "S = %d must be in [1, %d]", S, MOE_MAX_SEQUENCES);
   return MXFP4_OK;
 }
 }  // namespace
@@ -573,7 +573,7 @@ int moe_combine_norm_backward(const void* dx_out, const uint16_t* dxn, const voi
 }
 
 size_t moe_balance_workspace_size(int T, int E, int S) {
-  if (T < 0 || T > MOE_MAX_TOKENS || E < 1 || E > MXFP4_MAX_EXPERTS || S < 1 || (long long)S * E > 0x7fffffffLL)
+  if (T < 0 || T > MOE_MAX_TOKENS || E < 1 || E > MXFP4_MAX_EXPERTS || S < 1 || S > MOE_MAX_SEQUENCES)
     return (size_t)-1;
   return mxfp4::balance_workspace_bytes(T, E, S);
 }
