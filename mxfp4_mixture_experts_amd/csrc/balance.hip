@@ -38,6 +38,12 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// the number of a thread's group: the same for a whole wave where L is 64, so
+// that a token's addresses are scalar there
+template <int L>
+__device__ __forceinline__ int group_of_thread() {
+  return L == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / L) : (int)threadIdx.x / L;
+}
 template <int L>
 __device__ __forceinline__ bool group_any(bool p) {
   const uint64_t m = __ballot(p);
@@ -107,6 +113,26 @@ __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
   const float base = (off - m) * kLog2e;
 #pragma unroll
   for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f(fmaf(v[j] - off, kLog2e, base));
+}
+// The sums of three values over a group.  A whole wave adds them together: after
+// each exchange across rows a row holds the partial sums of one of them.
+template <int L>
+__device__ __forceinline__ void group_sum3(float& a, float& b, float& c) {
+  if constexpr (L == 64) {
+    const auto ab = __builtin_amdgcn_permlane32_swap(bits(a), bits(b), false, false);
+    const auto cc = __builtin_amdgcn_permlane32_swap(bits(c), bits(c), false, false);
+    const float x = __uint_as_float(ab[0]) + __uint_as_float(ab[1]);  // a in rows 0, 1; b in rows 2, 3
+    const float y = __uint_as_float(cc[0]) + __uint_as_float(cc[1]);
+    const auto xy = __builtin_amdgcn_permlane16_swap(bits(x), bits(y), false, false);
+    const float rows = group_sum<16>(__uint_as_float(xy[0]) + __uint_as_float(xy[1]));  // a, c, b, c
+    a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rows), 0));
+    b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rows), 32));
+    c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rows), 16));
+  } else {
+    a = group_sum<L>(a);
+    b = group_sum<L>(b);
+    c = group_sum<L>(c);
+  }
 }
 // the log-sum-exp from m and the sum of the exponentials
 __device__ __forceinline__ float log_sum(float m, float sum) {
@@ -178,7 +204,7 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
   __shared__ float redz[kWaves];
   __shared__ int redn[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int j = threadIdx.x % L, group = threadIdx.x / L;
+  const int j = threadIdx.x % L, group = group_of_thread<L>();
   const int e0 = j * 8;
   const int c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
   int s = seq ? max(sequence_of(seq, S, c0), 0) : 0;
@@ -187,11 +213,6 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
     if (a >= c1) break;
     const int b = seq ? min(seq[s + 1], c1) : c1;
     if (b <= a) continue;
-    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
-    __syncthreads();
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float z2 = 0.f;
-    int n = 0;
     Raw8<uint16_t> next;
     int id_next = -1;
     auto fetch = [&](int t) {
@@ -199,6 +220,11 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
       id_next = j < k ? ids[(size_t)t * k + j] : -1;
     };
     if (a + group < b) fetch(a + group);
+    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float z2 = 0.f;
+    int n = 0;
     for (int t = a + group; t < b; t += kGroups) {
       float v[8], m;
       settle_logits<L>(next, e0, E, v);
@@ -404,7 +430,7 @@ __global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward
   constexpr int kNone = 0x7fffffff;
   __shared__ __align__(16) float slot_value[kRouteThreads * 8];
   __shared__ __align__(16) int slot_owner[kRouteThreads * 8];
-  const int j = threadIdx.x % L, group = threadIdx.x / L;
+  const int j = threadIdx.x % L, group = group_of_thread<L>();
   const int e0 = j * 8;
   float* value = slot_value + group * (L * 8);  // a group's experts; other groups never touch them
   int* owner = slot_owner + group * (L * 8);
@@ -491,15 +517,20 @@ __global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward
         sum += v[i];
         pc = fmaf(v[i], c[i], pc);
       }
-      sum = group_sum<L>(sum);
-      pc = group_sum<L>(pc);
+      group_sum3<L>(sum, pc, qd);
       const float r = __builtin_amdgcn_rcpf(sum);
       const float bz = ((b == 0.f ? 0.f : b * log_sum(m, sum)) - pc * r) * r;
+      if (L == 64 ? __ballot(!live) == 0 : true) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[i] = live ? v[i] * fmaf(c[i], r, bz) : 0.f;
+        for (int i = 0; i < 8; i++) v[i] = L == 64 || live ? v[i] * fmaf(c[i], r, bz) : 0.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = 0.f;
+      }
+    } else {
+      qd = group_sum<L>(qd);
     }
     if (dgates) {
-      qd = group_sum<L>(qd);
       for (int q0 = 0; q0 < (L < kMaxTopK ? k : 1); q0 += L) {
         int at = id;
         float d = g != 0.f ? g * (dg - qd) : 0.f;
