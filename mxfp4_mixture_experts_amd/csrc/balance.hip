@@ -91,8 +91,7 @@ __device__ __forceinline__ void load_counts(const int32_t* row, int e0, int E, i
 // where no logit is above that.  While every token of the wave has its largest
 // logit in [-64, 64], m is 0 and no maximum over the lanes is needed: no
 // exponential passes fp32's range, and a sum of them is at least e^-64.  (Router
-// logits lie there; of the 125 instructions a token of 512 experts takes, 20 are
-// saved.)  Otherwise m is the row's maximum, taken off first where it is so low
+// logits lie there: 27.5 -> 25.3 us for the balance of 65536 x 512.)  Otherwise m is the row's maximum, taken off first where it is so low
 // that its product with log2 e would pass fp32's range.  One rounding before
 // the exponential either way; that of m log2 e is common to the row and cancels
 // in the probabilities.
@@ -168,7 +167,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int t) {
 constexpr int kSumCols = 64;  // experts per workgroup of the second launch
 struct BalanceLayout {
   int chunk, chunks, slots, blocks;
-  size_t p, c, zn, part, total;  // byte offsets
+  size_t zn, p, c, part, arrivals, total;  // byte offsets
 };
 BalanceLayout balance_layout(int T, int E, int S) {
   BalanceLayout b;
@@ -183,7 +182,8 @@ BalanceLayout balance_layout(int T, int E, int S) {
   b.p = b.zn + (size_t)b.slots * 8;
   b.c = b.p + cell;
   b.part = b.c + cell;
-  b.total = b.part + (size_t)S * b.blocks * 4 + (size_t)S * 4;
+  b.arrivals = b.part + (size_t)S * b.blocks * 4 + (size_t)S * 4;
+  b.total = b.arrivals + 4;
   return b;
 }
 
@@ -195,7 +195,7 @@ template <int L>
 __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
     const uint16_t* __restrict__ logits, const int32_t* __restrict__ ids, int T, int E, int k,
     const int32_t* __restrict__ seq, int S, int chunk, float* __restrict__ part_p, int32_t* __restrict__ part_c,
-    float2* __restrict__ part_zn) {
+    float2* __restrict__ part_zn, int* __restrict__ arrivals) {
   constexpr int kThreads = kPieceThreads<L>;
   constexpr int kGroups = kThreads / L;
   constexpr int kWaves = kThreads / 64;
@@ -207,6 +207,7 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
   const int j = threadIdx.x % L, group = group_of_thread<L>();
   const int e0 = j * 8;
   const int c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, T);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *arrivals = 0;  // for the second launch
   int s = seq ? max(sequence_of(seq, S, c0), 0) : 0;
   for (; s < S; s++) {
     const int a = seq ? max(seq[s], c0) : c0;
@@ -287,24 +288,36 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
   }
 }
 
-// a sequence's share of the balance loss, from sum_e counts p and its n tokens
-__device__ __forceinline__ float sequence_loss(float cp, int n, int E, int k) {
-  return cp * ((float)E / (float)k) / ((float)n * (float)n);
-}
-
 // One sequence's pieces: 64 experts x 16 piece groups per workgroup, the pieces
-// of a group in order (four loads under way), then the groups in order.  The
-// only workgroup of a launch writes the losses too.
+// of a group in order (four loads under way), then the groups in order.  Each
+// workgroup leaves its share of the losses in the workspace and counts itself
+// in; the last one to do so adds the shares in order and writes the losses, so
+// the sum does not depend on which that is.  The shares go through
+// device-scope stores and loads (sc1: past the XCD's own L2 to the level that
+// all share), and a workgroup counts itself in once its stores are complete
+// (vmcnt); a release and acquire instead write back and drop whole L2s, 4 us for
+// one workgroup and 9 us for 296.
 constexpr int kSumThreads = 1024;
 constexpr int kSumDepth = 4;
+
+template <typename V>
+__device__ __forceinline__ V load_shared(const V* p) {  // written by another workgroup of this launch
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ void store_shared(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 __global__ __launch_bounds__(kSumThreads) void balance_sequences_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c, const float2* __restrict__ part_zn, int T,
-    int E, int k, const int32_t* __restrict__ seq, int S, int chunk, int32_t* __restrict__ counts,
-    int32_t* __restrict__ tokens, float* __restrict__ losses, float* __restrict__ part, float* __restrict__ seq_z) {
+    int E, int k, const int32_t* __restrict__ seq, int S, int chunk, int32_t* __restrict__ counts, int32_t* tokens,
+    float* __restrict__ losses, float* part, float* seq_z, int* arrivals) {
   constexpr int kRows = kSumThreads / kSumCols;
   __shared__ float redp[kRows][kSumCols];
   __shared__ int redc[kRows][kSumCols];
-  __shared__ float cp_all;
+  __shared__ float z_all;
+  __shared__ int n_all, last_all;
   const int s = blockIdx.x;
   const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;  // a wave is one row
   const int e = blockIdx.y * kSumCols + col;
@@ -337,8 +350,8 @@ __global__ __launch_bounds__(kSumThreads) void balance_sequences_kernel(
       n += __float_as_int(zn.y);
     }
     z = group_sum<64>(z);
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+    n = group_sum<64>(n);
+    if (col == 0) z_all = z, n_all = n;
   }
   redp[row][col] = p;
   redc[row][col] = c;
@@ -348,57 +361,54 @@ __global__ __launch_bounds__(kSumThreads) void balance_sequences_kernel(
     for (int i = 1; i < kRows; i++) p += redp[i][col], c += redc[i][col];
     if (e < E) counts[(size_t)s * E + e] = c;
     const float cp = group_sum<64>((float)c * p);
-    if (col == 0) {
-      part[(size_t)s * gridDim.y + blockIdx.y] = cp;
-      cp_all = cp;
-    }
-  }
-  const bool alone = gridDim.x == 1 && gridDim.y == 1;
-  if (alone) __syncthreads();
-  if (row == 1 && col == 0 && blockIdx.y == 0) {
-    seq_z[s] = z;
-    tokens[s] = n;
-    if (alone) {
-      tokens[1] = n;
+    const bool alone = gridDim.x == 1 && gridDim.y == 1;
+    if (col == 0 && alone) {
+      n = n_all;
+      tokens[0] = tokens[1] = n;
       tokens[2] = n > 0;
-      losses[0] = n > 0 ? sequence_loss(cp_all, n, E, k) : 0.f;
-      losses[1] = n > 0 ? z / (float)n : 0.f;
+      losses[0] = n > 0 ? cp * ((float)E / (float)k) / ((float)n * (float)n) : 0.f;
+      losses[1] = n > 0 ? z_all / (float)n : 0.f;
+      last_all = 0;
+    } else if (col == 0) {
+      n = n_all;
+      store_shared(part + (size_t)s * gridDim.y + blockIdx.y,
+                   n > 0 ? cp * ((float)E / (float)k) / ((float)n * (float)n) : 0.f);
+      if (blockIdx.y == 0) {
+        store_shared(seq_z + s, z_all);
+        store_shared(tokens + s, n);
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+      asm volatile("" ::: "memory");
+      last_all = __hip_atomic_fetch_add(arrivals, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 (int)(gridDim.x * gridDim.y) - 1;
     }
   }
-}
-
-// The losses of several sequences or blocks of experts.
-constexpr int kLossThreads = 512;
-__global__ __launch_bounds__(kLossThreads) void balance_losses_kernel(const float* __restrict__ part,
-                                                                      const float* __restrict__ seq_z, int E, int k,
-                                                                      int S, int blocks, int32_t* __restrict__ tokens,
-                                                                      float* __restrict__ losses) {
-  constexpr int kWaves = kLossThreads / 64;
-  __shared__ float redb[kWaves], redz[kWaves];
-  __shared__ int redn[kWaves], redu[kWaves];
-  float loss = 0.f, z = 0.f;
-  int n = 0, used = 0;
-  for (long long i = threadIdx.x; i < (long long)S * blocks; i += kLossThreads) {
-    const int s = (int)(i / blocks);
-    const int ns = tokens[s];
-    if (ns > 0) loss += sequence_loss(part[i], ns, E, k);
-  }
-  for (int s = threadIdx.x; s < S; s += kLossThreads) {
-    const int ns = tokens[s];
-    if (ns > 0) z += seq_z[s], n += ns, used++;
+  __syncthreads();
+  if (!last_all) return;
+  float loss = 0.f;
+  z = 0.f;
+  n = 0;
+  int used = 0;
+  for (int i = threadIdx.x; i < S * (int)gridDim.y; i += kSumThreads) loss += load_shared(part + i);
+  for (int i = threadIdx.x; i < S; i += kSumThreads) {
+    const int ns = load_shared(tokens + i);
+    z += load_shared(seq_z + i);
+    n += ns;
+    used += ns > 0;
   }
   loss = group_sum<64>(loss);
   z = group_sum<64>(z);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64), used += __shfl_xor(used, o, 64);
-  if ((threadIdx.x & 63) == 0) {
-    const int w = threadIdx.x >> 6;
-    redb[w] = loss, redz[w] = z, redn[w] = n, redu[w] = used;
+  n = group_sum<64>(n);
+  used = group_sum<64>(used);
+  if (col == 0) {
+    redp[row][0] = loss, redp[row][1] = z;
+    redc[row][0] = n, redc[row][1] = used;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int w = 1; w < kWaves; w++) loss += redb[w], z += redz[w], n += redn[w], used += redu[w];
+    for (int w = 1; w < kRows; w++) loss += redp[w][0], z += redp[w][1], n += redc[w][0], used += redc[w][1];
     tokens[S] = n;
     tokens[S + 1] = used;
     losses[0] = used > 0 ? loss / (float)used : 0.f;
@@ -602,22 +612,17 @@ hipError_t launch_balance(const uint16_t* logits, const int32_t* ids, int T, int
   float2* part_zn = reinterpret_cast<float2*>(ws + b.zn);
   float* part = reinterpret_cast<float*>(ws + b.part);
   float* seq_z = part + (size_t)S * b.blocks;
-  hipError_t e = hipSuccess;
-  if (b.chunks > 0) {
-    with_lanes(E, [&](auto lanes) {
-      constexpr int L = decltype(lanes)::value;
-      hipLaunchKernelGGL((balance_pieces_kernel<L>), dim3(b.chunks), dim3(kPieceThreads<L>), 0, stream, logits, ids, T,
-                         E, k, seq, S, b.chunk, part_p, part_c, part_zn);
-    });
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  int* arrivals = reinterpret_cast<int*>(ws + b.arrivals);
+  const dim3 grid(b.chunks > 0 ? b.chunks : 1);  // without tokens: the arrivals alone
+  with_lanes(E, [&](auto lanes) {
+    constexpr int L = decltype(lanes)::value;
+    hipLaunchKernelGGL((balance_pieces_kernel<L>), grid, dim3(kPieceThreads<L>), 0, stream, logits, ids, T, E, k, seq,
+                       S, b.chunk, part_p, part_c, part_zn, arrivals);
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(balance_sequences_kernel, dim3(S, b.blocks), dim3(kSumThreads), 0, stream, part_p, part_c,
-                     part_zn, T, E, k, seq, S, b.chunk, counts, tokens, losses, part, seq_z);
-  e = hipGetLastError();
-  if (e != hipSuccess || (S == 1 && b.blocks == 1)) return e;
-  hipLaunchKernelGGL(balance_losses_kernel, dim3(1), dim3(kLossThreads), 0, stream, part, seq_z, E, k, S, b.blocks,
-                     tokens, losses);
+                     part_zn, T, E, k, seq, S, b.chunk, counts, tokens, losses, part, seq_z, arrivals);
   return hipGetLastError();
 }
 
