@@ -134,6 +134,8 @@ __device__ __forceinline__ float rms_scale(float sum, float inv_n, float eps) {
   return rsqrtf(fmaf(sum, inv_n, eps));
 }
 
+// moe_norm.  Bound by HBM at length: 8192 fp32 rows of 2880 (142 MB) take 26 us,
+// 5.4 TB/s, as a copy does; one row takes 2.0 us, the launch and one round trip.
 template <typename X, int CH, bool PART>
 __global__ __launch_bounds__(kMaxTeam) void norm_kernel(const X* __restrict__ x, const uint16_t* __restrict__ w, int T,
                                                         int N, float inv_n, float eps, uint16_t* __restrict__ xn) {
@@ -173,7 +175,8 @@ __global__ __launch_bounds__(kMaxTeam) void norm_kernel(const X* __restrict__ x,
 
 // The block's output.  x_out may be x itself: each element is read and written
 // by one thread, in this order (what the row's last chunk reads beside its own
-// elements, it drops).
+// elements, it drops).  Bound by HBM at length: 8192 x 4 x 2880 (519 MB) take 91
+// us, 5.7 TB/s; one token takes 2.9 us.
 template <typename X, typename P, int CH, bool PART>
 __global__ __launch_bounds__(kMaxTeam) void combine_norm_kernel(const CombineNormArgs a) {
   constexpr int kSlots = CH == 1 ? 4 : CH == 2 ? 2 : 1;  // slots whose rows are under way together
@@ -286,7 +289,9 @@ __device__ __forceinline__ void store_columns(const Team<PART>& team, float (&dw
   for (int c = 0; c < CH; c++) store8(part + (size_t)blockIdx.x * N, team.at(c), N, dw[c]);
 }
 
-// Gradients of moe_norm.  dx may be dres itself.
+// Gradients of moe_norm.  dx may be dres itself.  8192 rows of 2880 (189 MB): 36
+// us, 5.3 TB/s, and 3 us for the column sums' launch; with 1000 rows of fp32 (29
+// MB, 9 + 3 us) the round trips of a workgroup's two rows one after the other.
 //
 // A team's next row is fetched ahead of this row's stores: loads and stores
 // complete in the order of their issue, so a load behind the stores would wait
@@ -370,6 +375,10 @@ __global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backwar
 // read again.  dx may be dx_out itself.  A team's next row is fetched into the
 // registers of this row as soon as these have been used, ahead of this row's
 // stores (as in norm_backward_kernel); so are its gates.
+//
+// 8192 x 4 x 2880 (944 MB): 187 us, 5.0 TB/s, and 5 us for the column sums; a
+// shorter batch (777 x 3 x 1023, 16 MB, 8 + 3 us) is bound by one row's chain of
+// loads, three sums over the team and stores.
 template <typename X, typename P, int CH, bool PART, int KR>
 __global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
   constexpr int KH = KR > 0 ? KR : 1;
