@@ -204,9 +204,11 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_kernel(const CombineNor
     float g[kSlots];
 #pragma unroll
     for (int u = 0; u < kSlots; u++) {
-      const int q = min(q0 + u, k - 1);
-      g[u] = q0 + u >= k || Nt == 0 ? 0.f : a.gates ? a.gates[(size_t)t * k + q] : 1.f;
-      fetch_row(team, proj + (size_t)q * N, Nt, pr[u]);
+      g[u] = 0.f;
+      if (q0 + u < k) {
+        if (Nt > 0) g[u] = a.gates ? a.gates[(size_t)t * k + q0 + u] : 1.f;
+        fetch_row(team, proj + (size_t)(q0 + u) * N, Nt, pr[u]);
+      }
     }
     if (ragged(N)) {
 #pragma unroll
