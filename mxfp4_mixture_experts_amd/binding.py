@@ -472,14 +472,15 @@ def moe_norm(x, w, T: int, N: int, xn, eps: float = 1e-5, stream=None):
     """The block's input norm (moe_norm): xn [T,N] bf16 = x * rsqrt(mean(x^2) + eps) * w of each row
     of x [T,N] bf16 or f32; w [N] bf16."""
     lib = load_library()
+    T, N = int(T), int(N)
     dev = _device_of(xn, "xn")
     xt = _dtype(x, "x")
     _run(lib.moe_norm, dev, stream, _arg(x, "x", _ELEMENTS[xt], T * N, dev), xt,
-         _arg(w, "w", _BF16, N, dev), T, N, eps, _arg(xn, "xn", _BF16, T * N, dev))
+         _arg(w, "w", _BF16, N, dev), T, N, float(eps), _arg(xn, "xn", _BF16, T * N, dev))
 
 
 def moe_norm_backward_workspace_size(T: int, N: int) -> int:
-    return _size(load_library().moe_norm_backward_workspace_size(T, N), "moe_norm_backward")
+    return _size(load_library().moe_norm_backward_workspace_size(int(T), int(N)), "moe_norm_backward")
 
 
 def moe_norm_backward(dxn, x, w, T: int, N: int, dx, dw=None, dres=None, eps: float = 1e-5, workspace=None,
@@ -488,12 +489,13 @@ def moe_norm_backward(dxn, x, w, T: int, N: int, dx, dw=None, dres=None, eps: fl
     stream's own gradient, added; dx may be dres) and dw [N] f32 (optional).  workspace: a uint8
     device tensor of at least moe_norm_backward_workspace_size(T, N) bytes, for dw."""
     lib = load_library()
+    T, N = int(T), int(N)
     dev = _device_of(dx, "dx")
     ws, nbytes = _workspace(workspace, dev)
     xt = _dtype(x, "x")
     xs = _ELEMENTS[xt]
     _run(lib.moe_norm_backward, dev, stream, _arg(dxn, "dxn", _BF16, T * N, dev), _arg(x, "x", xs, T * N, dev), xt,
-         _arg(w, "w", _BF16, N, dev), _arg(dres, "dres", xs, T * N, dev), T, N, eps, _arg(dx, "dx", xs, T * N, dev),
+         _arg(w, "w", _BF16, N, dev), _arg(dres, "dres", xs, T * N, dev), T, N, float(eps), _arg(dx, "dx", xs, T * N, dev),
          _arg(dw, "dw", _F32, N, dev), ws, nbytes)
 
 
@@ -504,16 +506,17 @@ def moe_combine_norm(proj, gates, T: int, k: int, N: int, x, x_out, w_post=None,
     x + scale * that (of x's type, may be x), and with w_next [N] bf16 the next block's input
     norm into xn [T,N] bf16."""
     lib = load_library()
+    T, k, N = int(T), int(k), int(N)
     dev = _device_of(x_out, "x_out")
     pt, xt = _dtype(proj, "proj"), _dtype(x, "x")
     _run(lib.moe_combine_norm, dev, stream, _arg(proj, "proj", _ELEMENTS[pt], T * k * N, dev), pt,
          _arg(gates, "gates", _F32, T * k, dev), T, k, N, _arg(w_post, "w_post", _BF16, N, dev),
-         _arg(x, "x", _ELEMENTS[xt], T * N, dev), xt, scale, eps, _arg(x_out, "x_out", _ELEMENTS[xt], T * N, dev),
+         _arg(x, "x", _ELEMENTS[xt], T * N, dev), xt, float(scale), float(eps), _arg(x_out, "x_out", _ELEMENTS[xt], T * N, dev),
          _arg(w_next, "w_next", _BF16, N, dev), _arg(xn, "xn", _BF16, T * N, dev))
 
 
 def moe_combine_norm_backward_workspace_size(T: int, N: int) -> int:
-    return _size(load_library().moe_combine_norm_backward_workspace_size(T, N), "moe_combine_norm_backward")
+    return _size(load_library().moe_combine_norm_backward_workspace_size(int(T), int(N)), "moe_combine_norm_backward")
 
 
 def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=None, dproj=None, dgates=None,
@@ -525,6 +528,7 @@ def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=No
     wanted.  workspace: a uint8 device tensor of at least
     moe_combine_norm_backward_workspace_size(T, N) bytes, for the weights' gradients."""
     lib = load_library()
+    T, k, N = int(T), int(k), int(N)
     dev = _device_of(proj, "proj")
     stream_like = next((t for t in (dx_out, x_out, dx) if t is not None), None)
     if stream_like is None:
@@ -535,14 +539,14 @@ def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=No
     _run(lib.moe_combine_norm_backward, dev, stream, _arg(dx_out, "dx_out", xs, T * N, dev),
          _arg(dxn, "dxn", _BF16, T * N, dev), _arg(x_out, "x_out", xs, T * N, dev),
          _arg(w_next, "w_next", _BF16, N, dev), _arg(proj, "proj", ps, T * k * N, dev), pt,
-         _arg(gates, "gates", _F32, T * k, dev), T, k, N, _arg(w_post, "w_post", _BF16, N, dev), xt, scale, eps,
+         _arg(gates, "gates", _F32, T * k, dev), T, k, N, _arg(w_post, "w_post", _BF16, N, dev), xt, float(scale), float(eps),
          _arg(dx, "dx", xs, T * N, dev), _arg(dproj, "dproj", ps, T * k * N, dev),
          _arg(dgates, "dgates", _F32, T * k, dev), _arg(dw_post, "dw_post", _F32, N, dev),
          _arg(dw_next, "dw_next", _F32, N, dev), ws, nbytes)
 
 
 def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
-    return _size(load_library().moe_balance_workspace_size(T, E, S), "moe_balance")
+    return _size(load_library().moe_balance_workspace_size(int(T), int(E), int(S)), "moe_balance")
 
 
 def moe_balance(logits, topk_ids, T: int, E: int, k: int, counts, tokens, losses, seq_offsets=None, S: int = 1,
@@ -553,6 +557,7 @@ def moe_balance(logits, topk_ids, T: int, E: int, k: int, counts, tokens, losses
     all T tokens).  workspace: a uint8 device tensor of at least moe_balance_workspace_size(T, E, S)
     bytes."""
     lib = load_library()
+    T, E, k, S = int(T), int(E), int(k), int(S)
     dev = _device_of(counts, "counts")
     ws, nbytes = _workspace(workspace, dev)
     _run(lib.moe_balance, dev, stream, _arg(logits, "logits", _BF16, T * E, dev),
@@ -568,6 +573,7 @@ def moe_route_backward(logits, topk_ids, gates, dgates, T: int, E: int, k: int, 
     the device, or None; with it logits, seq_offsets, S, counts and tokens as given to and written by
     moe_balance)."""
     lib = load_library()
+    T, E, k, S = int(T), int(E), int(k), int(S)
     dev = _device_of(dlogits, "dlogits")
     dt = _dtype(dlogits, "dlogits")
     _run(lib.moe_route_backward, dev, stream, _arg(logits, "logits", _BF16, T * E, dev),

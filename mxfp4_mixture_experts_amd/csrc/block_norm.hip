@@ -378,15 +378,20 @@ __global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backwar
 // registers of this row as soon as these have been used, ahead of this row's
 // stores (as in norm_backward_kernel); so are its gates.
 //
-// 8192 x 4 x 2880 (944 MB): 187 us, 5.0 TB/s, and 5 us for the column sums; a
+// 8192 x 4 x 2880 (944 MB): 181 us, 5.2 TB/s, and 5 us for the column sums; a
 // shorter batch (777 x 3 x 1023, 16 MB, 8 + 3 us) is bound by one row's chain of
 // loads, three sums over the team and stores.
+//
+// The threads of a workgroup: as many as the registers allow (three waves on a
+// SIMD, two with eight slots' rows or more than one chunk a thread).
+template <int CH, int KR>
+constexpr int kCombineThreads = CH == 1 && KR != 8 ? 768 : kMaxTeam;
 template <typename X, typename P, int CH, bool PART, int KR>
-__global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
+__global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backward_kernel(const CombineNormBackwardArgs a) {
   constexpr int KH = KR > 0 ? KR : 1;
   __shared__ __align__(16) float red1[2][kMaxWaveTeams][3][kMaxWaves], red2[2][kMaxWaveTeams][1][kMaxWaves];
   __shared__ __align__(16) float redg[2][kMaxWaveTeams][kMaxTopK][kMaxWaves];
-  __shared__ __align__(16) float cols[CH == 1 ? kMaxTeam * 8 : 8];
+  __shared__ __align__(16) float cols[CH == 1 ? kCombineThreads<CH, KR> * 8 : 8];
   const int N = a.N, k = a.k, T = a.T;
   const Team<PART> team(N);
   const int step = gridDim.x * team.count;
@@ -624,11 +629,12 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_backward_kernel(const C
 }
 
 // out[n] = sum_g part[g][n]: 16 columns (64 bytes of a row) x 64 interleaved
-// groups of rows, each added in order (eight loads under way), then the groups
+// groups of rows, each added in order (four loads under way: one round for the
+// 256 rows of a launch), then the groups
 // in order.
 constexpr int kSumCols = 16;
 constexpr int kSumGroups = 64;
-constexpr int kSumDepth = 8;
+constexpr int kSumDepth = 4;
 __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const float* __restrict__ part0, float* out0,
                                                                           const float* __restrict__ part1, float* out1,
                                                                           int G, int N) {
@@ -661,11 +667,10 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const 
 }
 
 // Teams and workgroups of a launch, by the rows' number and length alone.
-// Forward: workgroups of up to 256 threads.  Backward: 256 workgroups, one a CU
-// (their column sums are a small part of the traffic then; with the next row
-// fetched ahead, one row under way on a CU keeps up with two: 8192 x 4 x 2880,
-// block output, 191 us against 193 with 512 workgroups and 197 with 768), then
-// more teams in each.
+// Forward: workgroups of up to 256 threads.  Backward: up to 256 workgroups, one
+// a CU, and then more teams in each, so that the column sums are 256 rows at
+// most (two workgroups a CU, block output, 2048 x 4 x 2880 bf16: 48 us; two
+// teams in one: 39 us).
 constexpr int kForwardThreads = 256;
 constexpr int kBackwardGroups = 256;
 dim3 forward_block(int N) {
@@ -678,6 +683,12 @@ dim3 backward_block(int T, int N, int threads) {
   const int want = (int)(((long long)T + kBackwardGroups - 1) / kBackwardGroups);
   return dim3(team, want < 1 ? 1 : want < most ? want : most);
 }
+// One chunk a thread and teams of several waves, which wait for each other at
+// barriers: 768 or 1024 threads a workgroup (gradients of the block output,
+// 8192 x 1 x 2880 bf16: 69 us, with 512 threads 99).  Teams of one wave or less
+// do better with 512 (norm gradient, 16384 x 96: 9.1 us, with 1024 threads 10.8;
+// block output, 16384 x 4 x 200: 36.5 us, with 768 threads 40.1).
+bool many_waves(int N) { return chunks_per_thread(N) == 1 && team_threads(N) > 64; }
 int backward_groups(int T, dim3 block) {
   const int groups = (int)(((long long)T + block.y - 1) / block.y);
   return groups < kBackwardGroups ? groups : kBackwardGroups;
@@ -726,7 +737,7 @@ hipError_t launch_norm(const void* x, bool x_f32, const uint16_t* w, int T, int 
 
 hipError_t launch_norm_backward(const uint16_t* dxn, const void* x, bool x_f32, const uint16_t* w, const void* dres,
                                 int T, int N, float eps, void* dx, float* dw, void* workspace, hipStream_t stream) {
-  const dim3 block = backward_block(T, N, chunks_per_thread(N) == 1 ? kMaxThreads : kMaxTeam);
+  const dim3 block = backward_block(T, N, many_waves(N) ? kMaxThreads : kMaxTeam);
   const int G = backward_groups(T, block);
   if (G == 0) return launch_column_sums(nullptr, dw, nullptr, nullptr, 0, N, stream);
   float* sums = !dw ? nullptr : G == 1 ? dw : static_cast<float*>(workspace);
@@ -785,7 +796,11 @@ hipError_t launch_combine_norm(CombineNormArgs a, bool x_f32, bool proj_f32, hip
 
 hipError_t launch_combine_norm_backward(CombineNormBackwardArgs a, bool x_f32, bool proj_f32, float* dw_post,
                                         float* dw_next, void* workspace, hipStream_t stream) {
-  const dim3 block = backward_block(a.T, a.N, kMaxTeam);
+  // the slots' rows held in registers: at most 64 values a thread
+  const int ch = chunks_per_thread(a.N);
+  const int most = ch == 1 ? 8 : ch == 2 ? 4 : 0, few = most / 2;
+  const int held = a.k <= few ? few : a.k <= most ? most : 0;
+  const dim3 block = backward_block(a.T, a.N, many_waves(a.N) && held != 8 ? kCombineThreads<1, 0> : kMaxTeam);
   const int G = backward_groups(a.T, block);
   if (G == 0) return launch_column_sums(nullptr, dw_post, nullptr, dw_next, 0, a.N, stream);
   a.stream = streams(a.T, a.k, a.N, proj_f32);
@@ -798,17 +813,19 @@ hipError_t launch_combine_norm_backward(CombineNormBackwardArgs a, bool x_f32, b
     using X = decltype(elem);
     constexpr int CH = decltype(ch)::value;
     constexpr bool PART = decltype(part)::value;
-    // the slots' rows held in registers: at most 64 values a thread
-    constexpr int KR = CH == 1 ? 8 : CH == 2 ? 4 : 0;
-    constexpr int KS = CH == 1 ? 4 : CH == 2 ? 2 : 0;
+    constexpr int most = CH == 1 ? 8 : CH == 2 ? 4 : 0, few = most / 2;
     auto with_proj = [&](auto pelem) {
       using P = decltype(pelem);
-      if (a.k <= KS)
-        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, KS>), grid, block, 0, stream, a);
-      else if (a.k <= KR)
-        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, KR>), grid, block, 0, stream, a);
+      auto launch = [&](auto rows) {
+        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, decltype(rows)::value>), grid, block, 0,
+                           stream, a);
+      };
+      if (a.k <= few)
+        launch(std::integral_constant<int, few>{});
+      else if (a.k <= most)
+        launch(std::integral_constant<int, most>{});
       else
-        hipLaunchKernelGGL((combine_norm_backward_kernel<X, P, CH, PART, 0>), grid, block, 0, stream, a);
+        launch(std::integral_constant<int, 0>{});
     };
     if (proj_f32)
       with_proj(float{});
