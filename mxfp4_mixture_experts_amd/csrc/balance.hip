@@ -304,7 +304,8 @@ __global__ __launch_bounds__(kPieceThreads<L>) void balance_pieces_kernel(
 // device-scope stores and loads (sc1: past the XCD's own L2 to the level that
 // all share), and a workgroup counts itself in once its stores are complete
 // (vmcnt); a release and acquire instead write back and drop whole L2s, 4 us for
-// one workgroup and 9 us for 296.
+// one workgroup and 9 us for 296.  arrivals == NULL: no counting, a third launch
+// adds the shares.
 constexpr int kSumThreads = 1024;
 constexpr int kSumDepth = 4;
 
@@ -315,6 +316,41 @@ __device__ __forceinline__ V load_shared(const V* p) {  // written by another wo
 template <typename V>
 __device__ __forceinline__ void store_shared(V* p, V v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The losses and the tokens' totals from the shares of every sequence and block
+// of experts, by one workgroup in a fixed order.
+__device__ __forceinline__ void sum_losses(const float* part, const float* seq_z, int S, int blocks, int32_t* tokens,
+                                           float* losses, float* redf, int* redi) {
+  constexpr int kWaves = kSumThreads / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float loss = 0.f, z = 0.f;
+  int n = 0, used = 0;
+  for (int i = threadIdx.x; i < S * blocks; i += kSumThreads) loss += load_shared(part + i);
+  for (int i = threadIdx.x; i < S; i += kSumThreads) {
+    const int ns = load_shared(tokens + i);
+    z += load_shared(seq_z + i);
+    n += ns;
+    used += ns > 0;
+  }
+  loss = group_sum<64>(loss);
+  z = group_sum<64>(z);
+  n = group_sum<64>(n);
+  used = group_sum<64>(used);
+  if (lane == 0) {
+    redf[wave] = loss, redf[kWaves + wave] = z;
+    redi[wave] = n, redi[kWaves + wave] = used;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kWaves; w++)
+      loss += redf[w], z += redf[kWaves + w], n += redi[w], used += redi[kWaves + w];
+    tokens[S] = n;
+    tokens[S + 1] = used;
+    losses[0] = used > 0 ? loss / (float)used : 0.f;
+    losses[1] = n > 0 ? z / (float)n : 0.f;
+  }
 }
 
 __global__ __launch_bounds__(kSumThreads) void balance_sequences_kernel(
@@ -385,43 +421,25 @@ __global__ __launch_bounds__(kSumThreads) void balance_sequences_kernel(
         store_shared(seq_z + s, z_all);
         store_shared(tokens + s, n);
       }
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-      asm volatile("" ::: "memory");
-      last_all = __hip_atomic_fetch_add(arrivals, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                 (int)(gridDim.x * gridDim.y) - 1;
+      last_all = 0;
+      if (arrivals) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        asm volatile("" ::: "memory");
+        last_all = __hip_atomic_fetch_add(arrivals, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   (int)(gridDim.x * gridDim.y) - 1;
+      }
     }
   }
   __syncthreads();
-  if (!last_all) return;
-  float loss = 0.f;
-  z = 0.f;
-  n = 0;
-  int used = 0;
-  for (int i = threadIdx.x; i < S * (int)gridDim.y; i += kSumThreads) loss += load_shared(part + i);
-  for (int i = threadIdx.x; i < S; i += kSumThreads) {
-    const int ns = load_shared(tokens + i);
-    z += load_shared(seq_z + i);
-    n += ns;
-    used += ns > 0;
-  }
-  loss = group_sum<64>(loss);
-  z = group_sum<64>(z);
-  n = group_sum<64>(n);
-  used = group_sum<64>(used);
-  if (col == 0) {
-    redp[row][0] = loss, redp[row][1] = z;
-    redc[row][0] = n, redc[row][1] = used;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < kRows; w++) loss += redp[w][0], z += redp[w][1], n += redc[w][0], used += redc[w][1];
-    tokens[S] = n;
-    tokens[S + 1] = used;
-    losses[0] = used > 0 ? loss / (float)used : 0.f;
-    losses[1] = n > 0 ? z / (float)n : 0.f;
-  }
+  if (last_all) sum_losses(part, seq_z, S, gridDim.y, tokens, losses, redp[0], redc[0]);
+}
+
+__global__ __launch_bounds__(kSumThreads) void balance_losses_kernel(const float* part, const float* seq_z, int S,
+                                                                     int blocks, int32_t* tokens, float* losses) {
+  __shared__ float redf[2 * kSumThreads / 64];
+  __shared__ int redi[2 * kSumThreads / 64];
+  sum_losses(part, seq_z, S, blocks, tokens, losses, redf, redi);
 }
 
 constexpr int kRouteThreads = 256;
@@ -614,6 +632,8 @@ void with_lanes(int E, F f) {
 
 }  // namespace
 
+constexpr int kArrivals = 128;  // workgroups of the second launch that count themselves in
+
 size_t balance_workspace_bytes(int T, int E, int S) { return balance_layout(T, E, S).total; }
 
 hipError_t launch_balance(const uint16_t* logits, const int32_t* ids, int T, int E, int k, const int32_t* seq, int S,
@@ -634,8 +654,18 @@ hipError_t launch_balance(const uint16_t* logits, const int32_t* ids, int T, int
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  // Many workgroups wait on each other's arrivals for longer than a launch
+  // takes: 65536 x 512 in 37 sequences, 296 workgroups, 25.0 us with arrivals and
+  // 23.3 with a third launch; 4096 x 32 in 8 sequences 9.5 and 10.0, 64 x 32 in
+  // 64 sequences 11.7 and 12.6 (and about 3.5 us less for the host).
+  const bool counted = (long long)S * b.blocks <= kArrivals;
   hipLaunchKernelGGL(balance_sequences_kernel, dim3(S, b.blocks), dim3(kSumThreads), 0, stream, part_p, part_c,
-                     part_zn, T, E, k, seq, S, b.chunk, counts, tokens, losses, part, seq_z, arrivals);
+                     part_zn, T, E, k, seq, S, b.chunk, counts, tokens, losses, part, seq_z,
+                     counted ? arrivals : nullptr);
+  e = hipGetLastError();
+  if (e != hipSuccess || counted) return e;
+  hipLaunchKernelGGL(balance_losses_kernel, dim3(1), dim3(kSumThreads), 0, stream, part, seq_z, S, b.blocks, tokens,
+                     losses);
   return hipGetLastError();
 }
 
