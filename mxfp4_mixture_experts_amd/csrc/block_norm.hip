@@ -607,7 +607,7 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
         for (int c = 0; c < CH; c++) {
           float o[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) o[j] = g * grad[c][j];
+          for (int j = 0; j < 8; j++) o[j] = g == 0.f ? 0.f : g * grad[c][j];
           store8(out, team.at(c), Nt, o, a.stream);
         }
       };

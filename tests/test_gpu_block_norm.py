@@ -313,6 +313,23 @@ def test_combine_norm_backward(T, k, N, xt, pt, post, nxt):
     _backward(T, k, N, xt, pt, post, nxt, gates, proj, check=True)
 
 
+def test_unrouted_slot_of_an_infinite_gradient():
+    """A gradient that holds an infinity or a NaN still leaves an unrouted slot's dproj and dgate 0."""
+    _announce("combine_norm_backward: infinite gradient, unrouted slot")
+    for N in (64, 2880):
+        T, k = 3, 2
+        gates = dev([[0.5, 0.0], [0.0, 0.0], [0.25, 0.75]])
+        proj = dev(np.ones((T, k, N)))
+        proj[0, 1] = proj[1] = float("nan")
+        dx_out = dev(np.ones((T, N)))
+        dx_out[0, 3], dx_out[1, 5] = float("inf"), float("nan")
+        dproj, dgates = nan_like((T, k, N), torch.float32), nan_like((T, k), torch.float32)
+        B.moe_combine_norm_backward(dx_out, proj, gates, T, k, N, dproj=dproj, dgates=dgates)
+        assert not dproj[0, 1].any() and not dproj[1].any() and not dgates[0, 1].any() and not dgates[1].any()
+        assert float(dproj[0, 0, 3]) == float("inf") and torch.equal(dproj[2, 1], torch.full((N,), 0.75, device="cuda"))
+        assert torch.equal(dgates[2], torch.full((k,), float(N), device="cuda"))
+
+
 def test_combine_norm_backward_dense():
     """k = 1 without gates: a dense block's output."""
     _announce("combine_norm_backward: gates None")
