@@ -628,41 +628,38 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
   if (a.part_next) store_columns(team, dw_next, cols, N, a.part_next);
 }
 
-// out[n] = sum_g part[g][n]: 16 columns (64 bytes of a row) x 64 interleaved
-// groups of rows, each added in order (four loads under way: one round for the
-// 256 rows of a launch), then the groups
-// in order.
+// out[n] = sum_g part[g][n] of at most 256 rows: 16 columns (64 bytes of a row) x
+// 64 interleaved groups of rows, a thread's four rows under way together; then
+// the four groups of a wave by row swaps, then the waves, all in a fixed order.
 constexpr int kSumCols = 16;
 constexpr int kSumGroups = 64;
 constexpr int kSumDepth = 4;
+constexpr int kBackwardGroups = kSumGroups * kSumDepth;  // rows of sums, workgroups of a backward launch
 __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const float* __restrict__ part0, float* out0,
                                                                           const float* __restrict__ part1, float* out1,
                                                                           int G, int N) {
-  __shared__ float red[kSumGroups][kSumCols + 1];
+  constexpr int kWaves = kSumCols * kSumGroups / 64;
+  __shared__ float red[kWaves][kSumCols];
   const float* part = blockIdx.y ? part1 : part0;
   float* out = blockIdx.y ? out1 : out0;
   const int col = threadIdx.x % kSumCols, grp = threadIdx.x / kSumCols;
   const int n = blockIdx.x * kSumCols + col;
   float s = 0.f;
-  if (n < N) {
-    for (int g = grp; g < G; g += kSumGroups * kSumDepth) {
-      float v[kSumDepth];
+  if (n < N && G > 0) {
+    float v[kSumDepth];
 #pragma unroll
-      for (int u = 0; u < kSumDepth; u++) {
-        const int gu = g + u * kSumGroups;
-        v[u] = part[(size_t)min(gu, G - 1) * N + n];
-      }
+    for (int u = 0; u < kSumDepth; u++) v[u] = part[(size_t)min(grp + u * kSumGroups, G - 1) * N + n];
 #pragma unroll
-      for (int u = 0; u < kSumDepth; u++) s += g + u * kSumGroups < G ? v[u] : 0.f;
-    }
+    for (int u = 0; u < kSumDepth; u++) s += grp + u * kSumGroups < G ? v[u] : 0.f;
   }
-  red[grp][col] = s;
+  s = rows_sum(s);
+  if ((threadIdx.x & 63) < kSumCols) red[threadIdx.x >> 6][col] = s;
   __syncthreads();
   if (grp == 0 && n < N) {
-    float v = red[0][col];
+    s = red[0][col];
 #pragma unroll
-    for (int g = 1; g < kSumGroups; g++) v += red[g][col];
-    out[n] = v;
+    for (int w = 1; w < kWaves; w++) s += red[w][col];
+    out[n] = s;
   }
 }
 
@@ -672,7 +669,6 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sum_kernel(const 
 // most (two workgroups a CU, block output, 2048 x 4 x 2880 bf16: 48 us; two
 // teams in one: 39 us).
 constexpr int kForwardThreads = 256;
-constexpr int kBackwardGroups = 256;
 dim3 forward_block(int N) {
   const int team = team_threads(N);
   return dim3(team, kForwardThreads > team ? kForwardThreads / team : 1);

@@ -230,6 +230,13 @@ template <int L, typename V>
 __device__ __forceinline__ V group_sum(V v) {
   return group_reduce<L>(v, [](V a, V b) { return a + b; });
 }
+// the sum of the four lanes of a wave that have the same place among 16
+__device__ __forceinline__ float rows_sum(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
 // The maximum, compared as integers in the floats' order: an integer maximum
 // takes its moved operand in the same instruction, a float one first quiets it.
 template <int L>
