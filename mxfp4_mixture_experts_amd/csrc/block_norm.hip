@@ -253,6 +253,9 @@ __global__ __launch_bounds__(kMaxTeam) void combine_norm_kernel(const CombineNor
     widen8(xr[c], xv);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
+      // rounded to the stream's type before the next norm, which is of the
+      // stream as stored: the gradients read it from there, and the separate
+      // calls have the same bits
       h[c][j] = rounded(fmaf(a.scale, h[c][j], xv[j]), x);
       s[0] = fmaf(h[c][j], h[c][j], s[0]);
     }
