@@ -294,6 +294,13 @@ __device__ __forceinline__ void store_columns(const Team<PART>& team, float (&dw
   for (int c = 0; c < CH; c++) store8(part + (size_t)blockIdx.x * N, team.at(c), N, dw[c]);
 }
 
+// Whether a gradient's launch fetches a team's next row ahead: not where a thread
+// has four chunks, whose two rows do not fit its registers (norm gradient, 2000
+// rows of 16000: 61 us, fetching ahead 181; 4000 of 8000, two chunks: 56 either
+// way, and 42 against 46 for the block output's, 1024 x 2 x 8192 bf16).
+template <int CH>
+constexpr bool kAhead = CH <= 2;
+
 // Gradients of moe_norm.  dx may be dres itself.  8192 rows of 2880 (189 MB): 36
 // us, 5.3 TB/s, and 3 us for the column sums' launch; with 1000 rows of fp32 (29
 // MB, 9 + 3 us) the round trips of a workgroup's two rows one after the other.
@@ -325,12 +332,13 @@ __global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backwar
     fetch_row(team, dxn + row, Nt, dr);
     if (dres) fetch_row(team, dres + row, Nt, rr);
   };
-  fetch(blockIdx.x * team.count + team.id);
+  if constexpr (kAhead<CH>) fetch(blockIdx.x * team.count + team.id);
   if (ragged(N)) settle_row(team, N, wr);
   int parity = 0;
   for (int t0 = blockIdx.x * team.count; t0 < T; t0 += step, parity ^= 1) {
     const int t = t0 + team.id;
     const int Nt = t < T ? N : 0;
+    if constexpr (!kAhead<CH>) fetch(t);
     float v[CH][8], d[CH][8], o[CH][8], s[2] = {0.f, 0.f};
     if (ragged(N)) {
       settle_row(team, Nt, xr);
@@ -355,7 +363,8 @@ __global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backwar
         s[1] = fmaf(v[c][j], d[c][j] * wv[j], s[1]);
       }
     }
-    if (t0 + step < T) fetch(t + step);
+    if constexpr (kAhead<CH>)
+      if (t0 + step < T) fetch(t + step);
     row_sum(team, s, red[parity]);
     const float r = rms_scale(s[0], inv_n, eps);
     const float m = s[1] * inv_n * r;
@@ -433,8 +442,10 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
       }
     }
   };
-  fetch_slots(blockIdx.x * team.count + team.id);
-  fetch_stream(blockIdx.x * team.count + team.id);
+  if constexpr (kAhead<CH>) {
+    fetch_slots(blockIdx.x * team.count + team.id);
+    fetch_stream(blockIdx.x * team.count + team.id);
+  }
   if (ragged(N)) {
     if (a.w_post) settle_row(team, N, wp);
     if (a.dxn) settle_row(team, N, wn);
@@ -453,6 +464,10 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
     const int t = t0 + team.id;
     const int Nt = t < T ? N : 0;
     const size_t row = (size_t)t * N;
+    if constexpr (!kAhead<CH>) {
+      fetch_slots(t);
+      fetch_stream(t);
+    }
     float h[CH][8], grad[CH][8], gate[KH], s[3] = {0.f, 0.f, 0.f};
     if (ragged(N)) {
       if constexpr (KR > 0) {
@@ -540,7 +555,8 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
         }
       }
     }
-    if (t0 + step < T) fetch_stream(t + step);
+    if constexpr (kAhead<CH>)
+      if (t0 + step < T) fetch_stream(t + step);
     if (a.dx) {
 #pragma unroll
       for (int c = 0; c < CH; c++) store8(static_cast<X*>(a.dx) + row, team.at(c), Nt, grad[c]);
@@ -602,7 +618,8 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
         }
       }
     }
-    if (t0 + step < T) fetch_slots(t + step);
+    if constexpr (kAhead<CH>)
+      if (t0 + step < T) fetch_slots(t + step);
     if (a.dproj) {
       auto store_slot = [&](int q, float g) {
         P* out = static_cast<P*>(a.dproj) + (row * k + (size_t)q * N);
