@@ -92,10 +92,9 @@ __device__ __forceinline__ void load_counts(const int32_t* row, int e0, int E, i
 // logit in [-64, 64], m is 0 and no maximum over the lanes is needed: no
 // exponential passes fp32's range, and a sum of them is at least e^-64.  (Router
 // logits lie there: 27.5 -> 25.3 us for the balance of 65536 x 512.)  Otherwise
-// m is the row's maximum, taken off first where it is so low that its product
-// with log2 e would pass fp32's range.  One rounding before the exponential
-// either way; that of m log2 e is common to the row and cancels in the
-// probabilities.
+// m is the row's maximum, taken off before the product with log2 e: rounded
+// apart, m log2 e would be off by far more than an exponent's range where m is
+// large.
 template <int L>
 __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
   float top = v[0];
@@ -109,10 +108,9 @@ __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
     return;
   }
   m = group_max<L>(top);
-  const float off = m < -1e38f ? m : 0.f;
-  const float base = (off - m) * kLog2e;
+  const float off = m > -INFINITY ? m : 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f(fmaf(v[j] - off, kLog2e, base));
+  for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f((v[j] - off) * kLog2e);
 }
 
 // The sums of three values over a group.  A whole wave adds them together: after

@@ -1,0 +1,120 @@
+"""The routing's balance and the logits' gradient over the whole range that their arguments may have:
+logits of any finite size, and what tokens beside a counted one hold.  Against the float64 oracle, or
+bit for bit.
+
+Tolerances, from the kernels' arithmetic (u = 2^-24, half a step of fp32).  A probability is
+exp2(x log2 e) / sum with x = l - m and m the row's maximum, or x = l while the maximum is small (at
+most 64 in size).  Its exponent is off by the roundings of l - m, of the product and of the constant: at
+most 2.3 u |x| of p, and |x| <= 87 where p has not vanished: 2^-16.2 of p; exp2, the sum over at most
+512 experts in chains of 8 + 6 and the reciprocal add under 20 u.  So p is within 2^-16.
+ - loss: p's error, and roundings of sums of one sign: at most 64 tokens in a lane's chain, 6 + 16 over
+   the lanes and waves, 32 + 16 + 6 and the sequences' in the later launches, under 200 u in all:
+   2^-15.2 of the loss, stated as 2^-15;
+ - z = m + ln(sum): 2^-17 for the sum's own error, and 4 u (|m| + |z|);
+ - a gradient: p once (2^-16), sums of p (within 2^-19 of their magnitudes, since far logits hardly
+   weigh), under 40 more roundings, and z's error times 2 dz / n: 2^-15 of the magnitudes, plus the
+   latter; then the output's own rounding.  fp32's least normal number is 2^-126: an exponential
+   below it may come out as 0, which with x = l - m (the sum is at least 1) takes less than 2^-126 of
+   p, and that times p's factor off the gradient.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.block_oracle as O
+from mxfp4_mixture_experts_amd import binding as B
+from test_gpu_balance import _announce, cuda, make, run_balance
+
+pytestmark = pytest.mark.gpu
+
+MOST = float(torch.finfo(torch.bfloat16).max)
+EXPERTS = [8, 32, 100, 512]        # 1, 4, 16 and 64 lanes a token
+
+
+def with_logits(c, l):
+    """The case c with the logits l (rounded to bf16) and the routing that follows from them."""
+    c["logits"] = torch.from_numpy(l.astype(np.float32)).to(torch.bfloat16).cuda()
+    c["l"] = c["logits"].float().cpu().numpy().astype(np.float64)
+    order = np.argsort(-c["l"], axis=1, kind="stable")[:, :c["k"]].astype(np.int32)
+    c["ids"] = np.where(c["ids"] == -1, -1, order).astype(np.int32)
+    return c
+
+
+def z_error(z, m):
+    return 2.0 ** -17 + 2.0 ** -22 * (np.abs(z) + np.abs(m))
+
+
+def check_losses(c):
+    counts, tokens, losses = run_balance(c)
+    wc, wt, wl = O.balance(c["l"], c["ids"], c["seq"])
+    np.testing.assert_array_equal(counts.cpu().numpy(), wc)
+    np.testing.assert_array_equal(tokens.cpu().numpy(), wt)
+    got = losses.double().cpu().numpy()
+    assert abs(got[0] - wl[0]) <= 2.0 ** -15 * wl[0], (got, wl)
+    live = [t for t, s in enumerate(O.counted(c["l"], c["ids"], c["seq"])) if s is not None]
+    z = np.array([O.softmax(c["l"][t])[1] for t in live])
+    if np.max(np.abs(z)) >= 2.0 ** 63:                    # its square may pass fp32's range
+        assert got[1] > 2.0 ** 100
+    else:
+        m = c["l"][live].max(1)
+        off = np.mean(2 * np.abs(z) * z_error(z, m) + z_error(z, m) ** 2) + 2.0 ** -16 * np.mean(z * z)
+        assert abs(got[1] - wl[1]) <= off, (got, wl, off)
+    return counts, tokens
+
+
+def logit_gradient(c, counts, tokens, dlosses, gates=True, dtype=torch.float32):
+    d = torch.full((c["T"], c["E"]), float("nan"), dtype=dtype, device="cuda")
+    B.moe_route_backward(c["logits"], cuda(c["ids"]), cuda(c["gates"]) if gates else None,
+                         cuda(c["dgates"]) if gates else None, c["T"], c["E"], c["k"], d,
+                         seq_offsets=cuda(c["seq"]) if c["given"] else None, S=len(c["seq"]) - 1, counts=counts,
+                         tokens=tokens, dlosses=cuda(np.asarray(dlosses, np.float32)))
+    return d
+
+
+def check_gradient(c, counts, tokens, dlosses, gates=True):
+    d = logit_gradient(c, counts, tokens, dlosses, gates).double().cpu().numpy()
+    want, mag = O.route_backward(c["l"], c["ids"], c["gates"], c["dgates"] if gates else None, c["seq"],
+                                 np.asarray(dlosses, np.float32).astype(np.float64))
+    load, toks, _ = O.balance(c["l"], c["ids"], c["seq"])
+    b = abs(dlosses[1]) * 2.0 / max(int(toks[-2]), 1)
+    bound = 2.0 ** -23 * np.abs(want) + 2.0 ** -15 * mag + 2.0 ** -126
+    for t, s in enumerate(O.counted(c["l"], c["ids"], c["seq"])):
+        if s is not None:
+            p, z = O.softmax(c["l"][t])
+            per_count = c["E"] * abs(dlosses[0]) / (c["k"] * float(toks[s]) ** 2 * float(toks[-1]))
+            factor = per_count * 2 * np.max(np.abs(load[s] - load[s].mean())) + b * abs(z)
+            bound[t] += p * b * z_error(z, c["l"][t].max()) + 2.0 ** -126 * factor
+    bad = np.argwhere(~(np.abs(d - want) <= bound))
+    assert bad.size == 0, (len(bad), bad[:3].tolist(), d[tuple(bad[0])], want[tuple(bad[0])])
+    return d
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("top", [1e5, -1e5, 3e9, 1e10, -1e10, 1e30, -1e30, 2.4e38, MOST, -1e38, -MOST])
+def test_large_finite_logits(top, E):
+    """A row whose largest logit is far from 0, some experts sharing it and some at the lowest
+    value, among ordinary tokens."""
+    _announce(f"logits up to {top:g}, E={E}")
+    T, k = 70, 4
+    c = make(T, E, k, None, seed=20, lost=0.0, masked=0.0)
+    l = c["l"].copy()
+    for t in (0, 3, 37, 69):
+        l[t] = top
+        l[t, 1::3] = -MOST
+        l[t, 2::3] = top * (1.25 if top < 0 else 0.5) if abs(top) < 2e38 else -MOST
+    with_logits(c, l)
+    counts, tokens = check_losses(c)
+    check_gradient(c, counts, tokens, [0.7 * T, 0.0], gates=False)
+    if abs(top) < 1e30:
+        check_gradient(c, counts, tokens, [0.7 * T, 0.2 * T])
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("spread", [20.0, 60.0, 300.0])
+def test_wide_logits(spread, E):
+    """Logits on both sides of 64, so that neighbouring tokens take either form of the exponential."""
+    _announce(f"logits spread over {spread}, E={E}")
+    T = 150
+    c = make(T, E, 4, [0, 40, 40, 149], seed=21, spread=spread)
+    counts, tokens = check_losses(c)
+    check_gradient(c, counts, tokens, [0.7 * T, 0.2 * T])
