@@ -89,18 +89,20 @@ __device__ __forceinline__ void load_counts(const int32_t* row, int e0, int E, i
 
 // The exponentials of a group's logits against a common m, in place; m is -inf
 // where no logit is above that.  While every token of the wave has its largest
-// logit in [-64, 64], m is 0 and no maximum over the lanes is needed: no
-// exponential passes fp32's range, and a sum of them is at least e^-64.  (Router
-// logits lie there: 27.5 -> 25.3 us for the balance of 65536 x 512.)  Otherwise
-// m is the row's maximum, taken off before the product with log2 e: rounded
-// apart, m log2 e would be off by far more than an exponent's range where m is
-// large.
+// logit in [-kNear, kNear], m is 0 and no maximum over the lanes is needed: no
+// exponential passes fp32's range, and a sum of them is at least e^-16, so that
+// the only probabilities which vanish with their exponentials lie under e^-71.
+// (Router logits lie there: 27.5 -> 25.3 us for the balance of 65536 x 512.)
+// Otherwise m is the row's maximum, taken off before the product with log2 e:
+// rounded apart, m log2 e would be off by far more than an exponent's range where
+// m is large.
+constexpr float kNear = 16.f;
 template <int L>
 __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
   float top = v[0];
 #pragma unroll
   for (int j = 1; j < 8; j++) top = fmaxf(top, v[j]);
-  const bool near = group_any<L>(top >= -64.f) && top <= 64.f;
+  const bool near = group_any<L>(top >= -kNear) && top <= kNear;
   if (__ballot(!near) == 0) {
     m = 0.f;
 #pragma unroll

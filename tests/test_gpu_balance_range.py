@@ -4,7 +4,7 @@ bit for bit.
 
 Tolerances, from the kernels' arithmetic (u = 2^-24, half a step of fp32).  A probability is
 exp2(x log2 e) / sum with x = l - m and m the row's maximum, or x = l while the maximum is small (at
-most 64 in size).  Its exponent is off by the roundings of l - m, of the product and of the constant: at
+most 16 in size).  Its exponent is off by the roundings of l - m, of the product and of the constant: at
 most 2.3 u |x| of p, and |x| <= 87 where p has not vanished: 2^-16.2 of p; exp2, the sum over at most
 512 experts in chains of 8 + 6 and the reciprocal add under 20 u.  So p is within 2^-16.
  - loss: p's error, and roundings of sums of one sign: at most 64 tokens in a lane's chain, 6 + 16 over
@@ -14,8 +14,8 @@ most 2.3 u |x| of p, and |x| <= 87 where p has not vanished: 2^-16.2 of p; exp2,
  - a gradient: p once (2^-16), sums of p (within 2^-19 of their magnitudes, since far logits hardly
    weigh), under 40 more roundings, and z's error times 2 dz / n: 2^-15 of the magnitudes, plus the
    latter; then the output's own rounding.  fp32's least normal number is 2^-126: an exponential
-   below it may come out as 0, which with x = l - m (the sum is at least 1) takes less than 2^-126 of
-   p, and that times p's factor off the gradient.
+   below it may come out as 0.  The sum is at least 1 with x = l - m and at least e^-16 with x = l, so
+   p loses less than 2^-126 e^16 < 2^-102, and the gradient that times p's factor.
 """
 import numpy as np
 import pytest
@@ -83,7 +83,7 @@ def check_gradient(c, counts, tokens, dlosses, gates=True):
             p, z = O.softmax(c["l"][t])
             per_count = c["E"] * abs(dlosses[0]) / (c["k"] * float(toks[s]) ** 2 * float(toks[-1]))
             factor = per_count * 2 * np.max(np.abs(load[s] - load[s].mean())) + b * abs(z)
-            bound[t] += p * b * z_error(z, c["l"][t].max()) + 2.0 ** -126 * factor
+            bound[t] += p * b * z_error(z, c["l"][t].max()) + 2.0 ** -102 * factor
     bad = np.argwhere(~(np.abs(d - want) <= bound))
     assert bad.size == 0, (len(bad), bad[:3].tolist(), d[tuple(bad[0])], want[tuple(bad[0])])
     return d
@@ -118,3 +118,21 @@ def test_wide_logits(spread, E):
     c = make(T, E, 4, [0, 40, 40, 149], seed=21, spread=spread)
     counts, tokens = check_losses(c)
     check_gradient(c, counts, tokens, [0.7 * T, 0.2 * T])
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("top,low", [(-60.0, -100.0), (-17.0, -95.0), (-16.0, -80.0), (-3.0, -85.0), (16.0, -60.0),
+                                     (60.0, -20.0), (64.0, -20.0)])
+def test_small_probabilities(top, low, E):
+    """Experts far below a token's largest logit keep their probability, and their gradient, down to
+    e^-71, wherever the largest lies."""
+    _announce(f"logits {top} and {low}, E={E}")
+    T = 70
+    c = make(T, E, 2, None, seed=24, lost=0.0, masked=0.0)
+    l = np.full((T, E), low)
+    l[np.arange(T), np.arange(T) % 3] = top
+    l[np.arange(T), 3 + np.arange(T) % 4] = 0.5 * (top + low)
+    with_logits(c, l)
+    counts, tokens = check_losses(c)
+    d = check_gradient(c, counts, tokens, [0.7 * T, 0.2 * T], gates=False)
+    assert np.all(d[np.arange(T), 3 + np.arange(T) % 4] != 0) and np.all(d[:, 7] != 0)
