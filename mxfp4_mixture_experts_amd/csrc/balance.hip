@@ -93,9 +93,11 @@ __device__ __forceinline__ void load_counts(const int32_t* row, int e0, int E, i
 // exponential passes fp32's range, and a sum of them is at least e^-16, so that
 // the only probabilities which vanish with their exponentials lie under e^-71.
 // (Router logits lie there: 27.5 -> 25.3 us for the balance of 65536 x 512.)
-// Otherwise m is the row's maximum, taken off before the product with log2 e:
-// rounded apart, m log2 e would be off by far more than an exponent's range where
-// m is large.
+// Otherwise the maxima are looked for, and m is 0 still for a token whose own lies
+// there -- the same bits whatever the tokens beside it in the wave hold -- and the
+// row's maximum for another, taken off before the product with log2 e: rounded
+// apart, m log2 e would be off by far more than an exponent's range where m is
+// large.
 constexpr float kNear = 16.f;
 template <int L>
 __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
@@ -110,6 +112,7 @@ __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
     return;
   }
   m = group_max<L>(top);
+  if (m >= -kNear && m <= kNear) m = 0.f;
   const float off = m > -INFINITY ? m : 0.f;
 #pragma unroll
   for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_exp2f((v[j] - off) * kLog2e);

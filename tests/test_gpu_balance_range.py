@@ -136,3 +136,50 @@ def test_small_probabilities(top, low, E):
     counts, tokens = check_losses(c)
     d = check_gradient(c, counts, tokens, [0.7 * T, 0.2 * T], gates=False)
     assert np.all(d[np.arange(T), 3 + np.arange(T) % 4] != 0) and np.all(d[:, 7] != 0)
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+def test_other_tokens_leave_the_bits(E):
+    """What unrouted tokens and padding hold -- logits of any size, NaN, infinities -- changes no bit of
+    the losses or of a counted token's gradient."""
+    _announce(f"what other tokens hold, E={E}")
+    T = 151
+    r = np.random.default_rng(E)
+    c = make(T, E, 4, [5, 60, 60, 140], seed=22, lost=0.0, masked=0.0)
+    other = np.zeros(T, bool)
+    other[r.choice(T, 40, replace=False)] = True
+    c["ids"][other] = -1
+    other[:5] = other[140:] = True                        # padding, routed or not
+    seen = []
+    for held in (None, 0.0, 65.0, -300.0, 1e30, -np.inf, np.inf, np.nan):
+        l = c["l"].copy()
+        if held is not None:
+            l[other] = held
+            l[other, 1] = -2.0
+        d = dict(c, logits=torch.from_numpy(l.astype(np.float32)).to(torch.bfloat16).cuda())
+        counts, tokens, losses = run_balance(d)
+        grads = [logit_gradient(d, counts, tokens, [0.7 * T, 0.2 * T], gates) for gates in (True, False)]
+        seen.append([counts, tokens, losses, *grads])
+        assert int(tokens[-2]) == int((~other).sum())
+        for got, want in zip(seen[-1], seen[0]):
+            assert torch.equal(got, want), held
+
+
+def test_a_row_does_not_depend_on_its_place():
+    """One token's gradient through the z loss: the same bits beside small and beside large logits, at
+    any place of a wave."""
+    _announce("one row at several places")
+    for E in EXPERTS:
+        r = np.random.default_rng(E + 1)
+        row = r.normal(size=E) * 3
+        T, k = 70, 2
+        rows = []
+        for place, around in ((0, 1.0), (17, 1.0), (17, 200.0), (69, 200.0)):
+            c = make(T, E, k, None, seed=23, lost=0.0, masked=0.0)
+            l = r.normal(size=(T, E)) * around
+            l[place] = row
+            with_logits(c, l)
+            counts, tokens, _ = run_balance(c)
+            assert int(tokens[-2]) == T
+            rows.append(logit_gradient(c, counts, tokens, [0.0, 0.2 * T], gates=False)[place])
+        assert all(torch.equal(x, rows[0]) for x in rows)
