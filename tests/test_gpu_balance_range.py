@@ -183,3 +183,105 @@ def test_a_row_does_not_depend_on_its_place():
             assert int(tokens[-2]) == T
             rows.append(logit_gradient(c, counts, tokens, [0.0, 0.2 * T], gates=False)[place])
         assert all(torch.equal(x, rows[0]) for x in rows)
+
+
+def _packed(T, E, k, seq, seed):
+    """A case on the device without masked experts, and buffers for its calls."""
+    c = make(T, E, k, seq, seed=seed, lost=0.0, masked=0.0)
+    S = len(seq) - 1
+    buf = dict(counts=torch.empty((S, E), dtype=torch.int32, device="cuda"),
+               tokens=torch.empty((S + 2,), dtype=torch.int32, device="cuda"), losses=torch.empty(2, device="cuda"),
+               ws=torch.empty((B.moe_balance_workspace_size(T, E, S),), dtype=torch.uint8, device="cuda"),
+               ids=cuda(c["ids"]), seq=cuda(c["seq"]), dl=cuda(np.array([0.7 * T, 0.2 * T], np.float32)),
+               dlogits=torch.full((T, E), float("nan"), device="cuda"))
+
+    def balance():
+        B.moe_balance(c["logits"], buf["ids"], T, E, k, buf["counts"], buf["tokens"], buf["losses"],
+                      seq_offsets=buf["seq"], S=S, workspace=buf["ws"])
+
+    def gradient():
+        B.moe_route_backward(c["logits"], buf["ids"], None, None, T, E, k, buf["dlogits"], seq_offsets=buf["seq"],
+                             S=S, counts=buf["counts"], tokens=buf["tokens"], dlosses=buf["dl"])
+    return c, buf, balance, gradient
+
+
+def _least_ms(call, times=5):
+    best = float("inf")
+    for _ in range(times):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("E", [8, 32, 512])
+@pytest.mark.parametrize("T,used", [(300, [0, 20, 150, 290]), (300, [0, 300]), (40, [0, 1, 2, 3, 30])])
+def test_runs_of_empty_sequences(T, used, E):
+    """Thousands of equal offsets in front of, inside and behind a chunk of tokens: the values of the
+    used sequences alone."""
+    _announce(f"runs of empty sequences, T={T} E={E} {used}")
+    k, run = 2, 3000
+    seq, at = [], []
+    for i, o in enumerate(used):
+        seq += [o] * (run if i < len(used) - 1 else 1 + run)
+        at.append(len(seq) - 1)
+    c, buf, balance, gradient = _packed(T, E, k, seq, 25)
+    balance()
+    gradient()
+    dense = dict(c, seq=np.asarray(used, np.int32))
+    wc, wt, wl = O.balance(c["l"], c["ids"], dense["seq"])
+    S = len(used) - 1
+    np.testing.assert_array_equal(buf["counts"][at[:-1]].cpu().numpy(), wc)
+    assert int(buf["counts"].sum()) == int(wc.sum())
+    np.testing.assert_array_equal(buf["tokens"][at[:-1]].cpu().numpy(), wt[:S])
+    assert buf["tokens"][-2:].tolist() == wt[-2:].tolist()
+    got = buf["losses"].double().cpu().numpy()
+    assert abs(got[0] - wl[0]) <= 2.0 ** -15 * wl[0] and abs(got[1] - wl[1]) <= 2.0 ** -15 * wl[1] + 2.0 ** -16
+    tokens = torch.cat([buf["tokens"][at[:-1]], buf["tokens"][-2:]]).contiguous()
+    counts = buf["counts"][at[:-1]].contiguous()
+    assert torch.equal(logit_gradient(dense, counts, tokens, buf["dl"].cpu().numpy(), gates=False), buf["dlogits"])
+    check_gradient(dense, counts, tokens, buf["dl"].cpu().numpy().astype(np.float64), gates=False)
+
+
+def test_runs_of_empty_sequences_cost_no_walk():
+    """65535 empty sequences in the middle of the tokens take about the time that they take behind
+    them, where no token passes them (looking at them one by one: over 20 times that)."""
+    _announce("time of empty sequences")
+    T, E, k, run = 64, 8, 2, 65535
+    inside = [0] + [33] * (run + 1) + [T]
+    behind = [0, 33] + [T] * (run + 1)
+    times = []
+    for seq in (inside, behind):
+        _, _, balance, gradient = _packed(T, E, k, seq, 26)
+        balance()
+        times.append((_least_ms(balance), _least_ms(gradient)))
+    print(f"[case] ms inside {times[0]}, behind {times[1]}", flush=True)
+    assert times[0][0] < 4 * times[1][0] and times[0][1] < 4 * times[1][1] + 0.1, times
+
+
+@pytest.mark.parametrize("E", [8, 512])
+def test_most_sequences(E):
+    """MOE_MAX_SEQUENCES of them, all but a few empty."""
+    _announce(f"2^20 sequences, E={E}")
+    T, k, S = 300, 2, B.MOE_MAX_SEQUENCES
+    seq = np.zeros(S + 1, np.int32)
+    used = [0, 5, 170, 290]
+    at = [3, S // 2, S - 9]                     # the used sequences
+    for i, s in enumerate(at):
+        seq[s + 1:] = used[i + 1]
+    c, buf, balance, gradient = _packed(T, E, k, seq, 27)
+    balance()
+    gradient()
+    wc, wt, wl = O.balance(c["l"], c["ids"], np.asarray(used))
+    np.testing.assert_array_equal(buf["counts"][at].cpu().numpy(), wc)
+    assert int(buf["counts"].sum(dtype=torch.int64)) == int(wc.sum())
+    assert buf["tokens"][at].tolist() == wt[:3].tolist() and buf["tokens"][-2:].tolist() == wt[-2:].tolist()
+    got = buf["losses"].double().cpu().numpy()
+    assert abs(got[0] - wl[0]) <= 2.0 ** -15 * wl[0] and abs(got[1] - wl[1]) <= 2.0 ** -15 * wl[1] + 2.0 ** -16
+    dense = dict(c, seq=np.asarray(used, np.int32))
+    tokens = torch.cat([buf["tokens"][at], buf["tokens"][-2:]]).contiguous()
+    assert torch.equal(logit_gradient(dense, buf["counts"][at].contiguous(), tokens, buf["dl"].cpu().numpy(),
+                                      gates=False), buf["dlogits"])
