@@ -430,6 +430,14 @@ def _arg(t: Optional[torch.Tensor], name: str, dtypes, count: int, device: int):
     raise ValueError(f"{name} holds {t.numel()} elements, {count} needed")
 
 
+def _sizes32(*sizes: int):
+    """Refuse a size that does not fit the C int that it is passed as: the call would see its lower
+    half.  (A call looks here only where a size has a bit from the 31st on.)"""
+    for v in sizes:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise MXFP4Error(1, f"size {v} does not fit an int32")
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     device = t.get_device()
     if device < 0:
@@ -475,6 +483,8 @@ def moe_norm(x, w, T: int, N: int, xn, eps: float = 1e-5, stream=None):
     of x [T,N] bf16 or f32; w [N] bf16."""
     lib = load_library()
     T, N = int(T), int(N)
+    if T >> 31 or N >> 31:
+        _sizes32(T, N)
     dev = _device_of(xn, "xn")
     xt = _dtype(x, "x")
     _run(lib.moe_norm, dev, stream, _arg(x, "x", _ELEMENTS[xt], T * N, dev), xt,
@@ -482,7 +492,9 @@ def moe_norm(x, w, T: int, N: int, xn, eps: float = 1e-5, stream=None):
 
 
 def moe_norm_backward_workspace_size(T: int, N: int) -> int:
-    return _size(load_library().moe_norm_backward_workspace_size(int(T), int(N)), "moe_norm_backward")
+    T, N = int(T), int(N)
+    _sizes32(T, N)
+    return _size(load_library().moe_norm_backward_workspace_size(T, N), "moe_norm_backward")
 
 
 def moe_norm_backward(dxn, x, w, T: int, N: int, dx, dw=None, dres=None, eps: float = 1e-5, workspace=None,
@@ -492,6 +504,8 @@ def moe_norm_backward(dxn, x, w, T: int, N: int, dx, dw=None, dres=None, eps: fl
     device tensor of at least moe_norm_backward_workspace_size(T, N) bytes, for dw."""
     lib = load_library()
     T, N = int(T), int(N)
+    if T >> 31 or N >> 31:
+        _sizes32(T, N)
     dev = _device_of(dx, "dx")
     ws, nbytes = _workspace(workspace, dev)
     xt = _dtype(x, "x")
@@ -509,6 +523,8 @@ def moe_combine_norm(proj, gates, T: int, k: int, N: int, x, x_out, w_post=None,
     norm into xn [T,N] bf16."""
     lib = load_library()
     T, k, N = int(T), int(k), int(N)
+    if T >> 31 or k >> 31 or N >> 31:
+        _sizes32(T, k, N)
     dev = _device_of(x_out, "x_out")
     pt, xt = _dtype(proj, "proj"), _dtype(x, "x")
     _run(lib.moe_combine_norm, dev, stream, _arg(proj, "proj", _ELEMENTS[pt], T * k * N, dev), pt,
@@ -518,7 +534,9 @@ def moe_combine_norm(proj, gates, T: int, k: int, N: int, x, x_out, w_post=None,
 
 
 def moe_combine_norm_backward_workspace_size(T: int, N: int) -> int:
-    return _size(load_library().moe_combine_norm_backward_workspace_size(int(T), int(N)), "moe_combine_norm_backward")
+    T, N = int(T), int(N)
+    _sizes32(T, N)
+    return _size(load_library().moe_combine_norm_backward_workspace_size(T, N), "moe_combine_norm_backward")
 
 
 def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=None, dproj=None, dgates=None,
@@ -531,6 +549,8 @@ def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=No
     moe_combine_norm_backward_workspace_size(T, N) bytes, for the weights' gradients."""
     lib = load_library()
     T, k, N = int(T), int(k), int(N)
+    if T >> 31 or k >> 31 or N >> 31:
+        _sizes32(T, k, N)
     dev = _device_of(proj, "proj")
     stream_like = next((t for t in (dx_out, x_out, dx) if t is not None), None)
     if stream_like is None:
@@ -548,7 +568,9 @@ def moe_combine_norm_backward(dx_out, proj, gates, T: int, k: int, N: int, dx=No
 
 
 def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
-    return _size(load_library().moe_balance_workspace_size(int(T), int(E), int(S)), "moe_balance")
+    T, E, S = int(T), int(E), int(S)
+    _sizes32(T, E, S)
+    return _size(load_library().moe_balance_workspace_size(T, E, S), "moe_balance")
 
 
 def moe_balance(logits, topk_ids, T: int, E: int, k: int, counts, tokens, losses, seq_offsets=None, S: int = 1,
@@ -560,6 +582,8 @@ def moe_balance(logits, topk_ids, T: int, E: int, k: int, counts, tokens, losses
     bytes."""
     lib = load_library()
     T, E, k, S = int(T), int(E), int(k), int(S)
+    if T >> 31 or E >> 31 or k >> 31 or S >> 31:
+        _sizes32(T, E, k, S)
     dev = _device_of(counts, "counts")
     ws, nbytes = _workspace(workspace, dev)
     _run(lib.moe_balance, dev, stream, _arg(logits, "logits", _BF16, T * E, dev),
@@ -576,6 +600,8 @@ def moe_route_backward(logits, topk_ids, gates, dgates, T: int, E: int, k: int, 
     moe_balance)."""
     lib = load_library()
     T, E, k, S = int(T), int(E), int(k), int(S)
+    if T >> 31 or E >> 31 or k >> 31 or S >> 31:
+        _sizes32(T, E, k, S)
     dev = _device_of(dlogits, "dlogits")
     dt = _dtype(dlogits, "dlogits")
     _run(lib.moe_route_backward, dev, stream, _arg(logits, "logits", _BF16, T * E, dev),
