@@ -285,3 +285,70 @@ def test_most_sequences(E):
     tokens = torch.cat([buf["tokens"][at], buf["tokens"][-2:]]).contiguous()
     assert torch.equal(logit_gradient(dense, buf["counts"][at].contiguous(), tokens, buf["dl"].cpu().numpy(),
                                       gates=False), buf["dlogits"])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [5, 8, 33, 64, 512])
+def test_tensors_off_16_bytes(E, dtype):
+    """Tensors that begin between 16-byte borders: the bits of aligned ones, and nothing before or
+    behind the outputs is written."""
+    _announce(f"balance, storage offsets, E={E} {dtype}")
+    T, k = 77, 3
+    c = make(T, E, k, [2, 30, 30, 75], seed=28)
+    dl = cuda(np.array([0.7 * T, 0.2 * T], np.float32))
+    args = [c["logits"], cuda(c["ids"]), cuda(c["gates"]), cuda(c["dgates"]), cuda(c["seq"]), dl]
+
+    def shifted(t, by):
+        flat = torch.full((t.numel() + 16,), 7, dtype=t.dtype, device="cuda")
+        flat[by:by + t.numel()] = t.reshape(-1)
+        return flat, flat[by:by + t.numel()].view(t.shape)
+
+    def run(by):
+        logits, ids, gates, dgates, seq, dlosses = (shifted(t, by)[1] for t in args)
+        outs = [shifted(torch.zeros(shape, dtype=d, device="cuda"), by)
+                for shape, d in (((3, E), torch.int32), ((5,), torch.int32), ((2,), torch.float32), ((T, E), dtype))]
+        (_, counts), (_, tokens), (_, losses), (_, dlogits) = outs
+        B.moe_balance(logits, ids, T, E, k, counts, tokens, losses, seq_offsets=seq, S=3,
+                      workspace=torch.full((B.moe_balance_workspace_size(T, E, 3),), 255, dtype=torch.uint8, device="cuda"))
+        B.moe_route_backward(logits, ids, gates, dgates, T, E, k, dlogits, seq_offsets=seq, S=3, counts=counts,
+                             tokens=tokens, dlosses=dlosses)
+        for flat, view in outs:
+            assert bool((flat[:by] == 7).all()) and bool((flat[by + view.numel():] == 7).all())
+        return [view for _, view in outs]
+
+    want = run(0)
+    for by in (1, 2, 3):
+        for got, w in zip(run(by), want):
+            assert torch.equal(got, w), by
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured balances of different sizes on one workspace, replayed in turn: each replay gives the
+    eager result."""
+    _announce("two graphs, one workspace")
+    sizes = [(700, 32, [0, 100, 100, 650]), (5000, 512, list(range(0, 5001, 25))), (64, 8, [0, 64])]
+    ws = torch.full((max(B.moe_balance_workspace_size(T, E, len(seq) - 1) for T, E, seq in sizes),), 255,
+                    dtype=torch.uint8, device="cuda")
+    graphs = []
+    for i, (T, E, seq) in enumerate(sizes):
+        c, buf, _, _ = _packed(T, E, 2, seq, 30 + i)
+        outs = [buf["counts"], buf["tokens"], buf["losses"]]
+
+        def call(c=c, buf=buf, T=T, E=E, S=len(seq) - 1):
+            B.moe_balance(c["logits"], buf["ids"], T, E, 2, buf["counts"], buf["tokens"], buf["losses"],
+                          seq_offsets=buf["seq"], S=S, workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((g, outs, want, (c, buf)))     # a graph reads its inputs where they were captured
+    for turn in (0, 1, 2, 1, 0, 2, 0):
+        g, outs, want, _ = graphs[turn]
+        for o in outs:
+            o.fill_(-7)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want)), turn
