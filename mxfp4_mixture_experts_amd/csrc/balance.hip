@@ -519,21 +519,22 @@ __global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward
     bool live = true;
     if constexpr (LOSSES) {
       settle_logits<L>(l_next, e0, E, v);
-      if (seq && t >= s_end && s < S) {
-        s++;
-        s_end = s < S ? seq[s + 1] : T;
-        if (t >= s_end && s < S) {
-          // behind more than one border: the first sequence that ends beyond t, by
-          // halving, since any number of empty ones may lie between (65535: 11 us for the
-          // call; one after the other 6.1 ms)
+      for (int steps = 0; seq && t >= s_end && s < S; steps++) {
+        if (steps < 4) {
+          s++;
+        } else {
+          // the first sequence that ends beyond t, by halving, since any number of
+          // empty ones may lie between (65535: 11 us for the call; one after the
+          // other 6.1 ms).  Up to four borders are quicker passed one by one
+          // (halving from the second: 5.6 us for 5540 x 38 in 11 sequences, so 5.5).
           int lo = s, hi = S;
           while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             (seq[mid + 1] <= t ? lo : hi) = mid;
           }
           s = hi;
-          s_end = s < S ? seq[s + 1] : T;
         }
+        s_end = s < S ? seq[s + 1] : T;
       }
       live = s >= 0 && s < S;
     }
