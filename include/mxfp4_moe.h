@@ -473,8 +473,8 @@ int moe_combine(const float* proj, const float* gates, int T, int k, int N, floa
  *   xn      [T, N] bf16 out: xn[t, n] = bf16(x[t, n] * r * w[n]) with
  *           r = (sum_n x[t, n]^2 / N + eps)^(-1/2), in fp32, rounded once.  (A
  *           row whose sum of squares passes fp32's range gets r = 0.)
- * Pointers need the alignment of their elements only.  One kernel launch; T = 0
- * returns MXFP4_OK and enqueues nothing.
+ * Pointers need the alignment of their elements only.  One kernel launch for every
+ * 2^22 rows; T = 0 returns MXFP4_OK and enqueues nothing.
  */
 int moe_norm(const void* x, int x_dtype, const uint16_t* w, int T, int N, float eps, uint16_t* xn, void* stream);
 
@@ -519,8 +519,8 @@ int moe_norm_backward(const uint16_t* dxn, const void* x, int x_dtype, const uin
  *   w_next  [N] bf16, and
  *   xn      [T, N] bf16 out, or both NULL: the norm of x_out as stored, the bits
  *           that moe_norm(x_out, w_next) gives.
- * A token with no routed slot keeps x_out = x.  One kernel launch; T = 0 returns
- * MXFP4_OK and enqueues nothing.
+ * A token with no routed slot keeps x_out = x.  One kernel launch for every 2^22
+ * tokens; T = 0 returns MXFP4_OK and enqueues nothing.
  */
 int moe_combine_norm(const void* proj, int proj_dtype, const float* gates, int T, int k, int N, const uint16_t* w_post,
                      const void* x, int x_dtype, float scale, float eps, void* x_out, const uint16_t* w_next,
@@ -588,7 +588,8 @@ size_t moe_balance_workspace_size(int T, int E, int S);
  *   losses  [2] fp32 out: with p the softmax over all E logits,
  *           losses[0] = (1 / S') sum_s E sum_e counts[s, e] / (k n_s) * mean p[., e],
  *           losses[1] = the mean over the counted tokens of logsumexp(logits)^2;
- *           0 where nothing is counted.  fp32, summed in a fixed order.
+ *           0 where nothing is counted.  fp32, summed in a fixed order; a probability
+ *           under e^-71 may count as 0 (in the gradient as well).
  *   workspace, workspace_bytes: at least moe_balance_workspace_size(T, E, S) bytes,
  *           16-byte aligned.  Calls that share a workspace must be ordered on one
  *           stream.

@@ -166,10 +166,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int t) {
 // Workspace of a balance call: a workgroup's chunk of tokens is cut at the
 // sequences' borders into pieces; piece (chunk c, sequence s) has the slot
 // c + s (distinct, since both only rise along the tokens).  A workgroup takes
-// its pieces one after another, about 0.7 us each, so chunks are no longer than
+// its pieces one after another, 1.2 to 2 us each, so chunks are no longer than
 // the mean sequence, from 64 tokens (which fill the chip from 16384 tokens on)
 // down to 4; beyond 32768 tokens they grow, so that there are never more than
-// 512 to add up.
+// 512 to add up.  Lengths far from their mean are what this does not serve: one
+// sequence of 4032 beside 64 of one token (4096 x 32) takes 86 us, of 64512 beside
+// 1024 of one (65536 x 512) 191 us, where 64 of random lengths take 15 and 23 us.
 constexpr int kSumCols = 64;  // experts per workgroup of the second launch
 struct BalanceLayout {
   int chunk, chunks, slots, blocks;
@@ -195,10 +197,10 @@ BalanceLayout balance_layout(int T, int E, int S) {
 
 // The threads of a piece's workgroup: more where a wave holds few tokens.
 //
-// What bounds the first launch: vector instructions (87 a token of 512 experts,
-// 10 of the 17 us for 65536 of them; 67 MB are 13 us at the rate of a copy) and
-// the latency of a workgroup's first loads and last sums; for 4096 tokens of 32
-// experts (4 us) these alone.
+// What bounds the first launch: vector instructions (83 a token of 512 experts:
+// at four cycles each about 9 of the 18 us for 65536 of them; 67 MB are 13 us at the
+// rate of a copy) and the latency of a workgroup's first loads and last sums; for
+// 4096 tokens of 32 experts (4 us) these alone.
 template <int L>
 constexpr int kPieceThreads = L >= 16 ? 1024 : 256;
 
@@ -468,8 +470,9 @@ constexpr int kRouteChunk = L >= 32 ? 8 * kRouteThreads / L : kRouteThreads / L 
 // further rounds, so the order of their sum is fixed.  (Comparing: 89 us for
 // 65536 tokens of 512 experts with 8 slots; this way 46.)
 //
-// What bounds it: 180 vector instructions a token of 512 experts, about 21 of
-// the 31 us for 65536 of them, where 141 MB are 26 us at the rate of a copy.
+// What bounds it: 181 vector instructions a token of 512 experts, at four cycles
+// each about 19 of the 31 us for 65536 of them, where 141 MB are 26 us at the rate of
+// a copy.  The gates' part alone (65536 x 512 x 8, bf16 out) takes 14.8 us, 5.0 TB/s.
 template <int L, typename O, bool LOSSES>
 __global__ __launch_bounds__(kRouteThreads, L == 64 ? 8 : 1) void route_backward_kernel(
     const uint16_t* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ gates,
@@ -677,9 +680,10 @@ hipError_t launch_balance(const uint16_t* logits, const int32_t* ids, int T, int
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Many workgroups wait on each other's arrivals for longer than a launch
-  // takes: 65536 x 512 in 37 sequences, 296 workgroups, 25.0 us with arrivals and
-  // 23.3 with a third launch; 4096 x 32 in 8 sequences 9.5 and 10.0, 64 x 32 in
-  // 64 sequences 11.7 and 12.6 (and about 3.5 us less for the host).
+  // takes.  By workgroups, with arrivals and with a third launch: 4096 x 32, 8: 10.8
+  // and 11.2 us, 64: 14.8 and 14.9, 128: 15.3 and 15.1, 192: 15.3 and 14.0, 512: 18.0 and
+  // 14.1; 65536 x 512, 64: 23.1 and 24.4, 128: 22.1 and 22.5, 192: 23.2 and 22.0, 512:
+  // 27.1 and 23.1.
   const bool counted = (long long)S * b.blocks <= kArrivals;
   hipLaunchKernelGGL(balance_sequences_kernel, dim3(S, b.blocks), dim3(kSumThreads), 0, stream, part_p, part_c,
                      part_zn, T, E, k, seq, S, b.chunk, counts, tokens, losses, part, seq_z,

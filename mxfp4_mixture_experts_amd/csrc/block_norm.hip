@@ -302,8 +302,8 @@ template <int CH>
 constexpr bool kAhead = CH <= 2;
 
 // Gradients of moe_norm.  dx may be dres itself.  8192 rows of 2880 (189 MB): 36
-// us, 5.3 TB/s, and 3 us for the column sums' launch; with 1000 rows of fp32 (29
-// MB, 9 + 3 us) the round trips of a workgroup's two rows one after the other.
+// us, 5.3 TB/s, and 5 us for the column sums' launch; with 1000 rows of fp32 (29
+// MB, 10 + 4 us) the round trips of a workgroup's two rows one after the other.
 //
 // A team's next row is fetched ahead of this row's stores: loads and stores
 // complete in the order of their issue, so a load behind the stores would wait
@@ -390,9 +390,12 @@ __global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backwar
 // registers of this row as soon as these have been used, ahead of this row's
 // stores (as in norm_backward_kernel); so are its gates.
 //
-// 8192 x 4 x 2880 (944 MB): 181 us, 5.2 TB/s, and 5 us for the column sums; a
-// shorter batch (777 x 3 x 1023, 16 MB, 8 + 3 us) is bound by one row's chain of
-// loads, three sums over the team and stores.
+// 8192 x 4 x 2880 (944 MB): 188 us, 5.0 TB/s, and 5 us for the column sums; a
+// shorter batch (777 x 3 x 1023, 16 MB, 9.2 + 2.8 us) is bound by one row's chain of
+// loads, three sums over the team and stores.  Where the rows are read again they
+// come one slot at a time (2048 x 16 x 2880, fp32 proj: 244 us, 3.3 TB/s of what it
+// has to move; 2048 x 8 x 2880, held: 102 us, 4.2 TB/s), and four chunks a thread
+// spill 233 to 308 registers (500 x 2 x 16000 bf16: 119 us, 1.1 TB/s).
 //
 // The threads of a workgroup: as many as the registers allow (three waves on a
 // SIMD, two with eight slots' rows or more than one chunk a thread).

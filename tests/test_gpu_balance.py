@@ -1,13 +1,16 @@
 """GPU parity of the routing's balance loss, per-expert counts and logit gradients (moe_balance,
 moe_route_backward) through the C ABI, against the float64 oracle.
 
-Tolerances.  Counts and tokens are equal.  A probability's exponent (l - m) is off by 2^-24 of itself
-twice (the difference, its product with log2 e); for |l - m| <= 40 that is 2^-18 of p, and the exponential,
-the sum and the division add under 32 roundings (2^-19): 2^-17 of p; what lies below e^-40 is under
-1e-17 of the row.  The sums over tokens add at most T / 1024 + 80 + 64 values of one sign in any chain,
-and a loss a few dozen roundings more: 2^-16 of the loss for T <= 70000 (144 + 68 roundings: 2^-16.2).
-z = m + log(sum): under 2^-21 (|m| + |z| + 1) each.  A gradient's terms carry 2^-17 from p three times
-and under 64 roundings: 2^-15 of their magnitudes, then the output's own rounding.
+Tolerances, in roundings of u = 2^-24.  Counts and tokens are equal.  A probability's exponent x (l - m, or
+l itself where the row's largest logit lies in [-16, 16]) is off by the difference, its product with
+log2 e and that constant: 2.3 u |x| of p, 92 u for |x| <= 40, and the exponential, the sum and the reciprocal
+add under 32 u: 2^-17 of p; what lies further down is under 1e-17 of the row (e^-40).  A loss adds, in any
+chain, the tokens of a lane (a chunk's, at most max(64, T / 512), over at least 16 groups: 9), 6 + 16 over
+lanes and waves, at most 512 / 16 + 1 pieces, 16 + 6 and the sequences' few dozen: under 110 u beside p's
+128: 2^-16 for T <= 70000.  (test_long_batch: chunks grow from 32768 tokens on, so that there are at most
+512.)  z = m + log(sum): 17 u for the sum and 4 u (|m| + |z|): under 2^-21 (|m| + |z| + 1) + 9 u each, the
+latter within the loss's 2^-16 z^2.  A gradient's terms carry 2^-17 from p three times and under 64
+roundings: 2^-15 of their magnitudes, then the output's own rounding.
 """
 import numpy as np
 import pytest

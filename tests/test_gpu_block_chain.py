@@ -1,7 +1,10 @@
 """The operators around the expert block together, as they are used: a block's forward pass from the
 residual stream to the next block's input, its router's gradients, captured graphs, other streams
 and offsets past 32 bits.  Values against the float64 oracles stage by stage (tolerances as in
-test_gpu_block_norm.py and test_gpu_balance.py), otherwise bit for bit against the separate calls."""
+test_gpu_block_norm.py and test_gpu_balance.py), otherwise bit for bit against the separate calls.
+
+The balance past 32-bit offsets: a workgroup's chunk of 16385 tokens runs 16 at a time, so a lane adds
+1024 or 1025 values; with even logits over 512 experts these are 1 / 512 each and every sum is exact."""
 import numpy as np
 import pytest
 import torch

@@ -9,7 +9,9 @@ value.  Before it comes fp32 arithmetic, each operation within 2^-24 of its resu
  - a gradient's terms (G, dh) pass two such row sums and under 64 more operations: 2^-17 of the sum of
    their magnitudes, which the oracle carries along (2^-16 behind the output norm, where the rounding
    of h moves r as well: the oracle's magnitudes hold that factor);
- - the weights' sums add T / 512 + 1 rows in a workgroup and at most 32 + 16 sums of workgroups.
+ - the weights' sums add a team's rows (one where T <= 256 times the teams of a workgroup), the
+   workgroup's teams (at most T / 256 + 1) and 4 + 2 + 16 sums of workgroups: under T / 512 + 64
+   roundings at the sizes here.
 """
 import numpy as np
 import pytest
