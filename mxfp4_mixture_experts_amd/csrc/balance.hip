@@ -92,12 +92,13 @@ __device__ __forceinline__ void load_counts(const int32_t* row, int e0, int E, i
 // logit in [-kNear, kNear], m is 0 and no maximum over the lanes is needed: no
 // exponential passes fp32's range, and a sum of them is at least e^-16, so that
 // the only probabilities which vanish with their exponentials lie under e^-71.
-// (Router logits lie there: 27.5 -> 25.3 us for the balance of 65536 x 512.)
-// Otherwise the maxima are looked for, and m is 0 still for a token whose own lies
-// there -- the same bits whatever the tokens beside it in the wave hold -- and the
-// row's maximum for another, taken off before the product with log2 e: rounded
-// apart, m log2 e would be off by far more than an exponent's range where m is
-// large.
+// (Router logits lie there.  65536 x 512: balance 22.5 us, gradient 31.6; with the
+// maxima looked for 24.4 and 32.3.  A wider range is quicker for larger logits, but
+// the product's rounding grows with them: 2^-20 of p at 16, 2^-18 at 64.)  Otherwise
+// the maxima are looked for, and m is 0 still for a token whose own lies there --
+// the same bits whatever the tokens beside it in the wave hold -- and the row's
+// maximum for another, taken off before the product with log2 e: rounded apart,
+// m log2 e would be off by far more than an exponent's range where m is large.
 constexpr float kNear = 16.f;
 template <int L>
 __device__ __forceinline__ void group_exp(float (&v)[8], float& m) {
