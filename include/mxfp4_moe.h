@@ -489,7 +489,8 @@ size_t moe_norm_backward_workspace_size(int T, int N);
  *   dres    [T, N] of x's type, or NULL (none): the gradient that reaches x past
  *           the norm, along the residual stream.
  *   dx      [T, N] of x's type, out; may be dres.  With x^ = x * r:
- *           dx = dres + r * (dxn w - x^ * sum_n(dxn w x^) / N), in fp32, rounded once.
+ *           dx = dres + r * (dxn w - x^ * sum_n(dxn w x^) / N), in fp32, rounded once.  (A row
+ *           with r = 0, as above: dres.)
  *   dw      [N] fp32 out, or NULL: dw[n] = sum_t dxn[t, n] * x^[t, n], added in a
  *           fixed order.  T = 0 writes zeros.
  *   workspace, workspace_bytes: at least moe_norm_backward_workspace_size(T, N)

@@ -133,6 +133,10 @@ __device__ __forceinline__ void row_sum(const Team<PART>& team, float (&v)[M], f
 __device__ __forceinline__ float rms_scale(float sum, float inv_n, float eps) {
   return rsqrtf(fmaf(sum, inv_n, eps));
 }
+// sum_n(d w v^) / N from sum_n(d w v).  Where the squares have passed fp32's
+// range r is 0 and v^ with it, and the sum of the products, which may have passed
+// it as well, is not taken times 0.
+__device__ __forceinline__ float unit_mean(float sum, float inv_n, float r) { return r == 0.f ? 0.f : sum * inv_n * r; }
 
 // moe_norm.  Bound by HBM at length: 8192 fp32 rows of 2880 (142 MB) take 26 us,
 // 5.4 TB/s, as a copy does; one row takes 2.0 us, the launch and one round trip.
@@ -367,7 +371,7 @@ __global__ __launch_bounds__(CH == 1 ? kMaxThreads : kMaxTeam) void norm_backwar
       if (t0 + step < T) fetch(t + step);
     row_sum(team, s, red[parity]);
     const float r = rms_scale(s[0], inv_n, eps);
-    const float m = s[1] * inv_n * r;
+    const float m = unit_mean(s[1], inv_n, r);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
       float wv[8];
@@ -543,7 +547,7 @@ __global__ __launch_bounds__((kCombineThreads<CH, KR>)) void combine_norm_backwa
     if (shared_dgates && t0 >= step) store_dgates(t - step, parity ^ 1);
     if (a.dxn) {
       const float r = rms_scale(s[0], a.inv_n, a.eps);
-      const float m = s[1] * a.inv_n * r;
+      const float m = unit_mean(s[1], a.inv_n, r);
 #pragma unroll
       for (int c = 0; c < CH; c++) {
         float wv[8], xv[8], dv[8];

@@ -67,3 +67,36 @@ def test_combine_norm_backward_rows_without_a_norm(T, k, N, post, nxt):
     _announce(f"combine_norm_backward rows: T={T} k={k} N={N} post={post} next={nxt}")
     _, gates, proj, _, _, _ = make_block(T, k, N, torch.bfloat16, torch.float32, key=51)
     _backward(T, k, N, torch.bfloat16, torch.float32, post, nxt, gates, proj, key=51, check=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [5, 200, 2880, 8192, 9000])
+def test_rows_whose_squares_pass_the_range(N, dtype):
+    """A row whose sum of squares passes fp32's range has r = 0: its norm is 0, and its gradient what
+    came past the norm, whatever its products add up to."""
+    _announce(f"rows of huge values, N={N} {dtype}")
+    T = 4
+    r = _rng(52, N)
+    x, w = stream_rows(r, T, N, dtype), weights(r, N)
+    x[1] = 3e38
+    x[2, ::2], x[2, 1::2] = 1e38, -2e38
+    dxn, dres = dev(2.0 + r.random((T, N)), torch.bfloat16), dev(r.normal(size=(T, N)), dtype)
+    xn, dx, dw = nan_like((T, N), torch.bfloat16), nan_like((T, N), dtype), nan_like((N,), torch.float32)
+    B.moe_norm(x, w, T, N, xn, eps=EPS)
+    assert not xn[1:3].any()
+    B.moe_norm_backward(dxn, x, w, T, N, dx, dw, dres=dres, eps=EPS,
+                        workspace=workspace(B.moe_norm_backward_workspace_size(T, N)))
+    assert torch.equal(dx[1:3], dres[1:3])
+    others = [0, 3]
+    want, want_w, mag, mag_w = O.norm_backward(f64(dxn)[others], f64(x)[others], f64(w), EPS)
+    want, mag = want + f64(dres)[others], mag + np.abs(f64(dres)[others])
+    close(dx[others], want, HALF[dtype] * np.abs(want) + 2.0 ** -17 * mag + TINY, "dx")
+    close(dw, want_w, (2.0 ** -18 + 64 * 2.0 ** -24) * mag_w + TINY, "dw")
+    # the next norm of the block's output: the same gradient
+    got, got_w = nan_like((T, N), dtype), nan_like((N,), torch.float32)
+    proj = dev(r.normal(size=(T, 1, N)))
+    B.moe_combine_norm_backward(dres, proj, None, T, 1, N, dx=got, dxn=dxn, x_out=x, w_next=w, dw_next=got_w, eps=EPS,
+                                workspace=workspace(B.moe_combine_norm_backward_workspace_size(T, N)))
+    assert torch.equal(got[1:3], dres[1:3])
+    close(got[others], want, HALF[dtype] * np.abs(want) + 2.0 ** -17 * mag + TINY, "dx")
+    close(got_w, want_w, (2.0 ** -18 + 64 * 2.0 ** -24) * mag_w + TINY, "dw_next")
