@@ -448,6 +448,85 @@ int mxfp4_dequantize(const uint8_t* blocks, const uint8_t* scales, long long row
                      void* stream);
 
 /*
+ * MXFP4 quantisation, the inverse of mxfp4_dequantize.
+ * (README "MXFP4" for the format.)
+ *
+ *   x       [rows, K] bf16 or fp32 (x_dtype), 16-byte aligned.  0 <= rows, K >= 32 and
+ *           K % 32 == 0, rows * K < 2^46.
+ *   blocks  [rows, K/32, 16] u8 out, 16-byte aligned, and scales [rows, K/32] u8 out:
+ *           a block of 32 consecutive elements has the exponent e = floor(log2(max |x|)) - 2,
+ *           at least -127 (a block of zeros too), and the scale byte e + 127 (at most 252);
+ *           a code is the E2M1 value nearest to x * 2^-e, ties to the even code,
+ *           magnitudes above 6 to 6; the sign is kept, of a zero too.  A block with a
+ *           NaN or an infinity gets scale byte 255 (E8M0's NaN) and zero codes.
+ *   values  [rows, K] bf16 out, 16-byte aligned, or NULL: what blocks and scales stand
+ *           for (exact; NaN for the blocks with byte 255), as a training step wants it
+ *           for the straight-through gradient.
+ * One kernel launch; rows = 0 returns MXFP4_OK and enqueues nothing.
+ */
+int mxfp4_quantize(const void* x, int x_dtype, long long rows, int K, uint8_t* blocks, uint8_t* scales,
+                   uint16_t* values, void* stream);
+
+/*
+ * The same along the columns, for a product that contracts over the rows (a
+ * layer's gradients contract over its output width and over the tokens).
+ *
+ *   x       [R, C] bf16 or fp32 (x_dtype), aligned to its elements.  0 <= R <= 2^30,
+ *           R % 32 == 0, 0 <= C <= 2^21, R * C < 2^46.
+ *   blocks  [C, R/32, 16], scales [C, R/32], values [C, R] (or NULL): out, as
+ *           mxfp4_quantize of the transpose of x writes them.
+ * One kernel launch; R = 0 or C = 0 returns MXFP4_OK and enqueues nothing.
+ */
+int mxfp4_quantize_transposed(const void* x, int x_dtype, long long R, int C, uint8_t* blocks, uint8_t* scales,
+                              uint16_t* values, void* stream);
+
+/*
+ * The product of two MXFP4 matrices, a linear layer: out = a . b^T + bias.
+ *
+ *   a_blocks [M, K/32, 16], a_scales [M, K/32]: the activations, as mxfp4_quantize
+ *           writes them.  b_blocks [N, K/32, 16], b_scales [N, K/32]: the weights.
+ *           The blocks 16-byte aligned.  Scale bytes 0..254, and 255 for a NaN block: every
+ *           output whose row of a or b holds one is NaN.
+ *   bias    [N] bf16, or NULL.
+ *   0 <= M <= 2^30, 1 <= N <= 2^27, 32 <= K < 2^26, K % 32 == 0,
+ *           (M / 64 + 1) * ceil(N / 64) < 2^24.
+ *   out     [M, N] fp32 or bf16 (out_dtype), out: out[m, n] = bias[n] +
+ *           sum_j a[m, j] * b[n, j], exact products on the scaled-FP4 MFMA summed in
+ *           fp32 in a fixed order, rounded once.
+ * One kernel launch, no workspace; M = 0 returns MXFP4_OK and enqueues nothing.
+ */
+int mxfp4_matmul(const uint8_t* a_blocks, const uint8_t* a_scales, const uint8_t* b_blocks, const uint8_t* b_scales,
+                 const uint16_t* bias, int M, int N, int K, void* out, int out_dtype, void* stream);
+
+/*
+ * The routed expert projection of MXFP4 activations: mxfp4_expert_proj with x
+ * quantised (mxfp4_quantize), one MFMA per operand pair, no workspace.
+ *
+ *   blocks, scales, bias, E, N, K, T, k, expert_offsets, sorted_rows: as for
+ *           mxfp4_expert_proj; T * k <= 2^30, N <= 2^27, K < 2^26,
+ *           (T * k / 64 + E) * ceil(N / 64) < 2^24.  Scale byte 255: as for mxfp4_matmul.
+ *   x_blocks, x_scales: x_per_slot == 0: [T, K/32, 16] and [T, K/32], one input per
+ *           token; x_per_slot != 0: [T, k, K/32, 16] and [T, k, K/32].
+ *   out     [T, k, N] fp32 or bf16 (out_dtype), out.  Rows absent from the grouping
+ *           are not written.
+ * One kernel launch; T = 0 returns MXFP4_OK and enqueues nothing.
+ */
+int mxfp4_expert_matmul(const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias, int E, int N, int K,
+                        const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
+                        const int32_t* expert_offsets, const int32_t* sorted_rows, void* out, int out_dtype,
+                        void* stream);
+
+/*
+ * The same through the gated activation of mxfp4_expert_proj_swiglu: N even,
+ *   act     [T, k, N / 2] bf16 out: bf16(swiglu(p[t, s, 2 i], p[t, s, 2 i + 1])) of the
+ *           fp32 projection p.
+ */
+int mxfp4_expert_matmul_swiglu(const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias, int E, int N,
+                               int K, const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
+                               const int32_t* expert_offsets, const int32_t* sorted_rows, uint16_t* act,
+                               void* stream);
+
+/*
  * Gate-weighted combine of the k projections of each token.
  * (src/experts.linnet fn forward_topk: the sum over k in f32; fn down_bias_of:
  * the down bias carries the router weights -- here the bias is already inside

@@ -53,6 +53,11 @@ ENTRY_POINTS = (
     "moe_balance_workspace_size",
     "moe_balance",
     "moe_route_backward",
+    "mxfp4_quantize",
+    "mxfp4_quantize_transposed",
+    "mxfp4_matmul",
+    "mxfp4_expert_matmul",
+    "mxfp4_expert_matmul_swiglu",
 )
 
 _lib_handle = None
@@ -129,6 +134,15 @@ def load_library():
     lib.moe_balance_workspace_size.argtypes = [i32, i32, i32]
     lib.moe_balance.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]
     lib.moe_route_backward.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, i32, vp]
+    i64 = ctypes.c_longlong
+    lib.mxfp4_quantize.argtypes = [vp, i32, i64, i32, vp, vp, vp, vp]
+    lib.mxfp4_quantize_transposed.argtypes = [vp, i32, i64, i32, vp, vp, vp, vp]
+    lib.mxfp4_matmul.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp]
+    lib.mxfp4_expert_matmul.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp]
+    lib.mxfp4_expert_matmul_swiglu.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    for name in ("mxfp4_quantize", "mxfp4_quantize_transposed", "mxfp4_matmul", "mxfp4_expert_matmul",
+                 "mxfp4_expert_matmul_swiglu"):
+        getattr(lib, name).restype = i32
     for name in ("moe_norm", "moe_norm_backward", "moe_combine_norm", "moe_combine_norm_backward", "moe_balance",
                  "moe_route_backward"):
         getattr(lib, name).restype = i32
@@ -610,3 +624,93 @@ def moe_route_backward(logits, topk_ids, gates, dgates, T: int, E: int, k: int, 
          _arg(seq_offsets, "seq_offsets", _I32, S + 1, dev), S, _arg(counts, "counts", _I32, S * E, dev),
          _arg(tokens, "tokens", _I32, S + 2, dev), _arg(dlosses, "dlosses", _F32, 2, dev),
          _arg(dlogits, "dlogits", _ELEMENTS[dt], T * E, dev), dt)
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 quantisation and the products of two MXFP4 operands
+# ---------------------------------------------------------------------------
+
+
+def _quantize(entry, x, outer: int, inner: int, out_rows: int, out_k: int, blocks, scales, values, stream):
+    dev = _device_of(blocks, "blocks")
+    xt = _dtype(x, "x")
+    n = out_rows * out_k
+    _run(entry, dev, stream, _arg(x, "x", _ELEMENTS[xt], n, dev), xt, outer, inner,
+         _arg(blocks, "blocks", _U8, n // 2, dev), _arg(scales, "scales", _U8, n // 32, dev),
+         _arg(values, "values", _BF16, n, dev))
+
+
+def mxfp4_quantize(x, blocks, scales, values=None, stream=None):
+    """x [..., K] bf16 or f32 -> MXFP4 (mxfp4_quantize): blocks [..., K/32, 16] and scales [..., K/32]
+    u8, and what they stand for into values [..., K] bf16 (optional)."""
+    K = int(x.shape[-1])
+    n = x.numel()
+    rows = n // K if K else 0
+    if K >> 31:
+        _sizes32(K)
+    _quantize(load_library().mxfp4_quantize, x, rows, K, rows, K, blocks, scales, values, stream)
+
+
+def mxfp4_quantize_transposed(x, blocks, scales, values=None, stream=None):
+    """x [R, C] bf16 or f32 -> MXFP4 of its transpose, blocks along the rows of x
+    (mxfp4_quantize_transposed): blocks [C, R/32, 16] and scales [C, R/32] u8, values [C, R] bf16
+    (optional)."""
+    if x.dim() != 2:
+        raise ValueError(f"x must have two dimensions, has {x.dim()}")
+    R, C = x.shape
+    if C >> 31:
+        _sizes32(C)
+    _quantize(load_library().mxfp4_quantize_transposed, x, R, C, C, R, blocks, scales, values, stream)
+
+
+def mxfp4_matmul(a_blocks, a_scales, b_blocks, b_scales, M: int, N: int, K: int, out, bias=None, stream=None):
+    """out [M,N] f32 or bf16 = a . b^T + bias (mxfp4_matmul) of a [M,K] and b [N,K] in MXFP4 (blocks
+    [..., K/32, 16] and scales [..., K/32] u8); bias [N] bf16 or None."""
+    lib = load_library()
+    M, N, K = int(M), int(N), int(K)
+    if M >> 31 or N >> 31 or K >> 31:
+        _sizes32(M, N, K)
+    dev = _device_of(out, "out")
+    ot = _dtype(out, "out")
+    _run(lib.mxfp4_matmul, dev, stream, _arg(a_blocks, "a_blocks", _U8, M * K // 2, dev),
+         _arg(a_scales, "a_scales", _U8, M * K // 32, dev), _arg(b_blocks, "b_blocks", _U8, N * K // 2, dev),
+         _arg(b_scales, "b_scales", _U8, N * K // 32, dev), _arg(bias, "bias", _BF16, N, dev), M, N, K,
+         _arg(out, "out", _ELEMENTS[ot], M * N, dev), ot)
+
+
+def _expert_args(blocks, scales, bias, E, N, K, x_blocks, x_scales, x_per_slot, T, k, expert_offsets, sorted_rows,
+                 dev):
+    rows = T * k if x_per_slot else T
+    return (_arg(blocks, "blocks", _U8, E * N * K // 2, dev), _arg(scales, "scales", _U8, E * N * K // 32, dev),
+            _arg(bias, "bias", _BF16, E * N, dev), E, N, K, _arg(x_blocks, "x_blocks", _U8, rows * K // 2, dev),
+            _arg(x_scales, "x_scales", _U8, rows * K // 32, dev), int(bool(x_per_slot)), T, k,
+            _arg(expert_offsets, "expert_offsets", _I32, E + 1, dev),
+            _arg(sorted_rows, "sorted_rows", _I32, T * k, dev))
+
+
+def mxfp4_expert_matmul(blocks, scales, bias, E: int, N: int, K: int, x_blocks, x_scales, x_per_slot: bool, T: int,
+                        k: int, expert_offsets, sorted_rows, out, stream=None):
+    """The routed projection of MXFP4 activations (mxfp4_expert_matmul): out [T,k,N] f32 or bf16;
+    x_blocks and x_scales as mxfp4_quantize writes them for x [T,K], or [T,k,K] with x_per_slot."""
+    lib = load_library()
+    E, N, K, T, k = int(E), int(N), int(K), int(T), int(k)
+    if E >> 31 or N >> 31 or K >> 31 or T >> 31 or k >> 31:
+        _sizes32(E, N, K, T, k)
+    dev = _device_of(out, "out")
+    ot = _dtype(out, "out")
+    _run(lib.mxfp4_expert_matmul, dev, stream,
+         *_expert_args(blocks, scales, bias, E, N, K, x_blocks, x_scales, x_per_slot, T, k, expert_offsets,
+                       sorted_rows, dev), _arg(out, "out", _ELEMENTS[ot], T * k * N, dev), ot)
+
+
+def mxfp4_expert_matmul_swiglu(blocks, scales, bias, E: int, N: int, K: int, x_blocks, x_scales, x_per_slot: bool,
+                               T: int, k: int, expert_offsets, sorted_rows, act, stream=None):
+    """The same through the gated activation (mxfp4_expert_matmul_swiglu): act [T,k,N/2] bf16."""
+    lib = load_library()
+    E, N, K, T, k = int(E), int(N), int(K), int(T), int(k)
+    if E >> 31 or N >> 31 or K >> 31 or T >> 31 or k >> 31:
+        _sizes32(E, N, K, T, k)
+    dev = _device_of(act, "act")
+    _run(lib.mxfp4_expert_matmul_swiglu, dev, stream,
+         *_expert_args(blocks, scales, bias, E, N, K, x_blocks, x_scales, x_per_slot, T, k, expert_offsets,
+                       sorted_rows, dev), _arg(act, "act", _BF16, T * k * (N // 2), dev))

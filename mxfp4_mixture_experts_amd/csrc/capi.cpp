@@ -624,4 +624,149 @@ int moe_route_backward(const uint16_t* logits, const int32_t* topk_ids, const fl
   return MXFP4_OK;
 }
 
+int mxfp4_quantize(const void* x, int x_dtype, long long rows, int K, uint8_t* blocks, uint8_t* scales,
+                   uint16_t* values, void* stream) {
+  g_last_error[0] = '\0';
+  if (!known_dtype(x_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "x_dtype = %d unknown", x_dtype);
+  if (rows < 0) return fail(MXFP4_ERR_INVALID_ARG, "rows = %lld must be >= 0", rows);
+  if (K < 32 || K % 32 != 0) return fail(MXFP4_ERR_INVALID_ARG, "K = %d must be a positive multiple of 32", K);
+  if (rows >= (1LL << 46) / K) return fail(MXFP4_ERR_INVALID_ARG, "rows * K must be below 2^46");
+  if (rows == 0) return MXFP4_OK;
+  if (!x || !blocks || !scales) return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(blocks) || !aligned16(values))
+    return fail(MXFP4_ERR_INVALID_ARG, "x, blocks and values must be 16-byte aligned");
+  int st = check_device();
+  if (st != MXFP4_OK) return st;
+  hipError_t e = mxfp4::launch_quantize(x, x_dtype == MXFP4_DTYPE_F32, (size_t)rows * (size_t)(K / 32), blocks, scales,
+                                        values, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  return MXFP4_OK;
+}
+
+int mxfp4_quantize_transposed(const void* x, int x_dtype, long long R, int C, uint8_t* blocks, uint8_t* scales,
+                              uint16_t* values, void* stream) {
+  g_last_error[0] = '\0';
+  if (!known_dtype(x_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "x_dtype = %d unknown", x_dtype);
+  if (R < 0 || R > (1LL << 30) || R % 32 != 0)
+    return fail(MXFP4_ERR_INVALID_ARG, "R = %lld must be a multiple of 32 in [0, 2^30]", R);
+  if (C < 0 || C > (1 << 21)) return fail(MXFP4_ERR_INVALID_ARG, "C = %d must be in [0, 2^21]", C);
+  if (R == 0 || C == 0) return MXFP4_OK;
+  if (R >= (1LL << 46) / C) return fail(MXFP4_ERR_INVALID_ARG, "R * C must be below 2^46");
+  if (!x || !blocks || !scales) return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned_elem(x, x_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "x is not aligned to its elements");
+  if (!aligned16(blocks) || !aligned16(values))
+    return fail(MXFP4_ERR_INVALID_ARG, "blocks and values must be 16-byte aligned");
+  int st = check_device();
+  if (st != MXFP4_OK) return st;
+  hipError_t e = mxfp4::launch_quantize_transposed(x, x_dtype == MXFP4_DTYPE_F32, R, C, blocks, scales, values,
+                                                   static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "quantize_transposed launch");
+  return MXFP4_OK;
+}
+
+namespace {
+// sizes that the products' launches and 32-bit offsets within a tile can take
+int check_fp4_sizes(long long R, int E, int N, int K) {
+  if (N < 1 || N > (1 << 27)) return fail(MXFP4_ERR_INVALID_ARG, "N = %d must be in [1, 2^27]", N);
+  if (K < 32 || K % 32 != 0 || K >= (1 << 26))
+    return fail(MXFP4_ERR_INVALID_ARG, "K = %d must be a positive multiple of 32 below 2^26", K);
+  if (R < 0 || R > (1LL << 30)) return fail(MXFP4_ERR_INVALID_ARG, "%lld rows must be in [0, 2^30]", R);
+  if ((R / 64 + E) * (((long long)N + 63) / 64) >= (1LL << 24))
+    return fail(MXFP4_ERR_INVALID_ARG, "%lld rows x N = %d outputs are too many", R, N);
+  return MXFP4_OK;
+}
+
+int expert_matmul_impl(const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias, int E, int N, int K,
+                       const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
+                       const int32_t* expert_offsets, const int32_t* sorted_rows, void* out, mxfp4::Fp4Out kind,
+                       void* stream) {
+  if (E < 1 || E > MXFP4_MAX_EXPERTS) return fail(MXFP4_ERR_INVALID_ARG, "E = %d must be in [1, %d]", E, MXFP4_MAX_EXPERTS);
+  if (T < 0) return fail(MXFP4_ERR_INVALID_ARG, "T = %d must be >= 0", T);
+  if (k < 1 || k > E || k > MXFP4_MAX_TOPK)
+    return fail(MXFP4_ERR_INVALID_ARG, "k = %d must be in [1, min(E = %d, %d)]", k, E, MXFP4_MAX_TOPK);
+  int st = check_fp4_sizes((long long)T * k, E, N, K);
+  if (st != MXFP4_OK) return st;
+  if (kind == mxfp4::kFp4OutSwiglu && N % 2 != 0)
+    return fail(MXFP4_ERR_INVALID_ARG, "N = %d must be even (gate and up rows in pairs)", N);
+  if (T == 0) return MXFP4_OK;
+  if (!blocks || !scales || !x_blocks || !x_scales || !expert_offsets || !sorted_rows || !out)
+    return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(blocks) || !aligned16(x_blocks))
+    return fail(MXFP4_ERR_INVALID_ARG, "blocks and x_blocks must be 16-byte aligned");
+  if (!aligned_to(bias, 2) || !aligned_to(expert_offsets, 4) || !aligned_to(sorted_rows, 4) ||
+      !aligned_to(out, kind == mxfp4::kFp4OutF32 ? 4 : 2))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if ((st = check_device()) != MXFP4_OK) return st;
+  mxfp4::Fp4MatmulArgs a{};
+  a.w = blocks;
+  a.ws = scales;
+  a.bias = bias;
+  a.x = x_blocks;
+  a.xs = x_scales;
+  a.offsets = expert_offsets;
+  a.rows = sorted_rows;
+  a.out = out;
+  a.E = E;
+  a.N = N;
+  a.K = K;
+  a.R = T * k;
+  a.x_div = x_per_slot ? 1 : k;
+  const hipError_t e = mxfp4::launch_fp4_matmul(a, kind, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "expert_matmul launch");
+  return MXFP4_OK;
+}
+}  // namespace
+
+int mxfp4_matmul(const uint8_t* a_blocks, const uint8_t* a_scales, const uint8_t* b_blocks, const uint8_t* b_scales,
+                 const uint16_t* bias, int M, int N, int K, void* out, int out_dtype, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_fp4_sizes(M, 1, N, K);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(out_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "out_dtype = %d unknown", out_dtype);
+  if (M == 0) return MXFP4_OK;
+  if (!a_blocks || !a_scales || !b_blocks || !b_scales || !out)
+    return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(a_blocks) || !aligned16(b_blocks))
+    return fail(MXFP4_ERR_INVALID_ARG, "a_blocks and b_blocks must be 16-byte aligned");
+  if (!aligned_to(bias, 2) || !aligned_elem(out, out_dtype))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  if ((st = check_device()) != MXFP4_OK) return st;
+  mxfp4::Fp4MatmulArgs a{};
+  a.w = b_blocks;
+  a.ws = b_scales;
+  a.bias = bias;
+  a.x = a_blocks;
+  a.xs = a_scales;
+  a.out = out;
+  a.E = 1;
+  a.N = N;
+  a.K = K;
+  a.R = M;
+  a.x_div = 1;
+  const hipError_t e = mxfp4::launch_fp4_matmul(a, out_dtype == MXFP4_DTYPE_F32 ? mxfp4::kFp4OutF32 : mxfp4::kFp4OutBf16,
+                                                static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "matmul launch");
+  return MXFP4_OK;
+}
+
+int mxfp4_expert_matmul(const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias, int E, int N, int K,
+                        const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
+                        const int32_t* expert_offsets, const int32_t* sorted_rows, void* out, int out_dtype,
+                        void* stream) {
+  g_last_error[0] = '\0';
+  if (!known_dtype(out_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "out_dtype = %d unknown", out_dtype);
+  return expert_matmul_impl(blocks, scales, bias, E, N, K, x_blocks, x_scales, x_per_slot, T, k, expert_offsets,
+                            sorted_rows, out, out_dtype == MXFP4_DTYPE_F32 ? mxfp4::kFp4OutF32 : mxfp4::kFp4OutBf16,
+                            stream);
+}
+
+int mxfp4_expert_matmul_swiglu(const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias, int E, int N,
+                               int K, const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
+                               const int32_t* expert_offsets, const int32_t* sorted_rows, uint16_t* act,
+                               void* stream) {
+  g_last_error[0] = '\0';
+  return expert_matmul_impl(blocks, scales, bias, E, N, K, x_blocks, x_scales, x_per_slot, T, k, expert_offsets,
+                            sorted_rows, act, mxfp4::kFp4OutSwiglu, stream);
+}
+
 }  // extern "C"

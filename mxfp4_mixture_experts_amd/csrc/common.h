@@ -28,6 +28,11 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
   return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
+// The same for any value (a NaN stays one), by the hardware convert
+__device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
 // The gpt-oss gated activation of one (gate, up) pair of projection outputs
 // (gpt-oss-20b files page, src/experts.linnet: constants LIMIT = 7 and
 // ALPHA = 1.702, fn activate): the gate clamped from above at LIMIT, the

@@ -67,6 +67,28 @@ hipError_t launch_expert_gemm(const uint8_t* blocks, const uint8_t* scales, cons
 hipError_t launch_dequantize(const uint8_t* blocks, const uint8_t* scales, size_t nblocks, uint16_t* out,
                              hipStream_t stream);
 
+// quantize.hip: nblocks blocks of 32 in storage order; or x [R, C] with blocks
+// along its columns (output row c).  values (bf16, or NULL): what is stored.
+hipError_t launch_quantize(const void* x, bool f32, size_t nblocks, uint8_t* blocks, uint8_t* scales,
+                           uint16_t* values, hipStream_t stream);
+hipError_t launch_quantize_transposed(const void* x, bool f32, long long R, int C, uint8_t* blocks, uint8_t* scales,
+                                      uint16_t* values, hipStream_t stream);
+
+// fp4_matmul.hip: products of two MXFP4 operands
+enum Fp4Out { kFp4OutF32 = 0, kFp4OutBf16 = 1, kFp4OutSwiglu = 2 };
+struct Fp4MatmulArgs {
+  const uint8_t* w;   // [E, N, K / 32, 16]
+  const uint8_t* ws;  // [E, N, K / 32]
+  const uint16_t* bias;  // [E, N], or NULL
+  const uint8_t* x;   // [rows, K / 32, 16]; routed row r reads row r / x_div
+  const uint8_t* xs;
+  const int32_t* offsets;  // [E + 1], or NULL: dense (E = 1, every row in order)
+  const int32_t* rows;     // [R], with offsets
+  void* out;               // [R, N] fp32 or bf16, or [R, N / 2] bf16 activations
+  int E, N, K, R, x_div;
+};
+hipError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int out_kind, hipStream_t stream);
+
 // router.hip: logits [T, E] bf16 = x [T, H] . w [E, H]^T + bias (fp32 sums, rounded once)
 hipError_t launch_router(const uint16_t* x, const uint16_t* w, const uint16_t* bias, int T, int H, int E,
                          uint16_t* logits, hipStream_t stream);
