@@ -256,42 +256,57 @@ __device__ __forceinline__ bool find_tile(const Fp4MatmulArgs& a, int NT, int la
 // Keeps the compiler's scheduler from moving instructions across.
 __device__ __forceinline__ void pipeline_fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// the storage order of a row's 8 blocks of a stage in LDS, so that 32 lanes that
-// read one block of 32 rows meet distinct banks
-__device__ __forceinline__ int row_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// Waits until at most N of the wave's loads are under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);
+}
 
-template <int WM, int WN, int MT, int NT>
+// The products of X rows (MFMA operand B) and W rows (operand A): a lane of an
+// accumulator then holds one routed row and runs of four consecutive outputs.
+// Four waves side by side along the weight rows; every wave multiplies all the
+// tile's routed rows, so a tile with few of them leaves whole sub-tiles out.
+//
+// K goes by stages of four blocks (128 elements).  A ring of four stages in
+// LDS, 64 bytes a row, filled by direct loads; a row's blocks lie in an order
+// (block ^ row / 2) in which eight lanes that read one block of eight rows meet
+// distinct banks.  Scale bytes come in groups of 16 blocks: a row's bytes start
+// anywhere, so two aligned 16-byte pieces hold them (clamped to the piece with
+// the row's last byte), which one thread a row shifts into place and splits into
+// the bytes of each half wave's blocks; the MFMA picks a byte of a word.
+template <int MT, int NT>
 struct TileShape {
-  static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-  static constexpr int TM = WM * MT * 32, TN = WN * NT * 32, kRows = TM + TN;
-  static constexpr int kPieces = kRows / 8 / kWaves;  // 1 KB pieces of a stage a wave brings
-  static constexpr int kScaleRows = (kRows + kThreads - 1) / kThreads;
-  static constexpr int kStageBytes = kRows * 128, kScaleBytes = kRows * 8;
+  static constexpr int kWaves = 4, kThreads = kWaves * 64;
+  static constexpr int TM = MT * 32, TN = kWaves * NT * 32, kRows = TM + TN;
+  static constexpr int kPieces = kRows / 16 / kWaves;  // 1 KB pieces of a stage (16 rows) a wave brings
+  static constexpr int kRawPieces = (kRows / 32 + kWaves - 1) / kWaves;  // 1 KB pieces of scales (32 rows)
+  static constexpr int kCook = (kRows + kThreads - 1) / kThreads;  // rows whose scales a thread places
+  static constexpr int kStage = kRows * 64;
+  static constexpr int kRaw = 4 * kStage, kCooked = kRaw + kRawPieces * kWaves * 1024;
+  static constexpr int kRowsAt = kCooked + kRows * 16;
   static constexpr int kOutStride = NT * 32 + 4;  // floats
-  static constexpr int kOutBytes = kWaves * 32 * kOutStride * 4;
-  static constexpr int kMain = 2 * (kStageBytes + kScaleBytes);
-  static constexpr int kLds = (kMain > kOutBytes ? kMain : kOutBytes) + TM * 4;
-  static_assert(kRows % (8 * kWaves) == 0 && kWaves % 2 == 0, "whole pieces; a piece's parity is its wave's");
+  static constexpr int kBiasAt = kWaves * 32 * kOutStride * 4;
+  static constexpr int kLds = kRowsAt + TM * 4;
+  static_assert(kRows % (16 * kWaves) == 0 && kBiasAt + TN * 4 <= kRowsAt, "whole pieces; room for the epilogue");
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
 };
 
-template <int WM, int WN, int MT, int NT, int OUT>
-__global__ __launch_bounds__(WM* WN * 64) void fp4_tile_kernel(Fp4MatmulArgs a, int vec) {
-  using S = TileShape<WM, WN, MT, NT>;
+template <int MT, int NT, int OUT>
+__global__ __launch_bounds__(256, 1) void fp4_tile_kernel(Fp4MatmulArgs a, int vec) {
+  using S = TileShape<MT, NT>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  int* const rows_lds = reinterpret_cast<int*>(lds + S::kRowsAt);
   // the array's offset in the workgroup's LDS
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  auto codes = [&](int buf) { return lds + buf * S::kStageBytes; };
-  auto scl = [&](int buf) { return lds + 2 * S::kStageBytes + buf * S::kScaleBytes; };
-  int* const rows_lds = reinterpret_cast<int*>(lds + S::kLds - S::TM * 4);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, half = lane >> 5;
-  const int NP = (a.N + S::TN - 1) / S::TN;
   Fp4Tile t;
-  if (!find_tile<S::TM>(a, NP, lane, t)) return;
+  if (!find_tile<S::TM>(a, (a.N + S::TN - 1) / S::TN, lane, t)) return;
   const int KB = a.K >> 5;
-  const int stages = (KB + 7) >> 3;
+  const int stages = (KB + 3) >> 2;
   const int n0 = t.nt * S::TN;
 
   for (int i = tid; i < S::TM; i += S::kThreads) rows_lds[i] = routed_row(a, t.p0 + i, t.f);
@@ -306,184 +321,261 @@ __global__ __launch_bounds__(WM* WN * 64) void fp4_tile_kernel(Fp4MatmulArgs a, 
     }
     return (size_t)t.e * a.N + min(n0 + i - S::TM, a.N - 1);
   };
-  const int slot = (lane & 7) ^ (lane >> 3) ^ (wave & 1);  // the block of a stage that this lane brings
+  // codes: piece p holds rows 16 p .. + 15; lane l brings row l / 4's LDS slot l % 4
+  const int slot = (lane & 3) ^ ((lane >> 3) & 3);
   const uint8_t* src[S::kPieces];
 #pragma unroll
   for (int p = 0; p < S::kPieces; p++) {
-    const int i = 8 * (wave + S::kWaves * p) + (lane >> 3);
+    const int i = 16 * (wave + S::kWaves * p) + (lane >> 2);
     src[p] = (i < S::TM ? a.x : a.w) + tile_row(i) * KB * 16;
   }
-  const uint8_t* ssrc[S::kScaleRows];
-#pragma unroll
-  for (int p = 0; p < S::kScaleRows; p++) {
-    const int i = min(tid + S::kThreads * p, S::kRows - 1);
-    ssrc[p] = (i < S::TM ? a.xs : a.ws) + tile_row(i) * KB;
-  }
-  auto bring = [&](int s, int buf) {
-    const int off = min(8 * s + slot, KB - 1) * 16;  // blocks past K: the last one, masked below
-#pragma unroll
-    for (int p = 0; p < S::kPieces; p++)
-      dma16(src[p] + off, lds0 + buf * S::kStageBytes + (wave + S::kWaves * p) * 1024);
+  auto bring = [&](int s, int buf, int p) {
+    const int off = min(4 * s + slot, KB - 1) * 16;  // blocks past K: the last one, masked when multiplied
+    dma16(src[p] + off, lds0 + buf * S::kStage + (wave + S::kWaves * p) * 1024);
   };
-  uint64_t sreg[S::kScaleRows];
-  auto bring_scales = [&](int s) {
-    const int left = KB - 8 * s;  // bytes of this stage
+  // scales: piece p holds rows 32 p .. + 31; lane l brings 16-byte piece l % 2 of row l / 2
+  const uint8_t* raw_src[S::kRawPieces];  // the group's first, aligned
+  int raw_last[S::kRawPieces];            // from it to the piece with the row's last byte
 #pragma unroll
-    for (int p = 0; p < S::kScaleRows; p++) {
-      if (left >= 8) {
-        __builtin_memcpy(&sreg[p], ssrc[p] + 8 * s, 8);
-      } else {
-        uint64_t v = 0;
-        for (int j = 0; j < left; j++) v |= (uint64_t)ssrc[p][8 * s + j] << (8 * j);
-        sreg[p] = v;
+  for (int p = 0; p < S::kRawPieces; p++) {
+    const int i = min(32 * (wave + S::kWaves * p) + (lane >> 1), S::kRows - 1);
+    const uintptr_t row = reinterpret_cast<uintptr_t>(i < S::TM ? a.xs : a.ws) + tile_row(i) * KB;
+    raw_src[p] = reinterpret_cast<const uint8_t*>(row & ~(uintptr_t)15);
+    raw_last[p] = (int)(((row + KB - 1) & ~(uintptr_t)15) - (row & ~(uintptr_t)15));
+  }
+  auto bring_scales = [&](int g, int p) {
+    dma16(raw_src[p] + min(16 * (g + (lane & 1)), raw_last[p]), lds0 + S::kRaw + (wave + S::kWaves * p) * 1024);
+  };
+  int shift[S::kCook];
+#pragma unroll
+  for (int p = 0; p < S::kCook; p++) {
+    const int i = min(tid + S::kThreads * p, S::kRows - 1);
+    shift[p] = (int)((reinterpret_cast<uintptr_t>(i < S::TM ? a.xs : a.ws) + tile_row(i) * KB) & 15);
+  }
+  // a group's scale bytes of a row into place: [half wave][8 K steps]
+  auto cook = [&]() {
+#pragma unroll
+    for (int p = 0; p < S::kCook; p++) {
+      const int i = tid + S::kThreads * p;
+      if (S::kRows % S::kThreads != 0 && i >= S::kRows) break;
+      const u32x4_t* q = reinterpret_cast<const u32x4_t*>(lds + S::kRaw + i * 32);
+      const u32x4_t lo = q[0], hi = q[1];
+      const bool by2 = shift[p] & 8, by1 = shift[p] & 4;
+      const uint32_t b[6] = {by2 ? lo.z : lo.x, by2 ? lo.w : lo.y, by2 ? hi.x : lo.z,
+                             by2 ? hi.y : lo.w, by2 ? hi.z : hi.x, by2 ? hi.w : hi.y};
+      uint32_t d[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const uint32_t d0 = by1 ? b[j + 1] : b[j];
+        const uint32_t d1 = by1 ? b[j + 2] : b[j + 1];
+        d[j] = __builtin_amdgcn_alignbyte(d1, d0, shift[p] & 3);
       }
+      *reinterpret_cast<u32x4_t*>(lds + S::kCooked + i * 16) =
+          u32x4_t{__builtin_amdgcn_perm(d[1], d[0], 0x06040200u), __builtin_amdgcn_perm(d[3], d[2], 0x06040200u),
+                  __builtin_amdgcn_perm(d[1], d[0], 0x07050301u), __builtin_amdgcn_perm(d[3], d[2], 0x07050301u)};
     }
   };
-  auto put_scales = [&](int buf) {
-#pragma unroll
-    for (int p = 0; p < S::kScaleRows; p++)
-      if (tid + S::kThreads * p < S::kRows)
-        *reinterpret_cast<uint64_t*>(scl(buf) + (tid + S::kThreads * p) * 8) = sreg[p];
-  };
 
-  const int wm = wave % WM, wn = wave / WM;
-  const int xr0 = wm * MT * 32, wr0 = S::TM + wn * NT * 32;
-  int off[4];
-#pragma unroll
-  for (int j = 0; j < 4; j++) off[j] = l32 * 128 + (((2 * j + half) ^ row_swizzle(l32)) << 4);
-  const uint32_t pick = half ? 0x07050301u : 0x06040200u;  // this half's blocks of the stage
+  const int wr0 = S::TM + wave * NT * 32;
+  const int swz = (l32 >> 1) & 3;
+  const int off0 = l32 * 64 + ((half ^ swz) << 4), off1 = l32 * 64 + (((2 + half) ^ swz) << 4);
 
-  v16f acc[NT][MT];
-#pragma unroll
-  for (int n = 0; n < NT; n++)
-#pragma unroll
-    for (int m = 0; m < MT; m++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) acc[n][m][i] = 0.f;
-
-  auto stage_scale = [&](int buf, int row) -> int {
-    const uint2 v = *reinterpret_cast<const uint2*>(scl(buf) + (row + l32) * 8);
-    return (int)__builtin_amdgcn_perm(v.y, v.x, pick);
-  };
-  auto read = [&](int buf, int row, int j) -> u32x4_t {
-    return *reinterpret_cast<const u32x4_t*>(codes(buf) + row * 128 + off[j]);
-  };
-
-  // The four K steps of a stage; the last stage's steps past K are left out and
-  // the block past K of a broken step is taken as zero codes (its scale, a
-  // byte 0 where the row has none, is finite).
-  auto stage = [&](int buf, int s, auto lastc) {
-    constexpr bool kLast = decltype(lastc)::value;
-    int wsc[NT], xsc[MT];
-#pragma unroll
-    for (int n = 0; n < NT; n++) wsc[n] = stage_scale(buf, wr0 + 32 * n);
-#pragma unroll
-    for (int m = 0; m < MT; m++) xsc[m] = stage_scale(buf, xr0 + 32 * m);
-    const int left = KB - 8 * s;
-    auto step = [&](auto jc) {
-      constexpr int J = decltype(jc)::value;
-      if (kLast && left <= 2 * J) return;
-      v8i xv[MT], wv[NT];
-#pragma unroll
-      for (int n = 0; n < NT; n++) wv[n] = fp4_operand(read(buf, wr0 + 32 * n, J));
-#pragma unroll
-      for (int m = 0; m < MT; m++) {
-        u32x4_t v = read(buf, xr0 + 32 * m, J);
-        if (kLast && 2 * J + half >= left) v = u32x4_t{0, 0, 0, 0};
-        xv[m] = fp4_operand(v);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int m = 0; m < MT; m++)
-          acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[n], xv[m], acc[n][m], kFmtFp4, kFmtFp4, J,
-                                                                      wsc[n], J, xsc[m]);
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 3>{});
-  };
-
-  bring(0, 0);
-  bring_scales(0);
-  put_scales(0);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's pieces are in LDS
-  __syncthreads();
-  for (int s = 0; s < stages - 1; s++) {
-    const int buf = s & 1;
-    bring(s + 1, buf ^ 1);  // read last in stage s - 1, which every wave has left
-    bring_scales(s + 1);
-    pipeline_fence();
-    stage(buf, s, std::false_type{});
-    pipeline_fence();  // the products do not wait behind the scales' arrival
-    put_scales(buf ^ 1);
-    __builtin_amdgcn_s_waitcnt(0x0f70);
-    __syncthreads();
-  }
-  stage((stages - 1) & 1, stages - 1, std::true_type{});
-  __syncthreads();
-
-  // Lane (l32, half) holds routed row l32 of each 32 x 32 block and weight rows
-  // 8 g + 4 half + i: through LDS, 32 routed rows at a time, so that a store
-  // instruction writes whole runs of a row.
-  float* const ob = reinterpret_cast<float*>(lds) + wave * 32 * S::kOutStride;
-  const int nw = n0 + wn * NT * 32;
-  const uint16_t* bias = a.bias ? a.bias + (size_t)t.e * a.N : nullptr;
-#pragma unroll
-  for (int m = 0; m < MT; m++) {
+  // The tile with its first MA sub-tiles of routed rows.
+  auto run = [&](auto mac) {
+    constexpr int MA = decltype(mac)::value;
+    v16f acc[NT][MA];
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
-      for (int g = 0; g < 4; g++)
-        *reinterpret_cast<f32x4_t*>(ob + l32 * S::kOutStride + 32 * n + 8 * g + 4 * half) =
-            f32x4_t{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
-    __builtin_amdgcn_wave_barrier();
-    constexpr int kChunks = NT * 4;  // 8 columns each
+      for (int m = 0; m < MA; m++)
 #pragma unroll
-    for (int it = 0; it < 32 * kChunks / 64; it++) {
-      const int idx = it * 64 + lane;
-      const int row = idx / kChunks, cc = idx % kChunks;
-      const int r = rows_lds[xr0 + 32 * m + row];
-      const int n = nw + 8 * cc;
-      float v[8];
-      const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(ob + row * S::kOutStride + 8 * cc);
-      const f32x4_t v1 = *reinterpret_cast<const f32x4_t*>(ob + row * S::kOutStride + 8 * cc + 4);
+        for (int i = 0; i < 16; i++) acc[n][m][i] = 0.f;
+    struct Ops {
+      u32x4_t w[NT], x[MA];
+    };
+    struct Scales {
+      uint2 w[NT], x[MA];
+    };
+    auto read = [&](Ops& o, int buf, int off) {
+      const uint8_t* b = lds + buf * S::kStage + off;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        v[i] = v0[i];
-        v[4 + i] = v1[i];
+      for (int n = 0; n < NT; n++) o.w[n] = *reinterpret_cast<const u32x4_t*>(b + (wr0 + 32 * n) * 64);
+#pragma unroll
+      for (int m = 0; m < MA; m++) o.x[m] = *reinterpret_cast<const u32x4_t*>(b + m * 2048);
+    };
+    auto read_scales = [&](Scales& c) {
+      const uint8_t* b = lds + S::kCooked + l32 * 16 + half * 8;
+#pragma unroll
+      for (int n = 0; n < NT; n++) c.w[n] = *reinterpret_cast<const uint2*>(b + (wr0 + 32 * n) * 16);
+#pragma unroll
+      for (int m = 0; m < MA; m++) c.x[m] = *reinterpret_cast<const uint2*>(b + m * 512);
+    };
+    // K step k (0 .. 7) of the group; `between` follows each MFMA
+    auto multiply = [&](const Ops& o, const Scales& c, auto kc, auto between) {
+      constexpr int k = decltype(kc)::value;
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int m = 0; m < MA; m++) {
+          acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              fp4_operand(o.w[n]), fp4_operand(o.x[m]), acc[n][m], kFmtFp4, kFmtFp4, k & 3,
+              (int)(k < 4 ? c.w[n].x : c.w[n].y), k & 3, (int)(k < 4 ? c.x[m].x : c.x[m].y));
+          between(n * MA + m);
+        }
+    };
+    Ops A, Bq;
+    Scales sc;
+
+    // Stage s = 4 g + Q, in ring slot Q, with another behind it.  Its first K
+    // step is multiplied while the second's operands are read; behind the
+    // barrier (every wave has read the slot, and the next stage has arrived)
+    // the slot takes stage s + 4 and the next stage's first operands are read
+    // while the second step is multiplied.
+    auto stage = [&](int g, auto qc) {
+      constexpr int Q = decltype(qc)::value;
+      constexpr int k = 2 * Q;
+      const int s = 4 * g + Q;
+      read(Bq, Q, off1);
+      pipeline_fence();
+      multiply(A, sc, std::integral_constant<int, k>{}, [](int) {});
+      if (Q == 3) cook();
+      pipeline_fence();
+      // under way behind what the next stage needs: two stages, in the second
+      // of a group its scales too
+      wait_loads<2 * S::kPieces + (Q == 1 ? S::kRawPieces : 0)>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      pipeline_fence();
+      read(A, (Q + 1) & 3, off0);
+      Scales next = sc;
+      if (Q == 3) read_scales(next);
+      if (Q == 0) {
+#pragma unroll
+        for (int p = 0; p < S::kRawPieces; p++) bring_scales(g + 1, p);
       }
-      if (r < 0 || n >= a.N) continue;
-      if (bias) {
+      pipeline_fence();
+      constexpr int kEach = (S::kPieces + NT * MA - 1) / (NT * MA);
+      multiply(Bq, sc, std::integral_constant<int, k + 1>{}, [&](int i) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] += bf16_bits_to_f32(bias[min(n + i, a.N - 1)]);
-      }
-      if (vec) {
-        store8<OUT>(a, r, n, v);
-      } else {
+        for (int p = i * kEach; p < (i + 1) * kEach && p < S::kPieces; p++) bring(s + 4, Q, p);
+        pipeline_fence();
+      });
+      sc = next;
+    };
+
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) store_pair<OUT>(a, r, n + i, v[i], v[i + 1]);
-      }
+    for (int p = 0; p < S::kRawPieces; p++) bring_scales(0, p);
+#pragma unroll
+    for (int s = 0; s < 4; s++)
+#pragma unroll
+      for (int p = 0; p < S::kPieces; p++) bring(s, s, p);
+    wait_loads<4 * S::kPieces < 63 ? 4 * S::kPieces : 63>();
+    asm volatile("s_barrier" ::: "memory");
+    cook();
+    wait_loads<3 * S::kPieces>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    read(A, 0, off0);
+    read_scales(sc);
+    const int last = stages - 1, groups = last >> 2;
+    for (int g = 0; g < groups; g++) {
+      stage(g, std::integral_constant<int, 0>{});
+      stage(g, std::integral_constant<int, 1>{});
+      stage(g, std::integral_constant<int, 2>{});
+      stage(g, std::integral_constant<int, 3>{});
     }
-    __builtin_amdgcn_wave_barrier();
-  }
+    if ((last & 3) > 0) stage(groups, std::integral_constant<int, 0>{});
+    if ((last & 3) > 1) stage(groups, std::integral_constant<int, 1>{});
+    if ((last & 3) > 2) stage(groups, std::integral_constant<int, 2>{});
+    // The last stage: blocks past K are taken as zero codes under a finite scale.
+    {
+      read(Bq, last & 3, off1);
+      const int left = KB - 4 * last;
+      auto tail = [&](Ops& o, int j) {
+        const bool keep = 2 * j + half < left;
+        const int k = 2 * (last & 3) + j;
+        auto byte = [&](uint2 v) -> uint32_t {
+          const uint32_t w = (k < 4 ? v.x : v.y) >> (8 * (k & 3));
+          return keep ? w : 0u;
+        };
+        Scales c;
+#pragma unroll
+        for (int n = 0; n < NT; n++) c.w[n].x = byte(sc.w[n]);
+#pragma unroll
+        for (int m = 0; m < MA; m++) {
+          c.x[m].x = byte(sc.x[m]);
+          o.x[m] = keep ? o.x[m] : u32x4_t{0, 0, 0, 0};
+        }
+        multiply(o, c, std::integral_constant<int, 0>{}, [](int) {});
+      };
+      tail(A, 0);
+      if (left > 2) tail(Bq, 1);
+    }
+    wait_loads<0>();  // nothing more comes into LDS
+    __syncthreads();
+
+    // Lane (l32, half) holds routed row l32 of each 32 x 32 block and weight rows
+    // 8 g + 4 half + i: through LDS, 32 routed rows at a time, so that a store
+    // instruction writes whole runs of a row.
+    float* const ob = reinterpret_cast<float*>(lds) + wave * 32 * S::kOutStride;
+    float* const bias_lds = reinterpret_cast<float*>(lds + S::kBiasAt) + wave * NT * 32;
+    const int nw = n0 + wave * NT * 32;
+    for (int i = lane; i < NT * 32; i += 64)
+      bias_lds[i] = a.bias ? bf16_bits_to_f32(a.bias[(size_t)t.e * a.N + min(nw + i, a.N - 1)]) : 0.f;
+#pragma unroll
+    for (int m = 0; m < MA; m++) {
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+          *reinterpret_cast<f32x4_t*>(ob + l32 * S::kOutStride + 32 * n + 8 * g + 4 * half) =
+              f32x4_t{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
+      __builtin_amdgcn_wave_barrier();
+      constexpr int kChunks = NT * 4;  // 8 columns each
+#pragma unroll
+      for (int it = 0; it < 32 * kChunks / 64; it++) {
+        const int idx = it * 64 + lane;
+        const int row = idx / kChunks, cc = idx % kChunks;
+        const int r = rows_lds[32 * m + row];
+        const int n = nw + 8 * cc;
+        float v[8];
+        const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(ob + row * S::kOutStride + 8 * cc);
+        const f32x4_t v1 = *reinterpret_cast<const f32x4_t*>(ob + row * S::kOutStride + 8 * cc + 4);
+        const f32x4_t b0 = *reinterpret_cast<const f32x4_t*>(bias_lds + 8 * cc);
+        const f32x4_t b1 = *reinterpret_cast<const f32x4_t*>(bias_lds + 8 * cc + 4);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          v[i] = v0[i] + b0[i];
+          v[4 + i] = v1[i] + b1[i];
+        }
+        if (r < 0 || n >= a.N) continue;
+        if (vec) {
+          store8<OUT>(a, r, n, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) store_pair<OUT>(a, r, n + i, v[i], v[i + 1]);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
+  const int subs = (min(t.f - t.p0, S::TM) + 31) >> 5;
+  if (MT >= 4 && subs >= 4) run(std::integral_constant<int, MT >= 4 ? 4 : 1>{});
+  else if (MT >= 3 && subs == 3) run(std::integral_constant<int, MT >= 3 ? 3 : 1>{});
+  else if (MT >= 2 && subs >= 2) run(std::integral_constant<int, MT >= 2 ? 2 : 1>{});
+  else run(std::integral_constant<int, 1>{});
 }
 
-template <int WM, int WN, int MT, int NT, int OUT>
+template <int MT, int NT, int OUT>
 hipError_t launch_tiles(const Fp4MatmulArgs& a, hipStream_t stream) {
-  using S = TileShape<WM, WN, MT, NT>;
-  static DynLdsLimit limit(reinterpret_cast<const void*>(fp4_tile_kernel<WM, WN, MT, NT, OUT>), S::kLds);
+  using S = TileShape<MT, NT>;
+  static DynLdsLimit limit(reinterpret_cast<const void*>(fp4_tile_kernel<MT, NT, OUT>), S::kLds);
   const hipError_t e = limit.ensure();
   if (e != hipSuccess) return e;
   // at most R / TM whole row tiles and one broken one for each expert with rows
   const long long mt = a.offsets ? a.R / S::TM + (long long)min(a.E, a.R) : ((long long)a.R + S::TM - 1) / S::TM;
   const long long tiles = mt * ((a.N + S::TN - 1) / S::TN);
   const long long grid = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid * S::kThreads > 0xffffffffLL) return hipErrorInvalidValue;
   const int vec = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
-  hipLaunchKernelGGL((fp4_tile_kernel<WM, WN, MT, NT, OUT>), dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream,
-                     a, vec);
+  hipLaunchKernelGGL((fp4_tile_kernel<MT, NT, OUT>), dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a, vec);
   return hipGetLastError();
 }
 
@@ -498,7 +590,7 @@ template <int OUT>
 hipError_t launch_out(const Fp4MatmulArgs& a, hipStream_t stream) {
   const long long groups = a.offsets ? min(a.E, a.R) : 1;
   if (a.R <= 16 * groups) return launch_rows<OUT>(a, stream);
-  return launch_tiles<2, 2, 2, 3, OUT>(a, stream);
+  return launch_tiles<4, 3, OUT>(a, stream);
 }
 
 }  // namespace
