@@ -14,20 +14,11 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kFmtFp4 = 4;  // MFMA operand format code of E2M1
 constexpr int kXcds = 8;
-
-// 16 bytes a lane from global memory into LDS: lane l's go to the wave's
-// destination + 16 l.  In asm, because the compiler waits for such a load's
-// arrival before any LDS read that it cannot tell apart from the destination;
-// here every arrival is waited for with s_waitcnt vmcnt before the barrier
-// behind which the data are read.  (No output registers; the nop is the wait
-// state between the write of m0 and its use.  Nothing else here uses m0.)
-__device__ __forceinline__ void dma16(const void* src, uint32_t lds_off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_off), "v"(src)
-               : "memory");
-}
 
 __device__ __forceinline__ v8i fp4_operand(u32x4_t v) {
   return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
@@ -52,29 +43,38 @@ __device__ __forceinline__ int routed_row(const Fp4MatmulArgs& a, int p, int f) 
   return (unsigned)r < (unsigned)a.R ? r : -1;
 }
 
-// V consecutive outputs of row r from column n on (V = 8: all of them exist and
-// the row's start and n allow 16-byte stores of fp32, of bf16, or 8-byte
-// stores of activations; V = 2: n + 1 may be past N).
+// Twice the bytes that one column of the product takes in the output.
 template <int OUT>
-__device__ __forceinline__ void store8(const Fp4MatmulArgs& a, int r, int n, const float (&v)[8]) {
+constexpr int kOutBytes2 = OUT == kFp4OutF32 ? 8 : OUT == kFp4OutBf16 ? 4 : 2;
+
+template <int OUT>
+__device__ __forceinline__ uint8_t* out_at(const Fp4MatmulArgs& a, int r, int n) {
+  return static_cast<uint8_t*>(a.out) + ((size_t)r * a.N + n) * kOutBytes2<OUT> / 2;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
+// Eight consecutive outputs of a row (as products, or as four activations), at
+// an address that is a multiple of their size (of 16 bytes for fp32).
+template <int OUT>
+__device__ __forceinline__ void store8(uint8_t* o, const float (&v)[8]) {
   if (OUT == kFp4OutF32) {
-    f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + (size_t)r * a.N + n);
-    o[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-    o[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    reinterpret_cast<f32x4_t*>(o)[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4_t*>(o)[1] = f32x4_t{v[4], v[5], v[6], v[7]};
   } else if (OUT == kFp4OutBf16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = f32_to_bf16_any(v[2 * i]) | f32_to_bf16_any(v[2 * i + 1]) << 16;
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + (size_t)r * a.N + n) = u32x4_t{w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<u32x4_t*>(o) = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                             pack_bf16(v[6], v[7])};
   } else {
-    uint32_t w[4];
+    float s[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = f32_to_bf16_any(swiglu(v[2 * i], v[2 * i + 1]));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + ((size_t)r * a.N + n) / 2) =
-        make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    for (int i = 0; i < 4; i++) s[i] = swiglu(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
   }
 }
 
+// Outputs n and n + 1 of row r (those below N), or their activation.
 template <int OUT>
 __device__ __forceinline__ void store_pair(const Fp4MatmulArgs& a, int r, int n, float v0, float v1) {
   if (n >= a.N) return;
@@ -210,45 +210,64 @@ __device__ __forceinline__ int incl_scan(int v, int lane) {
   return v;
 }
 
-// The workgroup's tile: tiles are numbered expert by expert, weight panel by
-// weight panel, the panel's row tiles next to each other, and every XCD takes
+// A tile's number within its expert's mt row tiles x NP weight panels: blocks of
+// kBlockTiles row tiles, in them panel by panel, so that the 32 tiles that an
+// XCD has under way share both their rows and their panels in its L2.
+constexpr int kBlockTiles = 8;
+__device__ __forceinline__ void place_tile(int local, int mt, int NP, int& m, int& nt) {
+  const int block = local / (kBlockTiles * NP);
+  const int rest = local - block * kBlockTiles * NP;
+  const int height = min(kBlockTiles, mt - block * kBlockTiles);
+  nt = rest / height;
+  m = block * kBlockTiles + rest - nt * height;
+}
+
+// The workgroup's tile: tiles are numbered expert by expert, and every XCD takes
 // a contiguous run of the numbers.  False for the surplus workgroups.
 template <int TM>
-__device__ __forceinline__ bool find_tile(const Fp4MatmulArgs& a, int NT, int lane, Fp4Tile& t) {
+__device__ __forceinline__ bool find_tile(const Fp4MatmulArgs& a, int NP, int lane, Fp4Tile& t) {
   int total = 0;
-  for (int base = 0; base < a.E; base += 64) {
-    int b = 0, f = 0;
-    if (base + lane < a.E) group_rows(a, base + lane, b, f);
-    int v = (f - b + TM - 1) / TM;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    total += v;
+  if (!a.offsets) {
+    total = (a.R + TM - 1) / TM;
+  } else {
+    for (int base = 0; base < a.E; base += 64) {
+      int b = 0, f = 0;
+      if (base + lane < a.E) group_rows(a, base + lane, b, f);
+      total += __builtin_amdgcn_readlane(incl_scan((f - b + TM - 1) / TM, lane), 63);
+    }
   }
-  total *= NT;
+  total *= NP;
   const int per = (total + kXcds - 1) / kXcds;
   const int i = blockIdx.x / kXcds;
   const int id = (blockIdx.x % kXcds) * per + i;
   if (i >= per || id >= total) return false;
+  if (!a.offsets) {
+    int m;
+    place_tile(id, total / NP, NP, m, t.nt);
+    t.e = 0;
+    t.p0 = m * TM;
+    t.f = a.R;
+    return true;
+  }
   int before = 0;
   for (int base = 0; base < a.E; base += 64) {
     int b = 0, f = 0;
     if (base + lane < a.E) group_rows(a, base + lane, b, f);
-    const int cnt = (f - b + TM - 1) / TM * NT;
+    const int cnt = (f - b + TM - 1) / TM * NP;
     const int incl = incl_scan(cnt, lane) + before;
     const uint64_t hit = wave_ballot(id >= incl - cnt && id < incl);
     if (hit) {
       const int src = __builtin_ctzll(hit);
-      const int local = id - __shfl(incl - cnt, src, 64);
-      b = __shfl(b, src, 64);
-      f = __shfl(f, src, 64);
-      const int mt = (f - b + TM - 1) / TM;
-      t.e = __builtin_amdgcn_readfirstlane(base + src);
-      t.nt = __builtin_amdgcn_readfirstlane(local / mt);
-      t.p0 = __builtin_amdgcn_readfirstlane(b + local % mt * TM);
-      t.f = __builtin_amdgcn_readfirstlane(f);
+      const int local = id - __builtin_amdgcn_readlane(incl - cnt, src);
+      t.e = base + src;
+      b = __builtin_amdgcn_readlane(b, src);
+      t.f = __builtin_amdgcn_readlane(f, src);
+      int m;
+      place_tile(local, (t.f - b + TM - 1) / TM, NP, m, t.nt);
+      t.p0 = b + m * TM;
       return true;
     }
-    before = __shfl(incl, 63, 64);
+    before = __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
@@ -256,49 +275,84 @@ __device__ __forceinline__ bool find_tile(const Fp4MatmulArgs& a, int NT, int la
 // Keeps the compiler's scheduler from moving instructions across.
 __device__ __forceinline__ void pipeline_fence() { __builtin_amdgcn_sched_barrier(0); }
 
+// Every wave's LDS reads and writes before it are done behind it; loads from
+// memory stay under way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// 16 bytes a lane from memory into LDS: lane l's go to the wave's destination +
+// 16 l.  In asm, because the compiler waits for the arrival of every such load
+// before any LDS read that it cannot tell apart from the destination; here
+// the arrival is waited for with vmcnt before the barrier behind which the
+// data are read.  (No output registers; the nop is the wait state between the
+// write of m0 and its use.  Nothing else here uses m0.)
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds_off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_off), "v"(src)
+               : "memory");
+}
+
 // Waits until at most N of the wave's loads are under way.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N < 64, "six bits");
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);
+  asm volatile("" ::: "memory");
 }
 
-// The products of X rows (MFMA operand B) and W rows (operand A): a lane of an
-// accumulator then holds one routed row and runs of four consecutive outputs.
-// Four waves side by side along the weight rows; every wave multiplies all the
-// tile's routed rows, so a tile with few of them leaves whole sub-tiles out.
+// K step j of a stage is the blocks first_block(j) and first_block(j) + 2.
+__device__ __forceinline__ constexpr int first_block(int j) { return (j & 2) * 2 + (j & 1); }
+
+// The order of a row's eight blocks of a stage in LDS, in which the lanes that
+// read one block of different rows meet different banks.
+__device__ __forceinline__ int row_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Four waves side by side along the weight rows.  The weights are the MFMA's
+// operand A, the activations operand B: a lane of an accumulator then holds
+// one routed row and runs of four consecutive outputs.  Every wave multiplies
+// all the tile's routed rows, so a tile with few of them leaves whole
+// sub-tiles out.
 //
-// K goes by stages of four blocks (128 elements).  A ring of four stages in
-// LDS, 64 bytes a row, filled by direct loads; a row's blocks lie in an order
-// (block ^ row / 2) in which eight lanes that read one block of eight rows meet
-// distinct banks.  Scale bytes come in groups of 16 blocks: a row's bytes start
-// anywhere, so two aligned 16-byte pieces hold them (clamped to the piece with
-// the row's last byte), which one thread a row shifts into place and splits into
-// the bytes of each half wave's blocks; the MFMA picks a byte of a word.
+// K goes by stages of eight blocks (256 elements): a row's 128 bytes of codes,
+// so that every line read from L2 is used while it is in L1 (with stages of
+// four blocks each line came twice).  A weight row belongs to one wave, so its
+// codes go straight to registers, up to two stages ahead, the four loads of a
+// line close together; the activations, which all waves share, go straight to
+// two slots of LDS.  A row's scale bytes start anywhere: a window of 32 blocks
+// comes as the three aligned 16-byte pieces that hold it (none without a byte of
+// the row); a thread a row shifts them into place and splits them into a word a
+// stage and half wave, of which the MFMA picks a byte.
+//
+// Two workgroups share a CU, two waves a SIMD: one wave a SIMD with half as many
+// accumulators again came to 0.6 of the rate, its loads, waits, first and last
+// steps in line with its products.  Loads are spread between the products, one
+// behind every second.
 template <int MT, int NT>
 struct TileShape {
   static constexpr int kWaves = 4, kThreads = kWaves * 64;
   static constexpr int TM = MT * 32, TN = kWaves * NT * 32, kRows = TM + TN;
-  static constexpr int kPieces = kRows / 16 / kWaves;  // 1 KB pieces of a stage (16 rows) a wave brings
-  static constexpr int kRawPieces = (kRows / 32 + kWaves - 1) / kWaves;  // 1 KB pieces of scales (32 rows)
-  static constexpr int kCook = (kRows + kThreads - 1) / kThreads;  // rows whose scales a thread places
-  static constexpr int kStage = kRows * 64;
-  static constexpr int kRaw = 4 * kStage, kCooked = kRaw + kRawPieces * kWaves * 1024;
-  static constexpr int kRowsAt = kCooked + kRows * 16;
-  static constexpr int kOutStride = NT * 32 + 4;  // floats
-  static constexpr int kBiasAt = kWaves * 32 * kOutStride * 4;
-  static constexpr int kLds = kRowsAt + TM * 4;
-  static_assert(kRows % (16 * kWaves) == 0 && kBiasAt + TN * 4 <= kRowsAt, "whole pieces; room for the epilogue");
-  static_assert(kLds <= 160 * 1024, "LDS of a CU");
+  static constexpr int kSlot = TM * 128;  // a stage of activations
+  static constexpr int kScalePieces = kRows * 3 / 64;  // 1 KB pieces of a window of scale bytes
+  static constexpr int kRawAt = 2 * kSlot;             // a window as it comes
+  static constexpr int kScalesAt = kRawAt + kRows * 48;  // eight stages' words: [stage][row][half]
+  static constexpr int kBiasAt = kScalesAt + 8 * kRows * 8;
+  static constexpr int kRowsAt = kBiasAt + TN * 4;
+  static constexpr int kSrcAt = kRowsAt + TM * 4;
+  static constexpr int kLds = kSrcAt + TM * 4;
+  static_assert(kRows * 3 % 64 == 0, "whole pieces");
+  static_assert(kLds <= 80 * 1024, "half the LDS of a CU");
 };
 
 template <int MT, int NT, int OUT>
-__global__ __launch_bounds__(256, 1) void fp4_tile_kernel(Fp4MatmulArgs a, int vec) {
+__global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4MatmulArgs a, int vec) {
   using S = TileShape<MT, NT>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  int* const rows_lds = reinterpret_cast<int*>(lds + S::kRowsAt);
-  // the array's offset in the workgroup's LDS
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  float* const bias_lds = reinterpret_cast<float*>(lds + S::kBiasAt);
+  int* const rows_lds = reinterpret_cast<int*>(lds + S::kRowsAt);  // the tile's routed rows, -1 if none
+  int* const src_lds = reinterpret_cast<int*>(lds + S::kSrcAt);    // X's rows that they read
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -306,255 +360,301 @@ __global__ __launch_bounds__(256, 1) void fp4_tile_kernel(Fp4MatmulArgs a, int v
   Fp4Tile t;
   if (!find_tile<S::TM>(a, (a.N + S::TN - 1) / S::TN, lane, t)) return;
   const int KB = a.K >> 5;
-  const int stages = (KB + 3) >> 2;
+  const int last = (KB - 1) >> 3;  // the last stage
   const int n0 = t.nt * S::TN;
 
-  for (int i = tid; i < S::TM; i += S::kThreads) rows_lds[i] = routed_row(a, t.p0 + i, t.f);
-  __syncthreads();
+  // this wave's weight rows (past N: the last one, whose products are not stored)
+  const int wn0 = min(n0 + wave * NT * 32, a.N - 1);
+  const int wrows = min(a.N - wn0, NT * 32);
+  const __amdgpu_buffer_rsrc_t wsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(a.w + ((size_t)t.e * a.N + wn0) * KB * 16), (short)0, wrows * KB * 16, 0x00020000);
+  int woff[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+      woff[n][u] = min(32 * n + 16 * u + (lane & 15), wrows - 1) * (KB * 16) + (lane >> 4) * 16;
+  u32x4_t w[2][NT][4];
+  // piece i of a stage's 4 NT: sub-tile i / 4, blocks 4 (i / 2 % 2) .. + 3, rows 16 (i % 2) .. + 15;
+  // past K the next row's codes or none
+  auto load_w = [&](int s, int i) {
+    return __builtin_amdgcn_raw_buffer_load_b128(wsrc, woff[i >> 2][i & 1], min(s, last) * 128 + 32 * (i & 2), 0);
+  };
+  // the rows and the bias first: the barrier waits for them, not for the weights
+  static_assert(S::TM <= S::kThreads, "a row a thread");
+  const int row0 = tid < S::TM ? routed_row(a, t.p0 + tid, t.f) : -1;
+  uint32_t bias0[(S::TN + S::kThreads - 1) / S::kThreads];
+#pragma unroll
+  for (int i = 0; i * S::kThreads < S::TN; i++)
+    bias0[i] = a.bias ? a.bias[(size_t)t.e * a.N + min(n0 + tid + i * S::kThreads, a.N - 1)] : 0;
+  pipeline_fence();
+#pragma unroll
+  for (int i = 0; i < 4 * NT; i++) w[0][i >> 2][i & 3] = load_w(0, i);
+  pipeline_fence();
+  if (tid < S::TM) {
+    rows_lds[tid] = row0;
+    // rows past the end read a valid one, whose products are not stored
+    src_lds[tid] = row0 < 0 ? 0 : a.x_div == 1 ? row0 : row0 / a.x_div;
+  }
+#pragma unroll
+  for (int i = 0; i * S::kThreads < S::TN; i++)
+    if (tid + i * S::kThreads < S::TN) bias_lds[tid + i * S::kThreads] = bf16_bits_to_f32(bias0[i]);
+  lds_barrier();
 
-  // tile row i: X's row of position i (i < TM), then W's row n0 + i - TM; rows
-  // past the end read a valid one, whose products are not stored
-  auto tile_row = [&](int i) -> size_t {
-    if (i < S::TM) {
-      const int r = rows_lds[i];
-      return r < 0 ? 0 : a.x_div == 1 ? r : r / a.x_div;
+  // activations: a wave brings MT pieces of 8 rows; lane l brings row l / 8's LDS
+  // place l % 8, the block place ^ row_swizzle(row)
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const int xblk = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+  const int* const x_src = src_lds + 8 * wave + (lane >> 3);
+  auto x_piece = [&](int s, int slot, int p) {
+    const int off = min(8 * s + xblk, KB - 1) * 16;  // blocks past K: the last one, masked later
+    dma16(a.x + (size_t)(uint32_t)x_src[32 * p] * (uint32_t)(KB * 16) + off,
+          lds0 + slot * S::kSlot + (wave + S::kWaves * p) * 1024);
+  };
+  auto bring_x = [&](int s, int slot) {
+#pragma unroll
+    for (int p = 0; p < MT; p++) x_piece(min(s, last), slot, p);
+  };
+  bring_x(0, 0);
+
+  // scales: tile row i is X's (i < TM), then W's row n0 + i - TM.  Piece c of the
+  // window's kRows x 3 goes to its place in order; a piece past the row's last
+  // byte reads the one with that byte again.
+  auto scale_row = [&](int i) -> uintptr_t {
+    return i < S::TM ? reinterpret_cast<uintptr_t>(a.xs) + (size_t)(uint32_t)src_lds[i] * (uint32_t)KB
+                     : reinterpret_cast<uintptr_t>(a.ws + (size_t)t.e * a.N * KB) +
+                           (size_t)(uint32_t)min(n0 + i - S::TM, a.N - 1) * (uint32_t)KB;
+  };
+  auto bring_scales = [&](int v) {
+#pragma unroll 1
+    for (int p = wave; p < S::kScalePieces; p += S::kWaves) {
+      const int c = 64 * p + lane;
+      const int i = c / 3;
+      const uintptr_t row = scale_row(i);
+      const uintptr_t at = min((row & ~(uintptr_t)15) + 32 * v + 16 * (c - 3 * i), (row + KB - 1) & ~(uintptr_t)15);
+      dma16(reinterpret_cast<const void*>(at), lds0 + S::kRawAt + p * 1024);
     }
-    return (size_t)t.e * a.N + min(n0 + i - S::TM, a.N - 1);
   };
-  // codes: piece p holds rows 16 p .. + 15; lane l brings row l / 4's LDS slot l % 4
-  const int slot = (lane & 3) ^ ((lane >> 3) & 3);
-  const uint8_t* src[S::kPieces];
+  bring_scales(0);
+  auto put_scales = [&](int v) {
+#pragma unroll 1
+    for (int i = tid; i < S::kRows; i += S::kThreads) {
+      const int shift = (int)(scale_row(i) & 15);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(lds + S::kRawAt + i * 48 + (shift & ~3));
+      uint32_t r[9], d[8];
 #pragma unroll
-  for (int p = 0; p < S::kPieces; p++) {
-    const int i = 16 * (wave + S::kWaves * p) + (lane >> 2);
-    src[p] = (i < S::TM ? a.x : a.w) + tile_row(i) * KB * 16;
-  }
-  auto bring = [&](int s, int buf, int p) {
-    const int off = min(4 * s + slot, KB - 1) * 16;  // blocks past K: the last one, masked when multiplied
-    dma16(src[p] + off, lds0 + buf * S::kStage + (wave + S::kWaves * p) * 1024);
-  };
-  // scales: piece p holds rows 32 p .. + 31; lane l brings 16-byte piece l % 2 of row l / 2
-  const uint8_t* raw_src[S::kRawPieces];  // the group's first, aligned
-  int raw_last[S::kRawPieces];            // from it to the piece with the row's last byte
+      for (int j = 0; j < 9; j++) r[j] = q[j];
 #pragma unroll
-  for (int p = 0; p < S::kRawPieces; p++) {
-    const int i = min(32 * (wave + S::kWaves * p) + (lane >> 1), S::kRows - 1);
-    const uintptr_t row = reinterpret_cast<uintptr_t>(i < S::TM ? a.xs : a.ws) + tile_row(i) * KB;
-    raw_src[p] = reinterpret_cast<const uint8_t*>(row & ~(uintptr_t)15);
-    raw_last[p] = (int)(((row + KB - 1) & ~(uintptr_t)15) - (row & ~(uintptr_t)15));
-  }
-  auto bring_scales = [&](int g, int p) {
-    dma16(raw_src[p] + min(16 * (g + (lane & 1)), raw_last[p]), lds0 + S::kRaw + (wave + S::kWaves * p) * 1024);
-  };
-  int shift[S::kCook];
+      for (int j = 0; j < 8; j++) d[j] = __builtin_amdgcn_alignbyte(r[j + 1], r[j], shift & 3);
 #pragma unroll
-  for (int p = 0; p < S::kCook; p++) {
-    const int i = min(tid + S::kThreads * p, S::kRows - 1);
-    shift[p] = (int)((reinterpret_cast<uintptr_t>(i < S::TM ? a.xs : a.ws) + tile_row(i) * KB) & 15);
-  }
-  // a group's scale bytes of a row into place: [half wave][8 K steps]
-  auto cook = [&]() {
-#pragma unroll
-    for (int p = 0; p < S::kCook; p++) {
-      const int i = tid + S::kThreads * p;
-      if (S::kRows % S::kThreads != 0 && i >= S::kRows) break;
-      const u32x4_t* q = reinterpret_cast<const u32x4_t*>(lds + S::kRaw + i * 32);
-      const u32x4_t lo = q[0], hi = q[1];
-      const bool by2 = shift[p] & 8, by1 = shift[p] & 4;
-      const uint32_t b[6] = {by2 ? lo.z : lo.x, by2 ? lo.w : lo.y, by2 ? hi.x : lo.z,
-                             by2 ? hi.y : lo.w, by2 ? hi.z : hi.x, by2 ? hi.w : hi.y};
-      uint32_t d[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const uint32_t d0 = by1 ? b[j + 1] : b[j];
-        const uint32_t d1 = by1 ? b[j + 2] : b[j + 1];
-        d[j] = __builtin_amdgcn_alignbyte(d1, d0, shift[p] & 3);
-      }
-      *reinterpret_cast<u32x4_t*>(lds + S::kCooked + i * 16) =
-          u32x4_t{__builtin_amdgcn_perm(d[1], d[0], 0x06040200u), __builtin_amdgcn_perm(d[3], d[2], 0x06040200u),
-                  __builtin_amdgcn_perm(d[1], d[0], 0x07050301u), __builtin_amdgcn_perm(d[3], d[2], 0x07050301u)};
+      for (int j = 0; j < 4; j++)
+        *reinterpret_cast<uint2*>(lds + S::kScalesAt + ((4 * (v & 1) + j) * S::kRows + i) * 8) =
+            make_uint2(__builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], 0x05040100u),
+                       __builtin_amdgcn_perm(d[2 * j + 1], d[2 * j], 0x07060302u));
     }
   };
 
-  const int wr0 = S::TM + wave * NT * 32;
-  const int swz = (l32 >> 1) & 3;
-  const int off0 = l32 * 64 + ((half ^ swz) << 4), off1 = l32 * 64 + (((2 + half) ^ swz) << 4);
+  const int xoff = l32 * 128 + ((2 * half ^ row_swizzle(l32)) << 4);  // block 2 half; K step j: ^ its first block << 4
 
   // The tile with its first MA sub-tiles of routed rows.
   auto run = [&](auto mac) {
     constexpr int MA = decltype(mac)::value;
+    // Lane (l32, half) holds routed row l32 of each 32 x 32 block and outputs
+    // 8 g + 4 half + i of it in element 4 g + i; the sums start at the bias.
     v16f acc[NT][MA];
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
-      for (int m = 0; m < MA; m++)
+      for (int g = 0; g < 4; g++) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(bias_lds + (wave * NT + n) * 32 + 8 * g + 4 * half);
 #pragma unroll
-        for (int i = 0; i < 16; i++) acc[n][m][i] = 0.f;
-    struct Ops {
-      u32x4_t w[NT], x[MA];
-    };
-    struct Scales {
-      uint2 w[NT], x[MA];
-    };
-    auto read = [&](Ops& o, int buf, int off) {
-      const uint8_t* b = lds + buf * S::kStage + off;
+        for (int m = 0; m < MA; m++)
 #pragma unroll
-      for (int n = 0; n < NT; n++) o.w[n] = *reinterpret_cast<const u32x4_t*>(b + (wr0 + 32 * n) * 64);
-#pragma unroll
-      for (int m = 0; m < MA; m++) o.x[m] = *reinterpret_cast<const u32x4_t*>(b + m * 2048);
-    };
-    auto read_scales = [&](Scales& c) {
-      const uint8_t* b = lds + S::kCooked + l32 * 16 + half * 8;
-#pragma unroll
-      for (int n = 0; n < NT; n++) c.w[n] = *reinterpret_cast<const uint2*>(b + (wr0 + 32 * n) * 16);
-#pragma unroll
-      for (int m = 0; m < MA; m++) c.x[m] = *reinterpret_cast<const uint2*>(b + m * 512);
-    };
-    // K step k (0 .. 7) of the group; `between` follows each MFMA
-    auto multiply = [&](const Ops& o, const Scales& c, auto kc, auto between) {
-      constexpr int k = decltype(kc)::value;
-#pragma unroll
-      for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int m = 0; m < MA; m++) {
-          acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fp4_operand(o.w[n]), fp4_operand(o.x[m]), acc[n][m], kFmtFp4, kFmtFp4, k & 3,
-              (int)(k < 4 ? c.w[n].x : c.w[n].y), k & 3, (int)(k < 4 ? c.x[m].x : c.x[m].y));
-          between(n * MA + m);
-        }
-    };
-    Ops A, Bq;
-    Scales sc;
-
-    // Stage s = 4 g + Q, in ring slot Q, with another behind it.  Its first K
-    // step is multiplied while the second's operands are read; behind the
-    // barrier (every wave has read the slot, and the next stage has arrived)
-    // the slot takes stage s + 4 and the next stage's first operands are read
-    // while the second step is multiplied.
-    auto stage = [&](int g, auto qc) {
-      constexpr int Q = decltype(qc)::value;
-      constexpr int k = 2 * Q;
-      const int s = 4 * g + Q;
-      read(Bq, Q, off1);
-      pipeline_fence();
-      multiply(A, sc, std::integral_constant<int, k>{}, [](int) {});
-      if (Q == 3) cook();
-      pipeline_fence();
-      // under way behind what the next stage needs: two stages, in the second
-      // of a group its scales too
-      wait_loads<2 * S::kPieces + (Q == 1 ? S::kRawPieces : 0)>();
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      pipeline_fence();
-      read(A, (Q + 1) & 3, off0);
-      Scales next = sc;
-      if (Q == 3) read_scales(next);
-      if (Q == 0) {
-#pragma unroll
-        for (int p = 0; p < S::kRawPieces; p++) bring_scales(g + 1, p);
+          for (int i = 0; i < 4; i++) acc[n][m][4 * g + i] = v[i];
       }
-      pipeline_fence();
-      constexpr int kEach = (S::kPieces + NT * MA - 1) / (NT * MA);
-      multiply(Bq, sc, std::integral_constant<int, k + 1>{}, [&](int i) {
+    u32x4_t x[MA];  // a K step's activations
+    struct Scales {
+      int w[NT], x[MA];
+    };
+    auto read_x = [&](int slot, int j, int m) {
+      x[m] = *reinterpret_cast<const u32x4_t*>(lds + slot * S::kSlot + (xoff ^ first_block(j) << 4) + m * 4096);
+    };
+    auto read_scales = [&](Scales& c, int s) {
+      const uint8_t* q = lds + S::kScalesAt + (s & 7) * (S::kRows * 8) + l32 * 8 + half * 4;
 #pragma unroll
-        for (int p = i * kEach; p < (i + 1) * kEach && p < S::kPieces; p++) bring(s + 4, Q, p);
-        pipeline_fence();
-      });
+      for (int n = 0; n < NT; n++) c.w[n] = *reinterpret_cast<const int*>(q + (S::TM + (wave * NT + n) * 32) * 8);
+#pragma unroll
+      for (int m = 0; m < MA; m++) c.x[m] = *reinterpret_cast<const int*>(q + m * 256);
+    };
+    // the pieces of sub-tile n, blocks 4 v .. + 3, become the operands of K steps 2 v and 2 v + 1
+    auto exchange = [&](int set, int n, int v) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const auto p = __builtin_amdgcn_permlane16_swap(w[set][n][2 * v][i], w[set][n][2 * v + 1][i], false, false);
+        w[set][n][2 * v][i] = p[0];
+        w[set][n][2 * v + 1][i] = p[1];
+      }
+    };
+    Scales sc;
+    auto multiply = [&](int set, int n, int m, auto jc) {
+      constexpr int J = decltype(jc)::value;
+      acc[n][m] =
+          __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(w[set][n][J]), fp4_operand(x[m]), acc[n][m],
+                                                          kFmtFp4, kFmtFp4, J, sc.w[n], J, sc.x[m]);
+    };
+    using J0 = std::integral_constant<int, 0>;
+    using J1 = std::integral_constant<int, 1>;
+    using J2 = std::integral_constant<int, 2>;
+    using J3 = std::integral_constant<int, 3>;
+
+    wait_loads<0>();  // the first stage's activations and window of scales
+    lds_barrier();
+    bring_x(1, 1);
+#pragma unroll
+    for (int i = 0; i < 4 * NT; i++)
+      if ((i & 2) == 0) w[1][i >> 2][i & 3] = load_w(1, i);
+    put_scales(0);
+    lds_barrier();
+    read_scales(sc, 0);
+#pragma unroll
+    for (int m = 0; m < MA; m++) read_x(0, 0, m);
+    // scale bytes of the last stage's blocks that exist
+    const int left = KB - 8 * last;
+    uint32_t kept = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) kept |= first_block(j) + 2 * half < left ? 0xffu << 8 * j : 0u;
+    auto keep_scales = [&](uint32_t mask) {
+#pragma unroll
+      for (int n = 0; n < NT; n++) sc.w[n] &= (int)mask;
+#pragma unroll
+      for (int m = 0; m < MA; m++) sc.x[m] &= (int)mask;
+    };
+    // Stage s, s % 2 = set.  Each K step goes over the wave's weight sub-tiles;
+    // behind the last one's product with a sub-tile of activations its registers
+    // take the next K step's.  The weights of the second half of stage s + 1 are
+    // asked for during the first half, those of the first half of stage s + 2
+    // during the second, into the registers that the half stage before set free.
+    // Before the last sub-tile of the last K step every wave has read the stage's
+    // slot, which then takes the activations of stage s + 2.
+    auto stage = [&](int s, auto setc) {
+      constexpr int set = decltype(setc)::value;
+      // The next window of scales: asked for at its predecessor's first stage, here
+      // with that stage's barrier, put in place in the third, read in the fourth.
+      if (set == 0 && s / 4 < (KB - 1) >> 5) {
+        if ((s & 3) == 0) bring_scales(s / 4 + 1);
+        else put_scales(s / 4 + 1);
+      }
+      Scales next;
+      exchange(set, 0, 0);
+      pipeline_fence();
+      auto step = [&](auto jc) {
+        constexpr int J = decltype(jc)::value;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          if (J == 3 && n == NT - 1) {
+            // the next stage's activations were asked for behind the last barrier;
+            // 4 NT - 1 loads of weights followed
+            wait_loads<4 * NT - 2>();
+            lds_barrier();
+            read_scales(next, s + 1);
+            pipeline_fence();
+          }
+#pragma unroll
+          for (int m = 0; m < MA; m++) {
+            multiply(set, n, m, jc);
+            if (n == NT - 1) read_x(J < 3 ? set : 1 - set, (J + 1) & 3, m);
+            if (J == 0 && m == 0 && n + 1 < NT) exchange(set, n + 1, 0);
+            if (J == 1 && m == 0) exchange(set, n, 1);
+            if (m == MA / 2) {
+              if (J < 2) w[1 - set][n][2 + (J & 1)] = load_w(s + 1, 4 * n + 2 + (J & 1));
+              else w[set][n][J & 1] = load_w(s + 2, 4 * n + (J & 1));
+            }
+            if (J == 3 && n == NT - 1) {
+#pragma unroll
+              for (int i = m * MT / MA; i < (m + 1) * MT / MA; i++) x_piece(min(s + 2, last), set, i);
+            }
+            pipeline_fence();
+          }
+        }
+      };
+      step(J0{});
+      step(J1{});
+      step(J2{});
+      step(J3{});
       sc = next;
     };
-
-#pragma unroll
-    for (int p = 0; p < S::kRawPieces; p++) bring_scales(0, p);
-#pragma unroll
-    for (int s = 0; s < 4; s++)
-#pragma unroll
-      for (int p = 0; p < S::kPieces; p++) bring(s, s, p);
-    wait_loads<4 * S::kPieces < 63 ? 4 * S::kPieces : 63>();
-    asm volatile("s_barrier" ::: "memory");
-    cook();
-    wait_loads<3 * S::kPieces>();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    read(A, 0, off0);
-    read_scales(sc);
-    const int last = stages - 1, groups = last >> 2;
-    for (int g = 0; g < groups; g++) {
-      stage(g, std::integral_constant<int, 0>{});
-      stage(g, std::integral_constant<int, 1>{});
-      stage(g, std::integral_constant<int, 2>{});
-      stage(g, std::integral_constant<int, 3>{});
+    // Stages in pairs.  A last one with an odd number goes with them, its blocks past
+    // K (which hold other rows' finite codes, or none) under scale byte 0 on both
+    // sides: products below 2^-240, that change no sum.  A last one with an even
+    // number follows, with the K steps that it has.
+    for (int s = 0; s < last; s += 2) {
+      stage(s, J0{});
+      keep_scales(s + 1 == last ? kept : ~0u);  // (no branch: with one the accumulators were spilled)
+      stage(s + 1, J1{});
     }
-    if ((last & 3) > 0) stage(groups, std::integral_constant<int, 0>{});
-    if ((last & 3) > 1) stage(groups, std::integral_constant<int, 1>{});
-    if ((last & 3) > 2) stage(groups, std::integral_constant<int, 2>{});
-    // The last stage: blocks past K are taken as zero codes under a finite scale.
-    {
-      read(Bq, last & 3, off1);
-      const int left = KB - 4 * last;
-      auto tail = [&](Ops& o, int j) {
-        const bool keep = 2 * j + half < left;
-        const int k = 2 * (last & 3) + j;
-        auto byte = [&](uint2 v) -> uint32_t {
-          const uint32_t w = (k < 4 ? v.x : v.y) >> (8 * (k & 3));
-          return keep ? w : 0u;
-        };
-        Scales c;
+    keep_scales(kept);
+    const int rest = last & 1 ? 0 : left;
+    auto tail = [&](auto jc) {
+      constexpr int J = decltype(jc)::value;
+      if (first_block(J) >= rest) return;
 #pragma unroll
-        for (int n = 0; n < NT; n++) c.w[n].x = byte(sc.w[n]);
+      for (int n = 0; n < NT; n++) {
+        if ((J & 1) == 0) exchange(0, n, J >> 1);
 #pragma unroll
         for (int m = 0; m < MA; m++) {
-          c.x[m].x = byte(sc.x[m]);
-          o.x[m] = keep ? o.x[m] : u32x4_t{0, 0, 0, 0};
+          if (J > 0 && n == 0) read_x(0, J, m);
+          multiply(0, n, m, jc);
         }
-        multiply(o, c, std::integral_constant<int, 0>{}, [](int) {});
-      };
-      tail(A, 0);
-      if (left > 2) tail(Bq, 1);
-    }
-    wait_loads<0>();  // nothing more comes into LDS
-    __syncthreads();
+      }
+    };
+    tail(J0{});
+    tail(J1{});
+    tail(J2{});
+    tail(J3{});
+    wait_loads<0>();  // nothing comes into LDS any more
 
-    // Lane (l32, half) holds routed row l32 of each 32 x 32 block and weight rows
-    // 8 g + 4 half + i: through LDS, 32 routed rows at a time, so that a store
-    // instruction writes whole runs of a row.
-    float* const ob = reinterpret_cast<float*>(lds) + wave * 32 * S::kOutStride;
-    float* const bias_lds = reinterpret_cast<float*>(lds + S::kBiasAt) + wave * NT * 32;
+    // Exchanged between the half waves, the lower one has the eight outputs
+    // 8 g .. + 7 of its row for even g, the upper one for odd g.
     const int nw = n0 + wave * NT * 32;
-    for (int i = lane; i < NT * 32; i += 64)
-      bias_lds[i] = a.bias ? bf16_bits_to_f32(a.bias[(size_t)t.e * a.N + min(nw + i, a.N - 1)]) : 0.f;
+    auto eight = [&](int n, int m, int g, float(&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[n][m][4 * g + i]),
+                                                        __float_as_uint(acc[n][m][4 * g + 4 + i]), false, false);
+        v[i] = __uint_as_float(p[0]);
+        v[4 + i] = __uint_as_float(p[1]);
+      }
+    };
+    if (vec && nw + NT * 32 <= a.N) {
+#pragma unroll
+      for (int m = 0; m < MA; m++) {
+        const int r = rows_lds[32 * m + l32];
+        uint8_t* o = out_at<OUT>(a, max(r, 0), nw + 8 * half);
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            float v[8];
+            eight(n, m, g, v);
+            if (r >= 0) store8<OUT>(o + (32 * n + 8 * g) * kOutBytes2<OUT> / 2, v);
+          }
+      }
+      return;
+    }
 #pragma unroll
     for (int m = 0; m < MA; m++) {
+      const int r = rows_lds[32 * m + l32];
 #pragma unroll
       for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int g = 0; g < 4; g++)
-          *reinterpret_cast<f32x4_t*>(ob + l32 * S::kOutStride + 32 * n + 8 * g + 4 * half) =
-              f32x4_t{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
-      __builtin_amdgcn_wave_barrier();
-      constexpr int kChunks = NT * 4;  // 8 columns each
+        for (int g = 0; g < 4; g += 2) {
+          float v[8];
+          eight(n, m, g, v);
+          if (r >= 0) {
 #pragma unroll
-      for (int it = 0; it < 32 * kChunks / 64; it++) {
-        const int idx = it * 64 + lane;
-        const int row = idx / kChunks, cc = idx % kChunks;
-        const int r = rows_lds[32 * m + row];
-        const int n = nw + 8 * cc;
-        float v[8];
-        const f32x4_t v0 = *reinterpret_cast<const f32x4_t*>(ob + row * S::kOutStride + 8 * cc);
-        const f32x4_t v1 = *reinterpret_cast<const f32x4_t*>(ob + row * S::kOutStride + 8 * cc + 4);
-        const f32x4_t b0 = *reinterpret_cast<const f32x4_t*>(bias_lds + 8 * cc);
-        const f32x4_t b1 = *reinterpret_cast<const f32x4_t*>(bias_lds + 8 * cc + 4);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          v[i] = v0[i] + b0[i];
-          v[4 + i] = v1[i] + b1[i];
+            for (int i = 0; i < 8; i += 2) store_pair<OUT>(a, r, nw + 32 * n + 8 * (g + half) + i, v[i], v[i + 1]);
+          }
         }
-        if (r < 0 || n >= a.N) continue;
-        if (vec) {
-          store8<OUT>(a, r, n, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) store_pair<OUT>(a, r, n + i, v[i], v[i + 1]);
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
     }
   };
   const int subs = (min(t.f - t.p0, S::TM) + 31) >> 5;
@@ -590,7 +690,7 @@ template <int OUT>
 hipError_t launch_out(const Fp4MatmulArgs& a, hipStream_t stream) {
   const long long groups = a.offsets ? min(a.E, a.R) : 1;
   if (a.R <= 16 * groups) return launch_rows<OUT>(a, stream);
-  return launch_tiles<4, 3, OUT>(a, stream);
+  return launch_tiles<4, 2, OUT>(a, stream);
 }
 
 }  // namespace
