@@ -664,16 +664,22 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4MatmulArgs a, int v
   else run(std::integral_constant<int, 1>{});
 }
 
+// At most so many tiles: R / TM whole row tiles and one broken one for each expert
+// with rows.
+template <int MT, int NT>
+long long tiles(const Fp4MatmulArgs& a) {
+  using S = TileShape<MT, NT>;
+  const long long mt = a.offsets ? a.R / S::TM + (long long)min(a.E, a.R) : ((long long)a.R + S::TM - 1) / S::TM;
+  return mt * ((a.N + S::TN - 1) / S::TN);
+}
+
 template <int MT, int NT, int OUT>
 hipError_t launch_tiles(const Fp4MatmulArgs& a, hipStream_t stream) {
   using S = TileShape<MT, NT>;
   static DynLdsLimit limit(reinterpret_cast<const void*>(fp4_tile_kernel<MT, NT, OUT>), S::kLds);
   const hipError_t e = limit.ensure();
   if (e != hipSuccess) return e;
-  // at most R / TM whole row tiles and one broken one for each expert with rows
-  const long long mt = a.offsets ? a.R / S::TM + (long long)min(a.E, a.R) : ((long long)a.R + S::TM - 1) / S::TM;
-  const long long tiles = mt * ((a.N + S::TN - 1) / S::TN);
-  const long long grid = (tiles + kXcds - 1) / kXcds * kXcds;
+  const long long grid = (tiles<MT, NT>(a) + kXcds - 1) / kXcds * kXcds;
   const int vec = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   hipLaunchKernelGGL((fp4_tile_kernel<MT, NT, OUT>), dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a, vec);
   return hipGetLastError();
@@ -688,8 +694,20 @@ hipError_t launch_rows(const Fp4MatmulArgs& a, hipStream_t stream) {
 
 template <int OUT>
 hipError_t launch_out(const Fp4MatmulArgs& a, hipStream_t stream) {
+  // Few rows an expert: 16 x 16 blocks that stream the weights (16 rows of 5760 x
+  // 2880: 5.4 us against 8.4 in the smallest tiles; 17 rows 9.0 against 8.4; 64 routed
+  // rows over 32 experts 66 us against 73, 128 rows 80 against 74).
   const long long groups = a.offsets ? min(a.E, a.R) : 1;
-  if (a.R <= 16 * groups) return launch_rows<OUT>(a, stream);
+  if (a.R <= (a.offsets ? 2 * groups : 16)) return launch_rows<OUT>(a, stream);
+  // Then the smallest tiles that give no CU two workgroups, for a tile's time
+  // hardly depends on how many run (17 to 256 rows of 5760 x 2880: 64 x 128 tiles 8.4
+  // to 9.8 us, 128 x 128 9.6 to 12.0, 128 x 256 12.7 to 17.0; 1024 rows: 24.6, 21.0,
+  // 19.8); and the smallest where an expert has few rows (1024 routed rows over 32
+  // experts of 5760 x 2880: 84 us in 64 x 128 tiles, 87 in 128 x 256; 2048 rows 119 and
+  // 96).
+  constexpr long long kCus = 256;
+  if (tiles<2, 1>(a) <= kCus || (a.offsets && a.R <= 32 * groups)) return launch_tiles<2, 1, OUT>(a, stream);
+  if (tiles<4, 1>(a) <= kCus) return launch_tiles<4, 1, OUT>(a, stream);
   return launch_tiles<4, 2, OUT>(a, stream);
 }
 
