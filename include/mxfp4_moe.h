@@ -66,6 +66,10 @@ typedef enum {
 #define MXFP4_DECODE_MAX_K 3072      /* mxfp4_moe_decode: all of a row's loads in flight at once */
 #define MXFP4_DECODE_MAX_T 64        /* mxfp4_moe_decode_batch: tokens ranked one per lane */
 
+#define MXFP4_LAYER_MAX_T 16         /* mxfp4_moe_layer: tokens */
+#define MXFP4_LAYER_MAX_TOPK 16
+#define MXFP4_LAYER_MAX_N 8192       /* mxfp4_moe_layer: H and F */
+#define MXFP4_LAYER_MAX_TN 65536     /* mxfp4_moe_layer: T * H and T * F, rows kept in LDS */
 #define MOE_NORM_MAX_N 16384         /* the norms: a row stays in one workgroup's registers */
 #define MOE_MAX_TOKENS (1 << 30)     /* the norms, moe_balance, moe_route_backward */
 #define MOE_MAX_SEQUENCES (1 << 20)  /* moe_balance, moe_route_backward */
@@ -525,6 +529,44 @@ int mxfp4_expert_matmul_swiglu(const uint8_t* blocks, const uint8_t* scales, con
                                int K, const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
                                const int32_t* expert_offsets, const int32_t* sorted_rows, uint16_t* act,
                                void* stream);
+
+/* Workspace bytes of mxfp4_moe_layer; (size_t)-1 for invalid sizes. */
+size_t mxfp4_moe_layer_workspace_size(int T, int H, int E, int k, int F);
+
+/*
+ * A whole expert layer for a few decoded tokens in two launches: moe_norm,
+ * mxfp4_moe_router, the routing, mxfp4_expert_proj_swiglu, mxfp4_expert_proj and
+ * the combine with the residual.
+ *
+ *   x       [T, H] bf16 or fp32 (x_dtype): the residual stream, or with w_norm
+ *           NULL the normed rows themselves (bf16 only).
+ *   w_norm  [H] bf16, or NULL; eps > 0 where it is given.  xn as moe_norm writes it.
+ *   router_w [E, H] bf16, router_b [E] bf16 or NULL: logits = xn . router_w^T +
+ *           router_b in fp32, not rounded.  A token's k largest logits are its
+ *           experts (the lower index of equals), the softmax over them its gates.
+ *   gu_blocks, gu_scales, gu_bias: [E, 2 F, H] MXFP4 as mxfp4_expert_proj_swiglu
+ *           takes it (rows 2 i and 2 i + 1 gate and up), the bias [E, 2 F] bf16 or
+ *           NULL.  down_blocks, down_scales, down_bias: [E, H, F] and [E, H].
+ *           Exact weights times bf16 activations summed in fp32; the activation
+ *           between the two is rounded to bf16.
+ *   residual != 0: x is added to the sum (in fp32, before its one rounding).
+ *   y       [T, H] bf16 or fp32 (y_dtype) out.  y may be x (of the same type).
+ *   topk_ids [T, k] i32, gates [T, k] fp32 out, each or NULL.
+ *   0 <= T <= MXFP4_LAYER_MAX_T, 1 <= E <= MXFP4_DECODE_MAX_EXPERTS,
+ *   1 <= k <= min(E, MXFP4_LAYER_MAX_TOPK), H and F multiples of 32 in
+ *   32..MXFP4_LAYER_MAX_N, T * H and T * F <= MXFP4_LAYER_MAX_TN.
+ *   workspace: mxfp4_moe_layer_workspace_size bytes, 16-byte aligned, the call's own
+ *           until it is done.
+ * x, w_norm, router_w and the two blocks 16-byte aligned.  A token with a logit that
+ * is NaN or +infinity reaches no expert: its ids are -1, its gates 0 and its y the
+ * residual (or 0).  As in moe_combine a slot with gate 0 adds nothing.  T = 0 returns
+ * MXFP4_OK and enqueues nothing.
+ */
+int mxfp4_moe_layer(const void* x, int x_dtype, int T, int H, int E, int k, int F, const uint16_t* w_norm, float eps,
+                    const uint16_t* router_w, const uint16_t* router_b, const uint8_t* gu_blocks,
+                    const uint8_t* gu_scales, const uint16_t* gu_bias, const uint8_t* down_blocks,
+                    const uint8_t* down_scales, const uint16_t* down_bias, int residual, void* y, int y_dtype,
+                    int32_t* topk_ids, float* gates, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Gate-weighted combine of the k projections of each token.

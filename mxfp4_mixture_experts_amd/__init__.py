@@ -17,7 +17,7 @@ __all__ = ["mxfp4_moe_route_group", "mxfp4_expert_proj", "mxfp4_expert_proj_work
            "moe_combine_norm_backward", "moe_combine_norm_backward_workspace_size", "moe_balance",
            "moe_balance_workspace_size", "moe_route_backward",
            "mxfp4_quantize", "mxfp4_quantize_transposed", "mxfp4_matmul", "mxfp4_expert_matmul",
-           "mxfp4_expert_matmul_swiglu",
+           "mxfp4_expert_matmul_swiglu", "mxfp4_moe_layer", "mxfp4_moe_layer_workspace_size",
            "library_path"]
 
 

@@ -58,6 +58,8 @@ ENTRY_POINTS = (
     "mxfp4_matmul",
     "mxfp4_expert_matmul",
     "mxfp4_expert_matmul_swiglu",
+    "mxfp4_moe_layer_workspace_size",
+    "mxfp4_moe_layer",
 )
 
 _lib_handle = None
@@ -140,8 +142,12 @@ def load_library():
     lib.mxfp4_matmul.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp]
     lib.mxfp4_expert_matmul.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp]
     lib.mxfp4_expert_matmul_swiglu.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.mxfp4_moe_layer_workspace_size.restype = sz
+    lib.mxfp4_moe_layer_workspace_size.argtypes = [i32] * 5
+    lib.mxfp4_moe_layer.argtypes = [vp, i32, i32, i32, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp,
+                                    i32, vp, i32, vp, vp, vp, sz, vp]
     for name in ("mxfp4_quantize", "mxfp4_quantize_transposed", "mxfp4_matmul", "mxfp4_expert_matmul",
-                 "mxfp4_expert_matmul_swiglu"):
+                 "mxfp4_expert_matmul_swiglu", "mxfp4_moe_layer"):
         getattr(lib, name).restype = i32
     for name in ("moe_norm", "moe_norm_backward", "moe_combine_norm", "moe_combine_norm_backward", "moe_balance",
                  "moe_route_backward"):
@@ -714,3 +720,35 @@ def mxfp4_expert_matmul_swiglu(blocks, scales, bias, E: int, N: int, K: int, x_b
     _run(lib.mxfp4_expert_matmul_swiglu, dev, stream,
          *_expert_args(blocks, scales, bias, E, N, K, x_blocks, x_scales, x_per_slot, T, k, expert_offsets,
                        sorted_rows, dev), _arg(act, "act", _BF16, T * k * (N // 2), dev))
+
+
+def mxfp4_moe_layer_workspace_size(T: int, H: int, E: int, k: int, F: int) -> int:
+    T, H, E, k, F = int(T), int(H), int(E), int(k), int(F)
+    _sizes32(T, H, E, k, F)
+    return _size(load_library().mxfp4_moe_layer_workspace_size(T, H, E, k, F), "mxfp4_moe_layer")
+
+
+def mxfp4_moe_layer(x, T: int, H: int, E: int, k: int, F: int, router_w, router_b, gu_blocks, gu_scales, gu_bias,
+                    down_blocks, down_scales, down_bias, y, w_norm=None, eps: float = 1e-5, residual: bool = False,
+                    topk_ids=None, gates=None, workspace=None, stream=None):
+    """A whole expert layer for a few tokens (mxfp4_moe_layer): norm (w_norm [H] bf16; None: x is
+    normed), router (router_w [E,H], router_b [E] bf16), gate/up [E,2F,H] and down [E,H,F] experts in
+    MXFP4 with bf16 biases, combine and with `residual` + x.  x [T,H] bf16 or (with w_norm) f32, y
+    [T,H] bf16 or f32, topk_ids [T,k] i32 and gates [T,k] f32 out; the biases, topk_ids and gates may
+    be None.  workspace: a uint8 device tensor of at least
+    mxfp4_moe_layer_workspace_size(T, H, E, k, F) bytes, 16-byte aligned."""
+    lib = load_library()
+    T, H, E, k, F = int(T), int(H), int(E), int(k), int(F)
+    if T >> 31 or H >> 31 or E >> 31 or k >> 31 or F >> 31:
+        _sizes32(T, H, E, k, F)
+    dev = _device_of(y, "y")
+    xt, yt = _dtype(x, "x"), _dtype(y, "y")
+    ws, nbytes = _workspace(workspace, dev)
+    _run(lib.mxfp4_moe_layer, dev, stream, _arg(x, "x", _ELEMENTS[xt], T * H, dev), xt, T, H, E, k, F,
+         _arg(w_norm, "w_norm", _BF16, H, dev), float(eps), _arg(router_w, "router_w", _BF16, E * H, dev),
+         _arg(router_b, "router_b", _BF16, E, dev), _arg(gu_blocks, "gu_blocks", _U8, E * F * H, dev),
+         _arg(gu_scales, "gu_scales", _U8, E * F * H // 16, dev), _arg(gu_bias, "gu_bias", _BF16, E * 2 * F, dev),
+         _arg(down_blocks, "down_blocks", _U8, E * H * F // 2, dev),
+         _arg(down_scales, "down_scales", _U8, E * H * F // 32, dev), _arg(down_bias, "down_bias", _BF16, E * H, dev),
+         int(bool(residual)), _arg(y, "y", _ELEMENTS[yt], T * H, dev), yt,
+         _arg(topk_ids, "topk_ids", _I32, T * k, dev), _arg(gates, "gates", _F32, T * k, dev), ws, nbytes)

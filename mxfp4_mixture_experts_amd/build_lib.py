@@ -19,7 +19,8 @@ LIB_NAME = "libmxfp4_moe.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["route_group.hip", "expert_gemv.hip", "expert_gemm.hip", "combine.hip", "dequantize.hip", "router.hip",
-           "block_norm.hip", "balance.hip", "quantize.hip", "fp4_matmul.hip", "capi.cpp"]
+           "block_norm.hip", "balance.hip", "quantize.hip", "fp4_matmul.hip",
+           "moe_layer.hip", "capi.cpp"]
 ARCH = "gfx950"
 
 

@@ -769,4 +769,81 @@ int mxfp4_expert_matmul_swiglu(const uint8_t* blocks, const uint8_t* scales, con
                             sorted_rows, act, mxfp4::kFp4OutSwiglu, stream);
 }
 
+static int check_layer_sizes(int T, int H, int E, int k, int F) {
+  if (T < 0 || T > MXFP4_LAYER_MAX_T)
+    return fail(MXFP4_ERR_INVALID_ARG, "T = %d out of range [0, %d]", T, MXFP4_LAYER_MAX_T);
+  if (E < 1 || E > MXFP4_DECODE_MAX_EXPERTS)
+    return fail(MXFP4_ERR_INVALID_ARG, "E = %d out of range [1, %d]", E, MXFP4_DECODE_MAX_EXPERTS);
+  if (k < 1 || k > E || k > MXFP4_LAYER_MAX_TOPK)
+    return fail(MXFP4_ERR_INVALID_ARG, "k = %d out of range [1, min(E, %d)]", k, MXFP4_LAYER_MAX_TOPK);
+  if (H < 32 || H > MXFP4_LAYER_MAX_N || H % 32 || F < 32 || F > MXFP4_LAYER_MAX_N || F % 32)
+    return fail(MXFP4_ERR_INVALID_ARG, "H = %d and F = %d must be multiples of 32 in [32, %d]", H, F,
+                MXFP4_LAYER_MAX_N);
+  if (T * H > MXFP4_LAYER_MAX_TN || T * F > MXFP4_LAYER_MAX_TN)
+    return fail(MXFP4_ERR_INVALID_ARG, "T * H and T * F must not pass %d", MXFP4_LAYER_MAX_TN);
+  return MXFP4_OK;
+}
+
+size_t mxfp4_moe_layer_workspace_size(int T, int H, int E, int k, int F) {
+  g_last_error[0] = '\0';
+  if (check_layer_sizes(T, H, E, k, F) != MXFP4_OK) return (size_t)-1;
+  return mxfp4::moe_layer_workspace_bytes(T, k, F);
+}
+
+int mxfp4_moe_layer(const void* x, int x_dtype, int T, int H, int E, int k, int F, const uint16_t* w_norm, float eps,
+                    const uint16_t* router_w, const uint16_t* router_b, const uint8_t* gu_blocks,
+                    const uint8_t* gu_scales, const uint16_t* gu_bias, const uint8_t* down_blocks,
+                    const uint8_t* down_scales, const uint16_t* down_bias, int residual, void* y, int y_dtype,
+                    int32_t* topk_ids, float* gates, void* workspace, size_t workspace_bytes, void* stream) {
+  static_assert(MXFP4_LAYER_MAX_T == mxfp4::kLayerMaxT && MXFP4_LAYER_MAX_TOPK == mxfp4::kLayerMaxTopK &&
+                    MXFP4_LAYER_MAX_N == mxfp4::kLayerMaxN && MXFP4_LAYER_MAX_TN == mxfp4::kLayerMaxTN,
+                "the launcher's LDS is sized by these");
+  g_last_error[0] = '\0';
+  int st = check_layer_sizes(T, H, E, k, F);
+  if (st != MXFP4_OK) return st;
+  if (!known_dtype(x_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "x_dtype = %d unknown", x_dtype);
+  if (!known_dtype(y_dtype)) return fail(MXFP4_ERR_INVALID_ARG, "y_dtype = %d unknown", y_dtype);
+  if (!w_norm && x_dtype != MXFP4_DTYPE_BF16)
+    return fail(MXFP4_ERR_INVALID_ARG, "x that is normed already (w_norm NULL) must be bf16");
+  if (w_norm && (!(eps > 0.f) || eps > 3.4e38f))
+    return fail(MXFP4_ERR_INVALID_ARG, "eps = %g must be positive and finite", (double)eps);
+  if (T == 0) return MXFP4_OK;
+  if (!x || !router_w || !gu_blocks || !gu_scales || !down_blocks || !down_scales || !y)
+    return fail(MXFP4_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(w_norm) || !aligned16(router_w) || !aligned16(gu_blocks) || !aligned16(down_blocks))
+    return fail(MXFP4_ERR_INVALID_ARG, "x, w_norm, router_w and the blocks must be 16-byte aligned");
+  if (!aligned_to(router_b, 2) || !aligned_to(gu_bias, 2) || !aligned_to(down_bias, 2) || !aligned_elem(y, y_dtype) ||
+      !aligned_to(topk_ids, 4) || !aligned_to(gates, 4))
+    return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  st = check_workspace(workspace, workspace_bytes, mxfp4::moe_layer_workspace_bytes(T, k, F));
+  if (st != MXFP4_OK) return st;
+  if ((st = check_device()) != MXFP4_OK) return st;
+  mxfp4::MoeLayerArgs a{};
+  a.x = x;
+  a.w_norm = w_norm;
+  a.router_w = router_w;
+  a.router_b = router_b;
+  a.gu = gu_blocks;
+  a.gu_scales = gu_scales;
+  a.gu_bias = gu_bias;
+  a.down = down_blocks;
+  a.down_scales = down_scales;
+  a.down_bias = down_bias;
+  a.y = y;
+  a.ids = topk_ids;
+  a.gates = gates;
+  a.T = T;
+  a.H = H;
+  a.E = E;
+  a.k = k;
+  a.F = F;
+  a.eps = eps;
+  a.residual = residual != 0;
+  a.y_f32 = y_dtype == MXFP4_DTYPE_F32;
+  const hipError_t e =
+      mxfp4::launch_moe_layer(a, x_dtype == MXFP4_DTYPE_F32, workspace, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "expert layer launch");
+  return MXFP4_OK;
+}
+
 }  // extern "C"

@@ -89,6 +89,38 @@ struct Fp4MatmulArgs {
 };
 hipError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int out_kind, hipStream_t stream);
 
+// moe_layer.hip: a whole expert layer for a few tokens in two launches
+constexpr int kLayerMaxT = 16;     // = MXFP4_LAYER_MAX_T
+constexpr int kLayerMaxTopK = 16;  // = MXFP4_LAYER_MAX_TOPK
+constexpr int kLayerMaxN = 8192;   // = MXFP4_LAYER_MAX_N
+constexpr int kLayerMaxTN = 65536;  // = MXFP4_LAYER_MAX_TN
+// dynamic LDS of a launch at most: T rows of the activations (128 KB), and 16 T k bytes of outputs
+// for every 1024 of H (T ceil(H / 1024) <= 80, 20 KB)
+constexpr int kLayerLds = 148 * 1024;
+struct MoeLayerArgs {
+  const void* x;           // [T, H] bf16 or fp32
+  const uint16_t* w_norm;  // [H], or NULL: x (bf16) is normed already
+  const uint16_t* router_w;
+  const uint16_t* router_b;  // or NULL
+  const uint8_t* gu;
+  const uint8_t* gu_scales;
+  const uint16_t* gu_bias;  // or NULL
+  const uint8_t* down;
+  const uint8_t* down_scales;
+  const uint16_t* down_bias;  // or NULL
+  void* y;                    // [T, H] bf16 or fp32
+  int32_t* ids;               // [T, k], or NULL
+  float* gates;               // [T, k], or NULL
+  int T, H, E, k, F;
+  float eps;
+  bool residual, y_f32;
+  int32_t* ws_ids;  // these set by the launcher
+  float* ws_gates;
+  uint16_t* act;  // [T, k, F]
+};
+size_t moe_layer_workspace_bytes(int T, int k, int F);
+hipError_t launch_moe_layer(MoeLayerArgs a, bool x_f32, void* workspace, hipStream_t stream);
+
 // router.hip: logits [T, E] bf16 = x [T, H] . w [E, H]^T + bias (fp32 sums, rounded once)
 hipError_t launch_router(const uint16_t* x, const uint16_t* w, const uint16_t* bias, int T, int H, int E,
                          uint16_t* logits, hipStream_t stream);
