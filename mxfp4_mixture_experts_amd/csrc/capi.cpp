@@ -838,10 +838,11 @@ int mxfp4_moe_layer(const void* x, int x_dtype, int T, int H, int E, int k, int 
   a.k = k;
   a.F = F;
   a.eps = eps;
+  a.inv_H = 1.0f / (float)H;
   a.residual = residual != 0;
   a.y_f32 = y_dtype == MXFP4_DTYPE_F32;
-  const hipError_t e =
-      mxfp4::launch_moe_layer(a, x_dtype == MXFP4_DTYPE_F32, workspace, static_cast<hipStream_t>(stream));
+  a.x_f32 = x_dtype == MXFP4_DTYPE_F32;
+  const hipError_t e = mxfp4::launch_moe_layer(a, workspace, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "expert layer launch");
   return MXFP4_OK;
 }

@@ -33,7 +33,6 @@
 
 #include "kernels.h"
 #include "common.h"
-#include "fp4_dot.h"
 #include "mxfp4_moe.h"
 #include "route_common.h"
 
@@ -644,6 +643,29 @@ struct T1Shape {
 
 // Routing parameters of the fused single-token decode: the token's router
 // logits in, the routing outputs (written by workgroup (0, 0)) out.
+// One MXFP4 block's 32 products with 32 staged bf16 inputs, added to a: the
+// block's four code words w (8 codes each) become exact bf16 weights through
+// v_cvt_scalef32_pk_bf16_fp4 with the E8M0 factor sf, and v_dot2_f32_bf16
+// multiplies them by the inputs x0 .. x3 (8 each) and sums in fp32, in element
+// order.  keep = 0 zeroes the block (a block past K).
+__device__ __forceinline__ float block_dot(const uint4 w, uint32_t keep, float sf, const uint4 x0, const uint4 x1,
+                                           const uint4 x2, const uint4 x3, float a) {
+  const uint32_t wd[4] = {w.x & keep, w.y & keep, w.z & keep, w.w & keep};
+  const uint4 xv[4] = {x0, x1, x2, x3};
+#pragma unroll
+  for (int d = 0; d < 4; d++) {
+    a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wd[d], sf, 0),
+                                        __builtin_bit_cast(bf16x2_t, xv[d].x), a, false);
+    a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wd[d], sf, 1),
+                                        __builtin_bit_cast(bf16x2_t, xv[d].y), a, false);
+    a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wd[d], sf, 2),
+                                        __builtin_bit_cast(bf16x2_t, xv[d].z), a, false);
+    a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wd[d], sf, 3),
+                                        __builtin_bit_cast(bf16x2_t, xv[d].w), a, false);
+  }
+  return a;
+}
+
 // FUSED: the workgroup routes the token itself (E <= 64) instead of reading
 // expert offsets: every lane e counts the experts whose logit beats its own
 // (a larger logit, or an equal one at a lower index), the k with count < k

@@ -94,9 +94,9 @@ constexpr int kLayerMaxT = 16;     // = MXFP4_LAYER_MAX_T
 constexpr int kLayerMaxTopK = 16;  // = MXFP4_LAYER_MAX_TOPK
 constexpr int kLayerMaxN = 8192;   // = MXFP4_LAYER_MAX_N
 constexpr int kLayerMaxTN = 65536;  // = MXFP4_LAYER_MAX_TN
-// dynamic LDS of a launch at most: T rows of the activations (128 KB), and 16 T k bytes of outputs
-// for every 1024 of H (T ceil(H / 1024) <= 80, 20 KB)
-constexpr int kLayerLds = 148 * 1024;
+// dynamic LDS of the two launches at most: T rows of H or F (128 KB) with their padding (T 16 bytes),
+// and in the first 1536 T bytes of partial sums
+constexpr int kLayerUpLds = 156 * 1024, kLayerDownLds = 136 * 1024;
 struct MoeLayerArgs {
   const void* x;           // [T, H] bf16 or fp32
   const uint16_t* w_norm;  // [H], or NULL: x (bf16) is normed already
@@ -112,14 +112,15 @@ struct MoeLayerArgs {
   int32_t* ids;               // [T, k], or NULL
   float* gates;               // [T, k], or NULL
   int T, H, E, k, F;
-  float eps;
-  bool residual, y_f32;
-  int32_t* ws_ids;  // these set by the launcher
-  float* ws_gates;
-  uint16_t* act;  // [T, k, F]
+  float eps, inv_H;  // 1 / H
+  bool x_f32, residual, y_f32;
+  int32_t* ws_experts;  // [3, 64] the experts with tokens, their tokens as bits, their rows' end; these set
+  float* ws_gates;      // [T, 64] by expert                                      by the launcher
+  int32_t* ws_ids;      // [T, k], -1 for a token that reaches no expert
+  uint16_t* act;        // [T k, F] expert by expert, token by token
 };
 size_t moe_layer_workspace_bytes(int T, int k, int F);
-hipError_t launch_moe_layer(MoeLayerArgs a, bool x_f32, void* workspace, hipStream_t stream);
+hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream);
 
 // router.hip: logits [T, E] bf16 = x [T, H] . w [E, H]^T + bias (fp32 sums, rounded once)
 hipError_t launch_router(const uint16_t* x, const uint16_t* w, const uint16_t* bias, int T, int H, int E,

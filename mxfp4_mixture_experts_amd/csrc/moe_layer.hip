@@ -11,373 +11,563 @@
 // at it), which costs less than a launch and its latency, and no workgroup ever
 // waits for another.
 //
-// Both launches stream the chosen experts' weights once for all tokens: a unit is 4
-// weight rows of an expert, 16 lanes a row, lane j of a row blocks j, j + 16, ... (256
-// contiguous bytes of a row a load).  The units of all chosen experts are spread
-// evenly over 256 workgroups of 12 waves, and a wave has the next unit's loads
-// under way while it multiplies.  A block becomes 32 exact bf16 weights and meets
-// each of its expert's tokens in bf16 dot products with fp32 sums; the tokens' rows
-// lie in LDS by pieces of 8 elements ([piece of a block][block]), so that 16
-// lanes' reads are contiguous.
+// Both launches stream the chosen experts' weights once for all tokens, by items of 16
+// weight rows x 4 blocks (lane: row lane % 16, block lane / 16), a wave's items in a
+// ring of registers far ahead of their use.  A block becomes 32 exact bf16 weights
+// (v_cvt_scalef32_pk_bf16_fp4) and one MFMA for each quarter of the blocks multiplies
+// them by up to 16 tokens' rows: the work of an item does not grow with the tokens.
+// K is split over the waves alike whatever the tokens are, and a token's sums hold
+// nothing of the others: its outputs are the same bits alone and in any batch.
 
 #include "kernels.h"
 #include "common.h"
-#include "fp4_dot.h"
 
 namespace mxfp4 {
 namespace {
 
-constexpr int kWaves = 12, kThreads = kWaves * 64;
-constexpr int kGroups = 256;  // workgroups: one a CU
-constexpr int kIns = 6;       // blocks a lane takes at a time: 96 blocks of a row
-constexpr int kSpan = 16 * kIns;
-constexpr int kPieces = 6;    // 8-element pieces of a router row a lane holds
-constexpr int kRouted = 3;    // router rows a wave holds
-constexpr int kMaxRows = kLayerMaxT * kLayerMaxTopK;
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ float row16_sum(float v) {  // over the 16 lanes of a row, fixed order
-  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));   // l ^ 1
-  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));   // l ^ 2
-  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));  // within 8
-  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));  // within 16
-  return v;
+constexpr int kWaves = 12, kThreads = kWaves * 64;
+constexpr int kGroups = 256;       // workgroups of the first launch: one a CU
+constexpr int kRouterRing = 15;    // router: loads of 16 rows x 32 elements in flight
+constexpr uint32_t kPast = 0x80000000u;  // an offset past every buffer: the load returns zeros
+
+// 2^(s - 127): s = 0 is the subnormal 2^-127
+__device__ __forceinline__ float e8m0_value(uint32_t s) { return __uint_as_float(max(s << 23, 0x00400000u)); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 __device__ __forceinline__ float lane_value(float v, int l) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
+__device__ __forceinline__ float row16_total(float v) {  // of the 16 lanes of a row, in a fixed order
+  v += dpp<0xB1>(v);    // l ^ 1
+  v += dpp<0x4E>(v);    // l ^ 2
+  v += dpp<0x141>(v);   // within 8
+  v += dpp<0x140>(v);   // within 16
+  return v;
+}
 __device__ __forceinline__ float wave_total(float v) {
-  v = row16_sum(v);
+  v = row16_total(v);
   return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 __device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true)));
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true)));
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true)));
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true)));
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  v = fmaxf(v, dpp<0x141>(v));
+  v = fmaxf(v, dpp<0x140>(v));
   return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
 }
 
-// One lane's blocks of a unit: the four weight rows are 16 lanes each.
-struct Unit {
-  uint4 w[kIns];
-  uint32_t s[kIns];
+// 16 weight rows x 4 blocks times the 16 tokens' inputs of those blocks, added to acc
+__device__ __forceinline__ f32x4_t item_mma(const u32x4_t w, uint32_t scale, const uint4* x, f32x4_t acc) {
+  const float sf = e8m0_value(scale);
+#pragma unroll
+  for (int d = 0; d < 4; d++) {
+    const bf16x2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[d], sf, 0);
+    const bf16x2_t a1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[d], sf, 1);
+    const bf16x2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[d], sf, 2);
+    const bf16x2_t a3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[d], sf, 3);
+    const bf16x8_t a = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[d]), acc, 0, 0, 0);
+  }
+  return acc;
+}
+
+// A wave's part of a unit's K: C items held in registers; each is loaded again, for the next
+// unit, as soon as it is used.
+template <int C>
+struct Stream {
+  u32x4_t w[C];
+  uint32_t s[C];
+  __amdgpu_buffer_rsrc_t wsrc, ssrc;  // the unit's 16 rows; of no bytes if there is none: zeros
+  __device__ __forceinline__ void open(const uint8_t* blocks, const uint8_t* scales, size_t first_row, int KB,
+                                       bool any) {
+    wsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(blocks + first_row * KB * 16), (short)0,
+                                             any ? 16 * KB * 16 : 0, 0x00020000);
+    ssrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales + first_row * KB), (short)0,
+                                             any ? 16 * KB : 0, 0x00020000);
+  }
+  __device__ __forceinline__ void load(int j, uint32_t w_at, uint32_t s_at) {
+    w[j] = __builtin_amdgcn_raw_buffer_load_b128(wsrc, w_at, 0, 0);
+    s[j] = __builtin_amdgcn_raw_buffer_load_b8(ssrc, s_at, 0, 0);
+  }
 };
-__device__ __forceinline__ void load_unit(Unit& u, const uint8_t* blocks, const uint8_t* scales, size_t row, int KB,
-                                          int b0, int j) {
-  const uint4* w = reinterpret_cast<const uint4*>(blocks) + row * KB;
-  const uint8_t* s = scales + row * KB;
+// Where a lane finds its blocks b, b + 4, ... of a row: in a unit's codes and scales, zeros
+// past the row, and among the row's inputs, past it the last block's.
+template <int C>
+struct Places {
+  uint32_t w[C], s[C];
+  int x[C];
+  __device__ __forceinline__ void set(int row, int b, int KB) {
 #pragma unroll
-  for (int i = 0; i < kIns; i++) {
-    const int b = min(b0 + 16 * i + j, KB - 1);  // past the row: its last block, masked when multiplied
-    u.w[i] = load_nt(w + b);
-    u.s[i] = s[b];
-  }
-}
-// sum over this lane's blocks of weights times the staged row (4 pieces of KB blocks)
-__device__ __forceinline__ float unit_dot(const Unit& u, const uint4* row, int KB, int b0, int j, float a) {
-#pragma unroll
-  for (int i = 0; i < kIns; i++) {
-    const int b = b0 + 16 * i + j;
-    if (b0 + 16 * i < KB) {
-      const int c = min(b, KB - 1);
-      a = block_dot(u.w[i], b < KB ? ~0u : 0u, e8m0_value(u.s[i]), row[c], row[KB + c], row[2 * KB + c],
-                    row[3 * KB + c], a);
+    for (int j = 0; j < C; j++) {
+      const bool in = b + 4 * j < KB;
+      s[j] = in ? row * KB + b + 4 * j : kPast;
+      w[j] = in ? (row * KB + b + 4 * j) * 16 : kPast;
+      x[j] = min(b + 4 * j, KB - 1) * 4;
     }
   }
-  return a;
+};
+
+// sum of v over this lane and those below
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row shifted right by 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 to row 1, lane 47 to row 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+  return v;
 }
 
-// The experts with tokens, from slot_of[t][e] (the slot, -1 if none): their list, and
-// each one's tokens as bits.  One wave.
-__device__ __forceinline__ void list_experts(const int8_t* slot_of, int T, int E, int lane, int* list, uint32_t* tokens,
-                                             int* count) {
-  uint32_t mask = 0;
-  for (int t = 0; t < T; t++)
-    if (lane < E && slot_of[t * 64 + lane] >= 0) mask |= 1u << t;
+// The experts with tokens, the i-th in lane i (past the last: the others, without tokens).  The
+// activations' rows stand expert by expert, token by token.
+struct Experts {
+  int expert;
+  uint32_t tokens;  // as bits
+  int rows_to;      // rows of the experts up to this one
+};
+__device__ __forceinline__ Experts list_experts(uint32_t mask, int lane) {
   const uint64_t used = wave_ballot(mask != 0);
-  if (mask) {
-    const int at = lanes_below(used);
-    list[at] = lane;
-    tokens[at] = mask;
-  }
-  if (lane == 0) *count = __popcll(used);
+  const int at = mask ? lanes_below(used) : __popcll(used) + lanes_below(~used);
+  Experts x;
+  x.expert = __builtin_amdgcn_ds_permute(at * 4, lane);
+  x.tokens = (uint32_t)__builtin_amdgcn_ds_permute(at * 4, (int)mask);
+  x.rows_to = wave_prefix(__popc(x.tokens));
+  return x;
 }
 
-template <bool F32>
-__device__ __forceinline__ void load8(const void* x, size_t i, float (&v)[8]) {
-  if (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 d = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
-    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)lo, (__bf16)hi});
+}
+__device__ __forceinline__ void unpack8(const uint4 d, float (&v)[8]) {
+  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+  for (int j = 0; j < 4; j++) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) { return f32_to_bf16_any(lo) | f32_to_bf16_any(hi) << 16; }
 
-// Norm, router, routing, and the gate/up projection through the activation.
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint4 xs[];  // [T][4][H / 32]
-  __shared__ float logits[kLayerMaxT * 64];
-  __shared__ int8_t slot_of[kLayerMaxT * 64];
-  __shared__ int list[64];
-  __shared__ uint32_t tokens[64];
-  __shared__ int count;
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int KB = a.H >> 5;
-  const int H8 = a.H >> 3;
+// 16-byte pieces from one row in LDS to the next: 4 for a block, and one by which four rows'
+// reads of 4 blocks each meet 16 different banks of 16 bytes
+__host__ __device__ constexpr int row_stride(int KB) { return 4 * KB + 1; }
 
-  // this wave's first router rows are under way during the norm
-  uint4 wr[kRouted][kPieces];
-  auto load_router = [&](int e0, int p0) {
+// The tokens' rows into LDS, normed: 16-byte piece p of token t at t RS + p.  A
+// wave takes 64 pieces of a token at a time, SLOTS such under way; `then` is called once
+// the first loads are under way.
+template <bool F32, bool NORM, int SLOTS, typename Then>
+__device__ __forceinline__ void stage_rows(const MoeLayerArgs& a, uint4* xs, int RS, float* squares, int wave, int lane,
+                                           Then then) {
+  const int H8 = a.H >> 3, spans = (H8 + 63) >> 6, parts = a.T * spans;
+  uint4 raw[SLOTS][F32 ? 2 : 1], wn[SLOTS];
+  int token[SLOTS], piece[SLOTS];  // (piece 64 spans and more: none)
+  auto load = [&](int u0) {
 #pragma unroll
-    for (int r = 0; r < kRouted; r++) {
-      const uint4* w = reinterpret_cast<const uint4*>(a.router_w) + (size_t)min(e0 + r * kWaves, a.E - 1) * H8;
-#pragma unroll
-      for (int i = 0; i < kPieces; i++) wr[r][i] = w[min(p0 + 64 * i + lane, H8 - 1)];
+    for (int i = 0; i < SLOTS; i++) {
+      const int u = u0 + i * kWaves + wave, t = min(u, parts - 1) / spans;
+      const int p = (u - t * spans) * 64 + lane, pc = min(p, H8 - 1);
+      const uint4* x = reinterpret_cast<const uint4*>(a.x) + ((size_t)t * H8 + pc) * (F32 ? 2 : 1);
+      raw[i][0] = x[0];
+      if (F32) raw[i][F32 ? 1 : 0] = x[1];
+      if (NORM) wn[i] = reinterpret_cast<const uint4*>(a.w_norm)[pc];
+      token[i] = t;
+      piece[i] = u < parts ? p : H8;
     }
   };
-  load_router(wave, 0);
-
-  // norm: a wave a token; piece p of 8 elements is piece p % 4 of block p / 4
-  for (int t = wave; t < a.T; t += kWaves) {
-    float r = 1.f;
-    if (a.w_norm) {
-      float ss = 0.f;
-      for (int p = lane; p < H8; p += 64) {
-        float v[8];
-        load8<F32>(a.x, (size_t)t * a.H + 8 * p, v);
+  auto values = [&](int i, float (&v)[8]) {
+    if (F32) {
+      const uint4 lo = raw[i][0], hi = raw[i][F32 ? 1 : 0];
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
+    } else {
+      unpack8(raw[i][0], v);
+    }
+  };
+  load(0);
+  then();
+  if (NORM) {
+    for (int u0 = 0; u0 < parts; u0 += SLOTS * kWaves) {
+      if (u0) load(u0);
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) {
+        float v[8], ss = 0.f;
+        values(i, v);
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(v[j], v[j], ss);
+        ss = wave_total(piece[i] < H8 ? ss : 0.f);
+        const int u = u0 + i * kWaves + wave;
+        if (u < parts && lane == 0) squares[token[i] * 16 + (u - token[i] * spans)] = ss;
       }
-      r = 1.0f / sqrtf(wave_total(ss) / (float)a.H + a.eps);
     }
-    for (int p = lane; p < H8; p += 64) {
-      uint4 o;
-      if (a.w_norm) {
+    __syncthreads();
+  }
+  for (int u0 = 0; u0 < parts; u0 += SLOTS * kWaves) {
+    if (parts > SLOTS * kWaves) load(u0);
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) {
+      uint4 o = raw[i][0];
+      if (NORM) {
         float v[8], w[8];
-        load8<F32>(a.x, (size_t)t * a.H + 8 * p, v);
-        load8<false>(a.w_norm, 8 * p, w);
+        values(i, v);
+        unpack8(wn[i], w);
+        const float ss = row16_total((lane & 15) < spans ? squares[token[i] * 16 + (lane & 15)] : 0.f);
+        const float r = __builtin_amdgcn_rsqf(fmaf(ss, a.inv_H, a.eps));
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = v[j] * r * w[j];
         o = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-      } else {
-        o = reinterpret_cast<const uint4*>(a.x)[(size_t)t * H8 + p];
       }
-      xs[(size_t)t * 4 * KB + (p & 3) * KB + (p >> 2)] = o;
+      const int p = piece[i];
+      if (p < H8) xs[token[i] * RS + p] = o;
     }
   }
-  for (int i = tid; i < a.T * 64; i += kThreads) slot_of[i] = -1;
+}
+
+// Norm, router, routing, and the gate/up projection through the activation.
+template <bool F32, bool NORM, int C, int TEAMS>
+__global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a) {
+  // the tokens' rows, then (16-byte aligned) partial sums: of the router, then two rounds of the teams' units
+  extern __shared__ __attribute__((aligned(16))) uint4 xs[];
+  __shared__ __attribute__((aligned(16))) float squares[kLayerMaxT * 16];
+  __shared__ uint32_t tokens[64];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, q = lane >> 4;
+  const int KB = a.H >> 5, H8 = a.H >> 3, RS = row_stride(KB);
+  float4* const part = reinterpret_cast<float4*>(xs + a.T * RS);
+
+  // router: 16 experts' rows a tile, the tile's K split over kWaves / tiles waves
+  const int tiles = (a.E + 15) >> 4, shares = kWaves / tiles;
+  const int tile = wave / shares, share = wave - tile * shares;
+  const int per_share = (KB + shares - 1) / shares;
+  const int r0 = share * per_share, r1 = min(r0 + per_share, KB);
+  const uint4* const router =
+      reinterpret_cast<const uint4*>(a.router_w) + (size_t)min(tile * 16 + col, a.E - 1) * H8 + q;
+  uint4 rw[kRouterRing];
+  auto load_router = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < kRouterRing; i++) rw[i] = router[4 * min(b0 + i, KB - 1)];
+  };
+  const uint32_t router_bias = (a.router_b ? a.router_b : a.router_w)[min(lane, a.E - 1)];
+  if (tid < 64) tokens[tid] = 0;
+  if (a.T * ((H8 + 63) >> 6) <= kWaves)
+    stage_rows<F32, NORM, 1>(a, xs, RS, squares, wave, lane, [&]() { load_router(r0); });
+  else
+    stage_rows<F32, NORM, 4>(a, xs, RS, squares, wave, lane, [&]() { load_router(r0); });
   __syncthreads();
 
-  // router: wave w takes experts w, w + kWaves, ..., kRouted at a time
-  const bool whole = H8 <= 64 * kPieces;  // a row is held whole
-  for (int e0 = wave; e0 < a.E; e0 += kRouted * kWaves) {
-    if (whole && e0 != wave) load_router(e0, 0);
-    for (int t = 0; t < a.T; t++) {
-      float acc[kRouted] = {};
-      for (int p0 = 0; p0 < H8; p0 += 64 * kPieces) {
-        if (!whole) load_router(e0, p0);
+  const int xrow = min(col, a.T - 1) * RS;  // (columns past the tokens repeat the last)
+  {
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    for (int b0 = r0; b0 < r1; b0 += kRouterRing) {
+      if (b0 != r0) load_router(b0);
 #pragma unroll
-        for (int i = 0; i < kPieces; i++) {
-          const int p = p0 + 64 * i + lane;
-          if (p < H8) {
-            const uint4 xv = xs[(size_t)t * 4 * KB + (p & 3) * KB + (p >> 2)];
-#pragma unroll
-            for (int r = 0; r < kRouted; r++) acc[r] = dot8(wr[r][i], xv, acc[r]);
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kRouted; r++) {
-        const int e = e0 + r * kWaves;
-        const float l = wave_total(acc[r]);
-        if (lane == 0 && e < a.E) logits[t * 64 + e] = l + (a.router_b ? bf16_bits_to_f32(a.router_b[e]) : 0.f);
-      }
+      for (int i = 0; i < kRouterRing; i++)
+        if (b0 + i < r1)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, rw[i]),
+                                                        __builtin_bit_cast(bf16x8_t, xs[xrow + 4 * (b0 + i) + q]), acc,
+                                                        0, 0, 0);
     }
+    if (col < a.T) part[(wave * a.T + col) * 4 + q] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   }
   __syncthreads();
 
   // routing: a wave a token, lane e expert e; k rounds of the largest logit, the lowest index among equals
   for (int t = wave; t < a.T; t += kWaves) {
-    const float l = lane < a.E ? logits[t * 64 + lane] : -INFINITY;
-    const bool bad = wave_ballot(!(l < INFINITY)) != 0;  // a NaN or an infinity has no softmax
-    bool open = lane < a.E;
-    float top = 0.f, mine = 0.f;  // lane s: exp(logit of slot s - the largest)
-    int id = -1;                  // lane s: the expert of slot s
+    float d[kWaves];
+#pragma unroll
+    for (int s = 0; s < kWaves; s++) {
+      const int w = min((lane >> 4) * shares + min(s, shares - 1), kWaves - 1);
+      d[s] = reinterpret_cast<const float*>(part)[(w * a.T + t) * 16 + (lane & 15)];
+    }
     float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < kWaves; s++) sum += s < shares ? d[s] : 0.f;
+    const float l = lane < a.E ? sum + (a.router_b ? bf16_bits_to_f32(router_bias) : 0.f) : -INFINITY;
+    const bool bad = wave_ballot(!(l < INFINITY)) != 0;  // a NaN or an infinity has no softmax
+    bool open = lane < a.E, mine = false;
+    float top = 0.f, of_slot = 0.f;  // the largest logit; lane s: that of slot s
+    int id = -1;                     // lane s: the expert of slot s
     for (int s = 0; s < a.k && !bad; s++) {
       const float m = wave_max(open ? l : -INFINITY);
       const int e = __builtin_ctzll(wave_ballot(open && l == m));
       if (s == 0) top = m;
-      const float g = m == top ? 1.f : expf(m - top);
-      sum += g;
       if (lane == e) {
         open = false;
-        slot_of[t * 64 + e] = (int8_t)s;
+        mine = true;
       }
       if (lane == s) {
         id = e;
-        mine = g;
+        of_slot = m;
       }
     }
-    if (blockIdx.x == 0 && lane < a.k) {
-      const float g = bad ? 0.f : mine / sum;
-      a.ws_ids[t * a.k + lane] = id;
-      a.ws_gates[t * a.k + lane] = g;
-      if (a.ids) a.ids[t * a.k + lane] = id;
-      if (a.gates) a.gates[t * a.k + lane] = g;
+    if (mine) atomicOr(&tokens[lane], 1u << t);
+    if (blockIdx.x == 0) {
+      // (of two equal infinities the difference is no number, the quotient 1)
+      const float g = id < 0 ? 0.f : of_slot == top ? 1.f : expf(of_slot - top);
+      const float all = wave_total(g);
+      const float ge = !mine ? 0.f : l == top ? 1.f : expf(l - top);
+      a.ws_gates[t * 64 + lane] = bad ? 0.f : ge / all;
+      if (lane < a.k) {
+        a.ws_ids[t * a.k + lane] = id;
+        if (a.ids) a.ids[t * a.k + lane] = id;
+        if (a.gates) a.gates[t * a.k + lane] = bad ? 0.f : g / all;
+      }
     }
   }
   __syncthreads();
-  if (wave == 0) list_experts(slot_of, a.T, a.E, lane, list, tokens, &count);
-  __syncthreads();
+  const Experts x = list_experts(tokens[lane], lane);
+  const int count = __popcll(wave_ballot(x.tokens != 0));
+  if (blockIdx.x == 0 && wave == 0) {
+    a.ws_experts[lane] = x.expert;
+    a.ws_experts[64 + lane] = (int)x.tokens;
+    a.ws_experts[128 + lane] = x.rows_to;
+  }
 
-  // units of 4 rows (two gate and up pairs) of the chosen experts
-  const int per = a.F >> 1;
-  const int units = count * per;
-  const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
-  int u = (int)((long long)units * blockIdx.x / gridDim.x) + wave;
-  const int q = lane >> 4, j = lane & 15;
-  auto row_of = [&](int v) {
-    const int i = v / per;
-    return (size_t)list[i] * (2 * a.F) + 4 * (v - i * per) + q;
-  };
-  Unit cur, next;
-  if (u < u1) load_unit(cur, a.gu, a.gu_scales, row_of(u), KB, 0, j);
-  for (; u < u1; u += kWaves) {
-    if (u + kWaves < u1) load_unit(next, a.gu, a.gu_scales, row_of(u + kWaves), KB, 0, j);
-    const int i = u / per;
-    const int e = list[i], r0 = 4 * (u - i * per);
-    const float bias = a.gu_bias ? bf16_bits_to_f32(a.gu_bias[(size_t)e * 2 * a.F + r0 + q]) : 0.f;
-    for (uint32_t m = __builtin_amdgcn_readfirstlane(tokens[i]); m; m &= m - 1) {
-      const int t = __builtin_ctz(m);
-      const uint4* row = xs + (size_t)t * 4 * KB;
-      float p = unit_dot(cur, row, KB, 0, j, 0.f);
-      for (int b0 = kSpan; b0 < KB; b0 += kSpan) {
-        Unit more;
-        load_unit(more, a.gu, a.gu_scales, (size_t)e * 2 * a.F + r0 + q, KB, b0, j);
-        p = unit_dot(more, row, KB, b0, j, p);
-      }
-      p = row16_sum(p) + bias;
-      const float up = __shfl_xor(p, 16, 64);
-      if (j == 0 && (q & 1) == 0) {
-        const int s = slot_of[t * 64 + e];
-        a.act[(size_t)(t * a.k + s) * a.F + (r0 >> 1) + (q >> 1)] = (uint16_t)f32_to_bf16_any(swiglu(p, up));
-      }
+  // Units of 16 rows (8 gate and up pairs) of the chosen experts, spread evenly over the
+  // workgroups; a workgroup's go to its teams in turn, one a round.
+  const int per = a.F >> 3, units = count * per;  // (per >= 4)
+  const int u0 = (int)((long long)units * blockIdx.x / gridDim.x);
+  const int mine = (int)((long long)units * (blockIdx.x + 1) / gridDim.x) - u0;
+  if (mine == 0) return;
+  constexpr int kTeam = kWaves / TEAMS;
+  const int team = wave / kTeam, part_of = wave - team * kTeam;
+  const int rounds = (mine + TEAMS - 1) / TEAMS;
+  Stream<C> st;
+  Places<C> at;
+  at.set(col, part_of * 4 * C + q, KB);
+  int ld_i = (u0 + team) / per, ld_tile = u0 + team - ld_i * per, ld_left = mine - team;
+  auto next_unit = [&]() {
+    const size_t unit = (size_t)__builtin_amdgcn_readlane(x.expert, min(ld_i, 63)) * per + ld_tile;
+    st.open(a.gu, a.gu_scales, unit * 16, KB, ld_left > 0);
+    ld_left -= TEAMS;
+    ld_tile += TEAMS;
+    if (ld_tile >= per) {
+      ld_tile -= per;
+      ld_i++;
     }
-    cur = next;
+  };
+  next_unit();
+#pragma unroll
+  for (int j = 0; j < C; j++) st.load(j, at.w[j], at.s[j]);
+  // the sum over a team, the bias and the activation: a thread has a unit's pair of rows and a token
+  const int out_pair = tid & 7, out_t = (tid >> 3) & 15, out_team = min(tid >> 7, TEAMS - 1);
+  const int out_tr = min(out_t, a.T - 1);
+  int out_i = (u0 + out_team) / per, out_tile = u0 + out_team - out_i * per;
+  const uint16_t* const bias = a.gu_bias ? a.gu_bias : a.router_w;  // (read and not used without one)
+  for (int r = 0; r < rounds; r++) {
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    const bool out = tid < TEAMS * 128 && out_t < a.T && r * TEAMS + out_team < mine;
+    // its bias is loaded ahead of the next round's weights: loads return in order
+    const int oi = min(out_i, count - 1), e = __shfl(x.expert, oi, 64), row = out_tile * 16 + 2 * out_pair;
+    const uint32_t its = __shfl(x.tokens, oi, 64);
+    const int rows_to = __shfl(x.rows_to, oi, 64);
+    const size_t bias_at = a.gu_bias ? (size_t)e * 2 * a.F + row : 0;
+    const uint32_t gate_bias = bias[bias_at], up_bias = bias[bias_at + 1];
+    next_unit();
+#pragma unroll
+    for (int j = 0; j < C; j++) {
+      acc = item_mma(st.w[j], st.s[j], xs + xrow + at.x[j], acc);
+      st.load(j, at.w[j], at.s[j]);
+    }
+    float4* const mine_of = part + (r & 1) * kWaves * a.T * 4;
+    if (col < a.T) mine_of[(wave * a.T + col) * 4 + q] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (out && (its >> out_tr & 1)) {
+      float gate = a.gu_bias ? bf16_bits_to_f32(gate_bias) : 0.f, up = a.gu_bias ? bf16_bits_to_f32(up_bias) : 0.f;
+      float2 d[kTeam];
+#pragma unroll
+      for (int p = 0; p < kTeam; p++)
+        d[p] = reinterpret_cast<const float2*>(mine_of)[((out_team * kTeam + p) * a.T + out_tr) * 8 + out_pair];
+#pragma unroll
+      for (int p = 0; p < kTeam; p++) {
+        gate += d[p].x;
+        up += d[p].y;
+      }
+      const int pos = rows_to - __popc(its >> out_tr);
+      a.act[(size_t)pos * a.F + (row >> 1)] = (uint16_t)f32_to_bf16_any(swiglu(gate, up));
+    }
+    out_tile += TEAMS;
+    if (out_tile >= per) {
+      out_tile -= per;
+      out_i++;
+    }
   }
 }
 
-// The down projection, the combine in slot order and the residual.
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, int lds_rows, int max_quads) {
-  // staged rows [lds_rows][4][F / 32], then the outputs [max_quads][4][T k]
-  extern __shared__ __attribute__((aligned(16))) uint4 as[];
-  __shared__ int8_t slot_of[kLayerMaxT * 64];
-  __shared__ int list[64];
-  __shared__ uint32_t tokens[64];
-  __shared__ int count;
-  __shared__ float gates[kMaxRows];
+// The down projection, the combine and the residual: a workgroup owns 16 output columns of
+// all tokens, its waves share K.  DEPTH experts' weights are under way; the activations lie
+// in LDS, as many experts' at a time as fit (a multiple of DEPTH).
+template <int C, int DEPTH>
+__global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, int lds_rows) {
+  extern __shared__ __attribute__((aligned(16))) uint4 as[];  // as the tokens' rows above
+  __shared__ float gates[kLayerMaxT * 64];
+  __shared__ float4 part[kWaves * kLayerMaxT * 4];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int KB = a.F >> 5, F8 = a.F >> 3;
-  const int R = a.T * a.k;
-  float* const outs = reinterpret_cast<float*>(as + (size_t)lds_rows * F8);
-  for (int i = tid; i < a.T * 64; i += kThreads) slot_of[i] = -1;
-  __syncthreads();
-  for (int r = tid; r < R; r += kThreads) {
-    const int t = r / a.k;
-    const int e = a.ws_ids[r];
-    gates[r] = a.ws_gates[r];
-    if ((unsigned)e < (unsigned)a.E) slot_of[t * 64 + e] = (int8_t)(r - t * a.k);
-  }
-  __syncthreads();
-  if (wave == 0) list_experts(slot_of, a.T, a.E, lane, list, tokens, &count);
-  __syncthreads();
+  const int col = lane & 15, q = lane >> 4;
+  const int KB = a.F >> 5, F8 = a.F >> 3, RS = row_stride(KB);
+  Experts x;
+  x.expert = a.ws_experts[lane];
+  x.tokens = (uint32_t)a.ws_experts[64 + lane];
+  x.rows_to = a.ws_experts[128 + lane];
+  // what is added at the end is loaded ahead: thread (token, column); the first four slots' biases
+  const int out_t = min(tid >> 4, a.T - 1), out_c = blockIdx.x * 16 + (tid & 15);
+  const size_t out_at = (size_t)out_t * a.H + out_c;
+  int id[4];
+#pragma unroll
+  for (int s = 0; s < 4; s++) id[s] = a.ws_ids[out_t * a.k + min(s, a.k - 1)];
+  float gate_in[2];  // T * 64 <= 1024 of them
+#pragma unroll
+  for (int i = 0; i < 2; i++) gate_in[i] = a.ws_gates[min(tid + i * kThreads, a.T * 64 - 1)];
 
-  const int quads = a.H >> 2;
-  const int q0 = (int)((long long)quads * blockIdx.x / gridDim.x);
-  const int nq = (int)((long long)quads * (blockIdx.x + 1) / gridDim.x) - q0;
-  const int q = lane >> 4, j = lane & 15;
-  // as many experts at a time as their tokens' rows fit
+  const int count = __popcll(wave_ballot(x.tokens != 0));
+  Stream<C> st[DEPTH];
+  Places<C> at;
+  at.set(col, wave * 4 * C + q, KB);
+  auto open = [&](int d, int i) {
+    st[d].open(a.down, a.down_scales,
+               (size_t)__builtin_amdgcn_readlane(x.expert, min(i, 63)) * a.H + (size_t)blockIdx.x * 16,
+               KB, i < count);
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; d++) {
+    open(d, d);
+#pragma unroll
+    for (int j = 0; j < C; j++) st[d].load(j, at.w[j], at.s[j]);
+  }
+  const uint16_t* const bias = a.down_bias ? a.down_bias : a.router_w;  // (read and not used without one)
+  auto bias_of = [&](int e) { return (uint32_t)bias[a.down_bias ? (size_t)max(e, 0) * a.H + out_c : 0]; };
+  uint32_t bias_bits[4];
+#pragma unroll
+  for (int s = 0; s < 4; s++) bias_bits[s] = bias_of(id[s]);
+  // (the 32 bits that hold x: x is 16-byte aligned and H even)
+  const uint32_t x_bits = static_cast<const uint32_t*>(a.x)[a.x_f32 ? out_at : out_at >> 1];
+#pragma unroll
+  for (int i = 0; i < 2; i++)
+    if (tid + i * kThreads < a.T * 64) gates[tid + i * kThreads] = gate_in[i];
+  const __amdgpu_buffer_rsrc_t act =
+      __builtin_amdgcn_make_buffer_rsrc(a.act, (short)0, a.T * a.k * a.F * 2, 0x00020000);
+
+  f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+  const int tcol = min(col, a.T - 1);
   for (int first = 0; first < count;) {
-    int end = first, rows = 0;
-    while (end < count) {
-      const int n = __popc(__builtin_amdgcn_readfirstlane(tokens[end]));
-      if (rows + n > lds_rows) break;
-      rows += n;
-      end++;
-    }
-    const int units = (end - first) * nq;
-    auto row_of = [&](int v) {
-      const int i = v / nq;
-      return (size_t)list[first + i] * a.H + 4 * (q0 + v - i * nq) + q;
-    };
-    Unit cur, next;
-    int u = wave;
-    if (u < units) load_unit(cur, a.down, a.down_scales, row_of(u), KB, 0, j);
-    // the rows, expert by expert, token by token
-    {
-      int at = 0;
-      for (int i = first; i < end; i++) {
-        const int e = list[i];
-        for (uint32_t m = __builtin_amdgcn_readfirstlane(tokens[i]); m; m &= m - 1, at++) {
-          const int t = __builtin_ctz(m);
-          const uint4* src = reinterpret_cast<const uint4*>(a.act + (size_t)(t * a.k + slot_of[t * 64 + e]) * a.F);
-          for (int p = tid; p < F8; p += kThreads) as[(size_t)at * F8 + (p & 3) * KB + (p >> 2)] = src[p];
-        }
+    // the experts whose rows fit, by DEPTH unless they are the last
+    const int row0 = first ? __builtin_amdgcn_readlane(x.rows_to, first - 1) : 0;
+    int last = min(count, __popcll(wave_ballot(x.rows_to - row0 <= lds_rows)));
+    if (last < count) last -= (last - first) % DEPTH;
+    const int rows = __builtin_amdgcn_readlane(x.rows_to, last - 1) - row0;
+    const int spans = (F8 + 63) >> 6, parts = rows * spans;
+    for (int u0 = wave; u0 < parts; u0 += 4 * kWaves) {
+      u32x4_t v[4];
+      int to[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int u = u0 + i * kWaves, r = u / spans, p = (u - r * spans) * 64 + lane;
+        const bool there = u < parts && p < F8;
+        v[i] = __builtin_amdgcn_raw_buffer_load_b128(act, there ? (uint32_t)((row0 + r) * F8 + p) * 16 : kPast, 0, 0);
+        to[i] = there ? r * RS + p : lds_rows * RS + lane;  // (64 pieces behind the rows)
       }
+#pragma unroll
+      for (int i = 0; i < 4; i++) as[to[i]] = __builtin_bit_cast(uint4, v[i]);
     }
     __syncthreads();
-    for (; u < units; u += kWaves) {
-      if (u + kWaves < units) load_unit(next, a.down, a.down_scales, row_of(u + kWaves), KB, 0, j);
-      const int i = u / nq, quad = u - i * nq;
-      const int e = list[first + i];
-      int at = 0;
-      for (int b = first; b < first + i; b++) at += __popc(tokens[b]);
-      const float bias = a.down_bias ? bf16_bits_to_f32(a.down_bias[(size_t)e * a.H + 4 * (q0 + quad) + q]) : 0.f;
-      for (uint32_t m = __builtin_amdgcn_readfirstlane(tokens[first + i]); m; m &= m - 1, at++) {
-        const int t = __builtin_ctz(m);
-        const uint4* row = as + (size_t)at * F8;
-        float p = unit_dot(cur, row, KB, 0, j, 0.f);
-        for (int b0 = kSpan; b0 < KB; b0 += kSpan) {
-          Unit more;
-          load_unit(more, a.down, a.down_scales, row_of(u), KB, b0, j);
-          p = unit_dot(more, row, KB, b0, j, p);
+    for (int i0 = first; i0 < last; i0 += DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; d++) {
+        // (past the last expert: no token, weights that read as zeros)
+        const int i = min(i0 + d, 63);
+        const uint32_t m = i0 + d < last ? __builtin_amdgcn_readlane(x.tokens, i) : 0u;
+        const bool has = (m >> col) & 1;
+        // this token's row; where it does not have the expert, some row, not used
+        const int row = has ? __builtin_amdgcn_readlane(x.rows_to, i) - row0 - __popc(m >> col) : 0;
+        const uint4* const in = as + row * RS;
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+        open(d, i0 + d + DEPTH);
+#pragma unroll
+        for (int j = 0; j < C; j++) {
+          acc = item_mma(st[d].w[j], st[d].s[j], in + at.x[j], acc);
+          st[d].load(j, at.w[j], at.s[j]);
         }
-        p = row16_sum(p) + bias;
-        if (j == 0) outs[(quad * 4 + q) * R + t * a.k + slot_of[t * 64 + e]] = p;
+        const float gt = gates[tcol * 64 + __builtin_amdgcn_readlane(x.expert, i)], g = has ? gt : 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; r++) y[r] = g != 0.f ? fmaf(g, acc[r], y[r]) : y[r];  // (0 adds nothing)
       }
-      cur = next;
     }
-    __syncthreads();
-    first = end;
+    first = last;
+    if (first < count) __syncthreads();
   }
-  for (int i = tid; i < nq * 4 * a.T; i += kThreads) {
-    const int t = i / (nq * 4), c = i - t * nq * 4;
-    const size_t at = (size_t)t * a.H + 4 * q0 + c;
-    float h = 0.f;
+  if (col < a.T) part[(wave * a.T + col) * 4 + q] = make_float4(y[0], y[1], y[2], y[3]);
+  __syncthreads();
+  if (tid < a.T * 16) {
+    float sum = 0.f, d[kWaves];
+#pragma unroll
+    for (int p = 0; p < kWaves; p++) d[p] = reinterpret_cast<const float*>(part)[(p * a.T + out_t) * 16 + (tid & 15)];
+#pragma unroll
+    for (int p = 0; p < kWaves; p++) sum += d[p];
     for (int s = 0; s < a.k; s++) {
-      const float g = gates[t * a.k + s];
-      if (g != 0.f) h = fmaf(g, outs[c * R + t * a.k + s], h);  // (a slot without an expert has gate 0)
+      const int e = s == 0 ? id[0] : s == 1 ? id[1] : s == 2 ? id[2] : s == 3 ? id[3] : a.ws_ids[out_t * a.k + s];
+      const uint32_t b =
+          s == 0 ? bias_bits[0] : s == 1 ? bias_bits[1] : s == 2 ? bias_bits[2] : s == 3 ? bias_bits[3] : bias_of(e);
+      const float g = e >= 0 && a.down_bias ? gates[out_t * 64 + e] : 0.f;
+      if (g != 0.f) sum = fmaf(g, bf16_bits_to_f32(b), sum);
     }
-    if (a.residual) h += F32 ? static_cast<const float*>(a.x)[at] : bf16_bits_to_f32(static_cast<const uint16_t*>(a.x)[at]);
-    if (a.y_f32) static_cast<float*>(a.y)[at] = h;
-    else static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_any(h);
+    const float xv = __uint_as_float(a.x_f32 ? x_bits : out_at & 1 ? x_bits & 0xffff0000u : x_bits << 16);
+    const float h = a.residual ? xv + sum : sum;
+    if (a.y_f32) static_cast<float*>(a.y)[out_at] = h;
+    else static_cast<uint16_t*>(a.y)[out_at] = (uint16_t)f32_to_bf16_any(h);
   }
+}
+
+// items that a wave of a team holds for its share of KB blocks, by twos
+int items_of(int KB, int team) { return ((KB + 4 * team - 1) / (4 * team) + 1) / 2 * 2; }
+
+template <bool F32, bool NORM, int C, int TEAMS>
+hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
+  static DynLdsLimit limit(reinterpret_cast<const void*>(layer_gate_up_kernel<F32, NORM, C, TEAMS>), kLayerUpLds);
+  // the tokens' rows, and two rounds of partial sums (the router's take the room of one)
+  const size_t lds = (size_t)a.T * row_stride(a.H / 32) * 16 + (size_t)2 * kWaves * 64 * a.T;
+  if (lds > (size_t)kLayerUpLds) return hipErrorInvalidConfiguration;
+  const hipError_t e = limit.ensure();
+  if (e != hipSuccess) return e;
+  const int R = a.T * a.k, most = (R < a.E ? R : a.E) * (a.F / 8);  // units of all experts that the tokens can reach
+  hipLaunchKernelGGL((layer_gate_up_kernel<F32, NORM, C, TEAMS>), dim3(most < kGroups ? most : kGroups), dim3(kThreads), lds,
+                     stream, a);
+  return hipGetLastError();
+}
+template <bool F32, bool NORM>
+hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
+  // three teams of 4 waves while a wave's share of K is 6 items at most, else one of 12
+  const int KB = a.H / 32, C = items_of(KB, kWaves / 3);
+  return C == 2                     ? launch_up<F32, NORM, 2, 3>(a, stream)
+         : C == 4                   ? launch_up<F32, NORM, 4, 3>(a, stream)
+         : C == 6                   ? launch_up<F32, NORM, 6, 3>(a, stream)
+         : items_of(KB, kWaves) <= 4 ? launch_up<F32, NORM, 4, 1>(a, stream)
+                                    : launch_up<F32, NORM, 6, 1>(a, stream);
+}
+
+template <int C, int DEPTH>
+hipError_t launch_down(const MoeLayerArgs& a, hipStream_t stream) {
+  static DynLdsLimit limit(reinterpret_cast<const void*>(layer_down_kernel<C, DEPTH>), kLayerDownLds);
+  const size_t row = (size_t)row_stride(a.F / 32) * 16;
+  const int fit = (int)(((size_t)kLayerDownLds - 64 * 16) / row), R = a.T * a.k;
+  if (fit < R && fit < DEPTH * a.T) {  // DEPTH experts' rows may not fit
+    if constexpr (DEPTH > 1) return launch_down<C, 1>(a, stream);
+    return hipErrorInvalidConfiguration;
+  }
+  const hipError_t e = limit.ensure();
+  if (e != hipSuccess) return e;
+  const int rows = fit < R ? fit : R;
+  hipLaunchKernelGGL((layer_down_kernel<C, DEPTH>), dim3(a.H / 16), dim3(kThreads),
+                     rows * row + 64 * 16, stream, a, rows);
+  return hipGetLastError();
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -385,38 +575,21 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t moe_layer_workspace_bytes(int T, int k, int F) {
-  const size_t R = (size_t)T * k;
-  return 2 * align256(R * 4) + align256(R * F * 2);
+  return T ? 1024 + (size_t)T * (64 * 4 + kLayerMaxTopK * 4) + align256((size_t)T * k * F * 2) : 0;
 }
 
-hipError_t launch_moe_layer(MoeLayerArgs a, bool x_f32, void* workspace, hipStream_t stream) {
-  const size_t R = (size_t)a.T * a.k;
+hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  a.ws_ids = reinterpret_cast<int32_t*>(ws);
-  a.ws_gates = reinterpret_cast<float*>(ws + align256(R * 4));
-  a.act = reinterpret_cast<uint16_t*>(ws + 2 * align256(R * 4));
-  const int quads = a.H / 4;
-  const int groups = quads < kGroups ? quads : kGroups;
-  const int max_quads = (quads + groups - 1) / groups;
-  const size_t outs = (size_t)max_quads * 4 * R * 4;
-  // every row that one expert can have, more where they fit
-  const size_t fit = (kLayerLds - outs) / ((size_t)a.F * 2);
-  const int lds_rows = (int)(fit < R ? fit : R);
-  static DynLdsLimit limits[4] = {{reinterpret_cast<const void*>(layer_gate_up_kernel<false>), kLayerLds},
-                                  {reinterpret_cast<const void*>(layer_gate_up_kernel<true>), kLayerLds},
-                                  {reinterpret_cast<const void*>(layer_down_kernel<false>), kLayerLds},
-                                  {reinterpret_cast<const void*>(layer_down_kernel<true>), kLayerLds}};
-  hipError_t e = limits[x_f32].ensure();
-  if (e == hipSuccess) e = limits[2 + x_f32].ensure();
+  a.ws_experts = reinterpret_cast<int32_t*>(ws);
+  a.ws_gates = reinterpret_cast<float*>(ws + 1024);
+  a.ws_ids = reinterpret_cast<int32_t*>(ws + 1024 + (size_t)a.T * 64 * 4);
+  a.act = reinterpret_cast<uint16_t*>(ws + 1024 + (size_t)a.T * (64 * 4 + kLayerMaxTopK * 4));
+  const hipError_t e = !a.w_norm ? launch_up<false, false>(a, stream)
+                       : a.x_f32 ? launch_up<true, true>(a, stream)
+                                 : launch_up<false, true>(a, stream);
   if (e != hipSuccess) return e;
-  const size_t up_lds = (size_t)a.T * a.H * 2, down_lds = (size_t)lds_rows * a.F * 2 + outs;
-  auto up = x_f32 ? layer_gate_up_kernel<true> : layer_gate_up_kernel<false>;
-  auto down = x_f32 ? layer_down_kernel<true> : layer_down_kernel<false>;
-  hipLaunchKernelGGL(up, dim3(kGroups), dim3(kThreads), up_lds, stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(down, dim3(groups), dim3(kThreads), down_lds, stream, a, lds_rows, max_quads);
-  return hipGetLastError();
+  const int C = items_of(a.F / 32, kWaves);  // (6 at most)
+  return C == 2 ? launch_down<2, 3>(a, stream) : C == 4 ? launch_down<4, 2>(a, stream) : launch_down<6, 1>(a, stream);
 }
 
 }  // namespace mxfp4

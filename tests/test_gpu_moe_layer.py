@@ -5,14 +5,16 @@ value known to +-e before it lies between the roundings of its ends, so a roundi
 alike costs nothing and one near a border its whole step.
   xn      before its rounding off by (H / 64 + 20) 2^-24 of itself: a lane's H / 64 squares summed in
           fp32 one after the other, the wave's sum, the root, the division and two products.
-  sums    a lane's dot products of pairs, one after the other (16 for each of its ceil(K / 512) blocks,
-          or H / 128 of the router), each off by 2^-23 of its operands at most twice, then the 16 or 64
-          lanes' sum and the bias: (n + 10) 2^-22 of the terms' magnitudes.
+  sums    an MFMA adds the products of 32 elements to its accumulator; taken as a sum aligned to its
+          largest term and cut there, 32 2^-23 of the terms' magnitudes over all steps, and each step's
+          sum is rounded (2^-23 with cutting), K / 32 times, then 12 waves' partial sums and the bias:
+          (2^-18 + (K / 32 + 16) 2^-23) of the magnitudes.
   gates   the logits' error dl moves a softmax by the factor exp(2 dl) at most; the exponential, the sum
           and the quotient by (k + 8) 2^-23.
   act     the projection's box through the activation (the oracle's swiglu_range), 4e-6 relative and 2e-5
           for its own arithmetic, as for the library's other gated projections, then its rounding.
-  y       k products and sums and the residual, (k + 2) 2^-23 of the magnitudes, and its rounding.
+  y       each wave's k products and sums, 12 waves' sums, the biases and the residual, (2 k + 14) 2^-23 of
+          the terms' magnitudes, and its rounding.
 The kernel's ids are held to the logits: each within 2 dl of what the oracle takes at its place, equal
 where the oracle's margins are wider; the oracle then follows the kernel's ids.
 """
@@ -35,6 +37,10 @@ def _announce(msg):
 
 def cuda(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def sums(mag, K):
+    return (2.0 ** -18 + (K / 32 + 16) * 2.0 ** -23) * mag
 
 
 def rounded(v, e):
@@ -87,7 +93,7 @@ class Layer:
             xn, exn = x, np.zeros_like(x)
         assert np.array_equal(xn, O.layer_route(x, self.w_norm, EPS, self.rw, self.rb, k)[0])
         logits, mag = O.matmul(xn, self.rw, self.rb)
-        dl = exn @ np.abs(self.rw).T + (H / 128 + 10) * 2.0 ** -22 * mag
+        dl = exn @ np.abs(self.rw).T + sums(mag, H)
         d = dl.max(1)
         # the kernel's routing
         ids, gates = self.ids.cpu().numpy(), self.gates.cpu().numpy().astype(np.float64)
@@ -103,21 +109,21 @@ class Layer:
         # through the experts
         p, mag = O.expert_matmul(w_gu, self.bgu, xn, False, ids)
         ep, _ = O.expert_matmul(np.abs(w_gu), None, exn, False, ids)
-        ep = ep + (16 * -(-H // 512) + 10) * 2.0 ** -22 * mag
+        ep = ep + sums(mag, H)
         f = M.swiglu(p)
         lo, hi = M.swiglu_range(p - ep, p + ep)
         ef = np.maximum(hi - f, f - lo)
         act, ea = rounded(f, ef + 4e-6 * (np.abs(f) + ef) + 2e-5)
-        o, mag = O.expert_matmul(w_down, self.bd, act, True, ids)
+        o, mag_o = O.expert_matmul(w_down, self.bd, act, True, ids)
         eo, _ = O.expert_matmul(np.abs(w_down), None, ea, True, ids)
-        eo = eo + (16 * -(-F // 512) + 10) * 2.0 ** -22 * mag
+        eo = eo + sums(mag_o, F)
         h = (g[..., None] * o).sum(1)
-        size = (g[..., None] * np.abs(o)).sum(1)
+        size = (g[..., None] * mag_o).sum(1)
         eh = (g[..., None] * eo + eg[..., None] * (np.abs(o) + eo)).sum(1)
         assert np.allclose(h, O.layer(xn, ids, g, w_gu, self.bgu, w_down, self.bd)[0], rtol=1e-12, atol=1e-12)
         if self.residual:
             h, size = h + x, size + np.abs(x)
-        eh = eh + (k + 2) * 2.0 ** -23 * (size + eh)
+        eh = eh + (2 * k + 14) * 2.0 ** -23 * (size + eh)
         half = 2.0 ** -8 if self.y.dtype == torch.bfloat16 else 2.0 ** -24
         bound = eh + half * (np.abs(h) + eh)
         got = self.y.float().cpu().numpy().astype(np.float64)
