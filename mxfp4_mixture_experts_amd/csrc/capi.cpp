@@ -787,7 +787,7 @@ static int check_layer_sizes(int T, int H, int E, int k, int F) {
 size_t mxfp4_moe_layer_workspace_size(int T, int H, int E, int k, int F) {
   g_last_error[0] = '\0';
   if (check_layer_sizes(T, H, E, k, F) != MXFP4_OK) return (size_t)-1;
-  return mxfp4::moe_layer_workspace_bytes(T, k, F);
+  return mxfp4::moe_layer_workspace_bytes(T, H, k, F);
 }
 
 int mxfp4_moe_layer(const void* x, int x_dtype, int T, int H, int E, int k, int F, const uint16_t* w_norm, float eps,
@@ -815,7 +815,7 @@ int mxfp4_moe_layer(const void* x, int x_dtype, int T, int H, int E, int k, int 
   if (!aligned_to(router_b, 2) || !aligned_to(gu_bias, 2) || !aligned_to(down_bias, 2) || !aligned_elem(y, y_dtype) ||
       !aligned_to(topk_ids, 4) || !aligned_to(gates, 4))
     return fail(MXFP4_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  st = check_workspace(workspace, workspace_bytes, mxfp4::moe_layer_workspace_bytes(T, k, F));
+  st = check_workspace(workspace, workspace_bytes, mxfp4::moe_layer_workspace_bytes(T, H, k, F));
   if (st != MXFP4_OK) return st;
   if ((st = check_device()) != MXFP4_OK) return st;
   mxfp4::MoeLayerArgs a{};

@@ -89,13 +89,13 @@ struct Fp4MatmulArgs {
 };
 hipError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int out_kind, hipStream_t stream);
 
-// moe_layer.hip: a whole expert layer for a few tokens in two launches
+// moe_layer.hip: a whole expert layer for a few tokens in three launches
 constexpr int kLayerMaxT = 16;     // = MXFP4_LAYER_MAX_T
 constexpr int kLayerMaxTopK = 16;  // = MXFP4_LAYER_MAX_TOPK
 constexpr int kLayerMaxN = 8192;   // = MXFP4_LAYER_MAX_N
 constexpr int kLayerMaxTN = 65536;  // = MXFP4_LAYER_MAX_TN
-// dynamic LDS of the two launches at most: T rows of H or F (128 KB) with their padding (T 16 bytes),
-// and in the first 1536 T bytes of partial sums
+// dynamic LDS of the two projections at most: T rows of H or F (128 KB) with their padding (T 16 bytes),
+// 1 KB, and in gate/up 1536 T bytes of partial sums
 constexpr int kLayerUpLds = 156 * 1024, kLayerDownLds = 136 * 1024;
 struct MoeLayerArgs {
   const void* x;           // [T, H] bf16 or fp32
@@ -116,10 +116,12 @@ struct MoeLayerArgs {
   bool x_f32, residual, y_f32;
   int32_t* ws_experts;  // [3, 64] the experts with tokens, their tokens as bits, their rows' end; these set
   float* ws_gates;      // [T, 64] by expert                                      by the launcher
+  float* ws_logits;     // [T, 64]
+  uint16_t* ws_xn;      // [T, H] normed rows (not with w_norm NULL)
   int32_t* ws_ids;      // [T, k], -1 for a token that reaches no expert
   uint16_t* act;        // [T k, F] expert by expert, token by token
 };
-size_t moe_layer_workspace_bytes(int T, int k, int F);
+size_t moe_layer_workspace_bytes(int T, int H, int k, int F);
 hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream);
 
 // router.hip: logits [T, E] bf16 = x [T, H] . w [E, H]^T + bias (fp32 sums, rounded once)

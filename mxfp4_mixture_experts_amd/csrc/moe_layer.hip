@@ -1,19 +1,20 @@
-// A whole expert layer for a few tokens in two launches, for gfx950:
+// A whole expert layer for a few tokens in three launches, for gfx950:
 //
-//   xn = bf16(x r w_norm), logits = xn . router^T + bias (fp32), the k largest and their
-//   softmax; act = bf16(swiglu(gate_up[e] . xn + bias)) for every chosen expert;
-//   y = (x +) sum over slots of gate (down[e] . act + bias).
+//   router  xn = bf16(x r w_norm), logits = xn . router^T + bias (fp32): a workgroup an
+//           expert, a wave a token, which norms the token itself;
+//   gate/up the k largest logits and their softmax (by every workgroup for itself), then
+//           act = bf16(swiglu(gate_up[e] . xn + bias)) for every chosen expert;
+//   down    y = (x +) sum over slots of gate (down[e] . act + bias).
 //
-// The layer has two points where every workgroup needs what all others made (the
-// routing; the activations).  The second is the border of the launches.  At the
-// first each workgroup of the first launch makes the routing itself: it reads the
-// router's E rows from L2 (at E = 32, H = 2880 184 KB, about 2.6 us with all 256 CUs
-// at it), which costs less than a launch and its latency, and no workgroup ever
-// waits for another.
+// The borders of the launches are the two points where every workgroup needs what all
+// others made; no workgroup waits for another.  With the norm and the router in the
+// gate/up launch too (each workgroup its own) the layer took 27.3 us for one token of
+// H = F = 2880, E = 32, k = 4 instead of @ONE@: 256 CUs read the same 184 KB at 17 bytes a
+// clock each, three times what a launch costs.
 //
-// Both launches stream the chosen experts' weights once for all tokens, by items of 16
-// weight rows x 4 blocks (lane: row lane % 16, block lane / 16), a wave's items in a
-// ring of registers far ahead of their use.  A block becomes 32 exact bf16 weights
+// Both projections stream the chosen experts' weights once for all tokens, by items of 16
+// weight rows x 4 blocks (lane: row lane % 16, block lane / 16), a wave's items in
+// registers ahead of their use.  A block becomes 32 exact bf16 weights
 // (v_cvt_scalef32_pk_bf16_fp4) and one MFMA for each quarter of the blocks multiplies
 // them by up to 16 tokens' rows: the work of an item does not grow with the tokens.
 // K is split over the waves alike whatever the tokens are, and a token's sums hold
@@ -29,8 +30,9 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 12, kThreads = kWaves * 64;
-constexpr int kGroups = 256;       // workgroups of the first launch: one a CU
-constexpr int kRouterRing = 15;    // router: loads of 16 rows x 32 elements in flight
+constexpr int kGroups = 256;       // workgroups of gate/up: one a CU
+constexpr int kRouterWaves = 8;    // router: tokens at a time
+constexpr int kPieces = 6;         // router: 16-byte pieces of a row that a lane holds
 constexpr uint32_t kPast = 0x80000000u;  // an offset past every buffer: the load returns zeros
 
 // 2^(s - 127): s = 0 is the subnormal 2^-127
@@ -157,139 +159,168 @@ __device__ __forceinline__ void unpack8(const uint4 d, float (&v)[8]) {
 // reads of 4 blocks each meet 16 different banks of 16 bytes
 __host__ __device__ constexpr int row_stride(int KB) { return 4 * KB + 1; }
 
-// The tokens' rows into LDS, normed: 16-byte piece p of token t at t RS + p.  A
-// wave takes 64 pieces of a token at a time, SLOTS such under way; `then` is called once
-// the first loads are under way.
-template <bool F32, bool NORM, int SLOTS, typename Then>
-__device__ __forceinline__ void stage_rows(const MoeLayerArgs& a, uint4* xs, int RS, float* squares, int wave, int lane,
-                                           Then then) {
-  const int H8 = a.H >> 3, spans = (H8 + 63) >> 6, parts = a.T * spans;
-  uint4 raw[SLOTS][F32 ? 2 : 1], wn[SLOTS];
-  int token[SLOTS], piece[SLOTS];  // (piece 64 spans and more: none)
-  auto load = [&](int u0) {
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) {
-      const int u = u0 + i * kWaves + wave, t = min(u, parts - 1) / spans;
-      const int p = (u - t * spans) * 64 + lane, pc = min(p, H8 - 1);
-      const uint4* x = reinterpret_cast<const uint4*>(a.x) + ((size_t)t * H8 + pc) * (F32 ? 2 : 1);
-      raw[i][0] = x[0];
-      if (F32) raw[i][F32 ? 1 : 0] = x[1];
-      if (NORM) wn[i] = reinterpret_cast<const uint4*>(a.w_norm)[pc];
-      token[i] = t;
-      piece[i] = u < parts ? p : H8;
-    }
-  };
-  auto values = [&](int i, float (&v)[8]) {
-    if (F32) {
-      const uint4 lo = raw[i][0], hi = raw[i][F32 ? 1 : 0];
-      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
-    } else {
-      unpack8(raw[i][0], v);
-    }
-  };
-  load(0);
-  then();
-  if (NORM) {
-    for (int u0 = 0; u0 < parts; u0 += SLOTS * kWaves) {
-      if (u0) load(u0);
-#pragma unroll
-      for (int i = 0; i < SLOTS; i++) {
-        float v[8], ss = 0.f;
-        values(i, v);
-#pragma unroll
-        for (int j = 0; j < 8; j++) ss = fmaf(v[j], v[j], ss);
-        ss = wave_total(piece[i] < H8 ? ss : 0.f);
-        const int u = u0 + i * kWaves + wave;
-        if (u < parts && lane == 0) squares[token[i] * 16 + (u - token[i] * spans)] = ss;
-      }
-    }
-    __syncthreads();
+// Rows of bf16 into LDS, 16-byte piece p of row r at r RS + p: a wave takes 64 pieces of a
+// row at a time, four such under way.  64 pieces behind the last row take what is not there.
+struct Rows {
+  __amdgpu_buffer_rsrc_t src;
+  int pieces, spans, RS, spare, wave, lane;  // of a row; 64s of them; a row in LDS; the pieces behind
+  u32x4_t v[4];
+  int to[4];
+  __device__ __forceinline__ void open(const void* rows, int bytes, int n8, int lds_rows, int w, int l) {
+    src = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(rows), (short)0, bytes, 0x00020000);
+    pieces = n8;
+    spans = (n8 + 63) >> 6;
+    RS = row_stride(n8 >> 2);
+    spare = lds_rows * RS + l;
+    wave = w;
+    lane = l;
   }
-  for (int u0 = 0; u0 < parts; u0 += SLOTS * kWaves) {
-    if (parts > SLOTS * kWaves) load(u0);
+  // parts u0, u0 + kWaves, ... of the rows from row0 on
+  __device__ __forceinline__ void load(int u0, int parts, int row0) {
 #pragma unroll
-    for (int i = 0; i < SLOTS; i++) {
-      uint4 o = raw[i][0];
-      if (NORM) {
-        float v[8], w[8];
-        values(i, v);
-        unpack8(wn[i], w);
-        const float ss = row16_total((lane & 15) < spans ? squares[token[i] * 16 + (lane & 15)] : 0.f);
-        const float r = __builtin_amdgcn_rsqf(fmaf(ss, a.inv_H, a.eps));
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = v[j] * r * w[j];
-        o = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-      }
-      const int p = piece[i];
-      if (p < H8) xs[token[i] * RS + p] = o;
+    for (int i = 0; i < 4; i++) {
+      const int u = u0 + i * kWaves, r = u / spans, p = (u - r * spans) * 64 + lane;
+      const bool there = u < parts && p < pieces;
+      uint32_t from = there ? (uint32_t)((row0 + r) * pieces + p) * 16 : kPast;
+      to[i] = there ? r * RS + p : spare;
+      asm("" : "+v"(from), "+v"(to[i]));  // both chosen here: no branch around the load
+      v[i] = __builtin_amdgcn_raw_buffer_load_b128(src, from, 0, 0);
     }
+  }
+  __device__ __forceinline__ void store(uint4* lds) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) lds[to[i]] = __builtin_bit_cast(uint4, v[i]);
+  }
+  __device__ __forceinline__ void all(uint4* lds, int parts, int row0) {
+    for (int u0 = wave; u0 < parts; u0 += 4 * kWaves) {
+      load(u0, parts, row0);
+      store(lds);
+    }
+  }
+};
+
+// Norm and router.  ONCE: a lane holds its pieces of a row, else it goes over the row again.
+template <bool F32, bool NORM, bool ONCE>
+__global__ __launch_bounds__(kRouterWaves * 64) void layer_router_kernel(MoeLayerArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int H8 = a.H >> 3, e = blockIdx.x;
+  const uint4* const router = reinterpret_cast<const uint4*>(a.router_w) + (size_t)e * H8;
+  const float bias = a.router_b ? bf16_bits_to_f32(a.router_b[e]) : 0.f;
+  for (int t = wave; t < a.T; t += kRouterWaves) {
+    const uint4* const x = reinterpret_cast<const uint4*>(a.x) + (size_t)t * H8 * (F32 ? 2 : 1);
+    uint4 raw[kPieces][F32 ? 2 : 1], wn[kPieces], rw[kPieces];
+    auto load_x = [&](int p0) {
+#pragma unroll
+      for (int i = 0; i < kPieces; i++) {
+        const int p = min(p0 + 64 * i + lane, H8 - 1);
+        raw[i][0] = x[p * (F32 ? 2 : 1)];
+        if (F32) raw[i][F32 ? 1 : 0] = x[p * 2 + 1];
+      }
+    };
+    auto load_w = [&](int p0) {
+#pragma unroll
+      for (int i = 0; i < kPieces; i++) {
+        const int p = min(p0 + 64 * i + lane, H8 - 1);
+        if (NORM) wn[i] = reinterpret_cast<const uint4*>(a.w_norm)[p];
+        rw[i] = router[p];
+      }
+    };
+    auto values = [&](int i, float (&v)[8]) {
+      if (F32) {
+        const uint4 lo = raw[i][0], hi = raw[i][F32 ? 1 : 0];
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
+      } else {
+        unpack8(raw[i][0], v);
+      }
+    };
+    float ss = 0.f, r = 1.f, acc = 0.f;
+    auto square = [&](int p0) {
+#pragma unroll
+      for (int i = 0; i < kPieces; i++) {
+        float v[8], s = 0.f;
+        values(i, v);
+#pragma unroll
+        for (int j = 0; j < 8; j++) s = fmaf(v[j], v[j], s);
+        ss += p0 + 64 * i + lane < H8 ? s : 0.f;
+      }
+    };
+    auto dot = [&](int p0) {
+#pragma unroll
+      for (int i = 0; i < kPieces; i++) {
+        const int p = p0 + 64 * i + lane;
+        uint4 o = raw[i][0];
+        if (NORM) {
+          float v[8], w[8];
+          values(i, v);
+          unpack8(wn[i], w);
+#pragma unroll
+          for (int j = 0; j < 8; j++) v[j] = v[j] * r * w[j];
+          o = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+        }
+        const uint32_t xv[4] = {o.x, o.y, o.z, o.w}, wv[4] = {rw[i].x, rw[i].y, rw[i].z, rw[i].w};
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, xv[j]), __builtin_bit_cast(bf16x2_t, wv[j]),
+                                              s, false);
+        acc += p < H8 ? s : 0.f;
+        if (NORM && p < H8 && t % gridDim.x == e) reinterpret_cast<uint4*>(a.ws_xn)[(size_t)t * H8 + p] = o;
+      }
+    };
+    load_x(0);
+    if (ONCE) {
+      load_w(0);
+      if (NORM) square(0);
+    } else if (NORM) {
+      square(0);
+      for (int p0 = 64 * kPieces; p0 < H8; p0 += 64 * kPieces) {
+        load_x(p0);
+        square(p0);
+      }
+    }
+    if (NORM) r = __builtin_amdgcn_rsqf(fmaf(wave_total(ss), a.inv_H, a.eps));
+    if (ONCE) {
+      dot(0);
+    } else {
+      for (int p0 = 0; p0 < H8; p0 += 64 * kPieces) {
+        load_x(p0);
+        load_w(p0);
+        dot(p0);
+      }
+    }
+    acc = wave_total(acc);
+    if (lane == 0) a.ws_logits[t * 64 + e] = acc + bias;
   }
 }
 
-// Norm, router, routing, and the gate/up projection through the activation.
-template <bool F32, bool NORM, int C, int TEAMS>
+// Routing, and the gate/up projection through the activation.
+template <int C, int TEAMS>
 __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a) {
-  // the tokens' rows, then (16-byte aligned) partial sums: of the router, then two rounds of the teams' units
+  // the tokens' rows, 64 pieces, then two rounds of the teams' partial sums
   extern __shared__ __attribute__((aligned(16))) uint4 xs[];
-  __shared__ __attribute__((aligned(16))) float squares[kLayerMaxT * 16];
   __shared__ uint32_t tokens[64];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, q = lane >> 4;
-  const int KB = a.H >> 5, H8 = a.H >> 3, RS = row_stride(KB);
-  float4* const part = reinterpret_cast<float4*>(xs + a.T * RS);
-
-  // router: 16 experts' rows a tile, the tile's K split over kWaves / tiles waves
-  const int tiles = (a.E + 15) >> 4, shares = kWaves / tiles;
-  const int tile = wave / shares, share = wave - tile * shares;
-  const int per_share = (KB + shares - 1) / shares;
-  const int r0 = share * per_share, r1 = min(r0 + per_share, KB);
-  const uint4* const router =
-      reinterpret_cast<const uint4*>(a.router_w) + (size_t)min(tile * 16 + col, a.E - 1) * H8 + q;
-  uint4 rw[kRouterRing];
-  auto load_router = [&](int b0) {
-#pragma unroll
-    for (int i = 0; i < kRouterRing; i++) rw[i] = router[4 * min(b0 + i, KB - 1)];
-  };
-  const uint32_t router_bias = (a.router_b ? a.router_b : a.router_w)[min(lane, a.E - 1)];
-  if (tid < 64) tokens[tid] = 0;
-  if (a.T * ((H8 + 63) >> 6) <= kWaves)
-    stage_rows<F32, NORM, 1>(a, xs, RS, squares, wave, lane, [&]() { load_router(r0); });
-  else
-    stage_rows<F32, NORM, 4>(a, xs, RS, squares, wave, lane, [&]() { load_router(r0); });
-  __syncthreads();
-
+  const int KB = a.H >> 5, RS = row_stride(KB);
+  float4* const part = reinterpret_cast<float4*>(xs + a.T * RS + 64);
   const int xrow = min(col, a.T - 1) * RS;  // (columns past the tokens repeat the last)
-  {
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    for (int b0 = r0; b0 < r1; b0 += kRouterRing) {
-      if (b0 != r0) load_router(b0);
-#pragma unroll
-      for (int i = 0; i < kRouterRing; i++)
-        if (b0 + i < r1)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, rw[i]),
-                                                        __builtin_bit_cast(bf16x8_t, xs[xrow + 4 * (b0 + i) + q]), acc,
-                                                        0, 0, 0);
-    }
-    if (col < a.T) part[(wave * a.T + col) * 4 + q] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  }
+
+  const float first_logit = lane < a.E && wave < a.T ? a.ws_logits[wave * 64 + lane] : 0.f;
+  if (tid < 64) tokens[tid] = 0;
+  Rows rows;
+  rows.open(a.w_norm ? a.ws_xn : a.x, a.T * a.H * 2, a.H >> 3, a.T, wave, lane);
+  rows.load(wave, a.T * rows.spans, 0);
   __syncthreads();
 
   // routing: a wave a token, lane e expert e; k rounds of the largest logit, the lowest index among equals
   for (int t = wave; t < a.T; t += kWaves) {
-    float d[kWaves];
-#pragma unroll
-    for (int s = 0; s < kWaves; s++) {
-      const int w = min((lane >> 4) * shares + min(s, shares - 1), kWaves - 1);
-      d[s] = reinterpret_cast<const float*>(part)[(w * a.T + t) * 16 + (lane & 15)];
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int s = 0; s < kWaves; s++) sum += s < shares ? d[s] : 0.f;
-    const float l = lane < a.E ? sum + (a.router_b ? bf16_bits_to_f32(router_bias) : 0.f) : -INFINITY;
+    const float given = t == wave ? first_logit : a.ws_logits[t * 64 + min(lane, a.E - 1)];
+    const float l = lane < a.E ? given : -INFINITY;
     const bool bad = wave_ballot(!(l < INFINITY)) != 0;  // a NaN or an infinity has no softmax
     bool open = lane < a.E, mine = false;
     float top = 0.f, of_slot = 0.f;  // the largest logit; lane s: that of slot s
@@ -320,6 +351,11 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
         if (a.gates) a.gates[t * a.k + lane] = bad ? 0.f : g / all;
       }
     }
+  }
+  rows.store(xs);
+  for (int u0 = wave + 4 * kWaves; u0 < a.T * rows.spans; u0 += 4 * kWaves) {
+    rows.load(u0, a.T * rows.spans, 0);
+    rows.store(xs);
   }
   __syncthreads();
   const Experts x = list_experts(tokens[lane], lane);
@@ -403,7 +439,7 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
 
 // The down projection, the combine and the residual: a workgroup owns 16 output columns of
 // all tokens, its waves share K.  DEPTH experts' weights are under way; the activations lie
-// in LDS, as many experts' at a time as fit (a multiple of DEPTH).
+// in LDS, as many experts' at a time as fit (one's at least: T rows).
 template <int C, int DEPTH>
 __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, int lds_rows) {
   extern __shared__ __attribute__((aligned(16))) uint4 as[];  // as the tokens' rows above
@@ -429,6 +465,18 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
   for (int i = 0; i < 2; i++) gate_in[i] = a.ws_gates[min(tid + i * kThreads, a.T * 64 - 1)];
 
   const int count = __popcll(wave_ballot(x.tokens != 0));
+  // the activations' rows of the experts that fit
+  Rows rows;
+  rows.open(a.act, a.T * a.k * a.F * 2, F8, lds_rows, wave, lane);
+  int first = 0, last = 0, row0 = 0, parts = 0;
+  auto next_rows = [&]() {
+    first = last;
+    row0 = first ? __builtin_amdgcn_readlane(x.rows_to, first - 1) : 0;
+    last = min(count, __popcll(wave_ballot(x.rows_to - row0 <= lds_rows)));  // at least one more
+    parts = (__builtin_amdgcn_readlane(x.rows_to, max(last, 1) - 1) - row0) * rows.spans;
+  };
+  next_rows();
+
   Stream<C> st[DEPTH];
   Places<C> at;
   at.set(col, wave * 4 * C + q, KB);
@@ -437,72 +485,64 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
                (size_t)__builtin_amdgcn_readlane(x.expert, min(i, 63)) * a.H + (size_t)blockIdx.x * 16,
                KB, i < count);
   };
-#pragma unroll
-  for (int d = 0; d < DEPTH; d++) {
-    open(d, d);
-#pragma unroll
-    for (int j = 0; j < C; j++) st[d].load(j, at.w[j], at.s[j]);
-  }
   const uint16_t* const bias = a.down_bias ? a.down_bias : a.router_w;  // (read and not used without one)
   auto bias_of = [&](int e) { return (uint32_t)bias[a.down_bias ? (size_t)max(e, 0) * a.H + out_c : 0]; };
-  uint32_t bias_bits[4];
+  uint32_t bias_bits[4], x_bits;
+  auto load_weights = [&]() {
 #pragma unroll
-  for (int s = 0; s < 4; s++) bias_bits[s] = bias_of(id[s]);
-  // (the 32 bits that hold x: x is 16-byte aligned and H even)
-  const uint32_t x_bits = static_cast<const uint32_t*>(a.x)[a.x_f32 ? out_at : out_at >> 1];
+    for (int d = 0; d < DEPTH; d++) {
+      open(d, d);
+#pragma unroll
+      for (int j = 0; j < C; j++) st[d].load(j, at.w[j], at.s[j]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; s++) bias_bits[s] = bias_of(id[s]);
+    // (the 32 bits that hold x: x is 16-byte aligned and H even)
+    x_bits = static_cast<const uint32_t*>(a.x)[a.x_f32 ? out_at : out_at >> 1];
+  };
+  // A wave that cannot issue its weights' loads for the others' waits: a few rows come before
+  // them; more would keep memory waiting for their latency, and go behind.
+  if (parts <= 4 * kWaves) {
+    rows.load(wave, parts, 0);
+    rows.store(as);
+    load_weights();
+  } else {
+    load_weights();
+    rows.all(as, parts, 0);
+  }
 #pragma unroll
   for (int i = 0; i < 2; i++)
     if (tid + i * kThreads < a.T * 64) gates[tid + i * kThreads] = gate_in[i];
-  const __amdgpu_buffer_rsrc_t act =
-      __builtin_amdgcn_make_buffer_rsrc(a.act, (short)0, a.T * a.k * a.F * 2, 0x00020000);
-
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
   const int tcol = min(col, a.T - 1);
-  for (int first = 0; first < count;) {
-    // the experts whose rows fit, by DEPTH unless they are the last
-    const int row0 = first ? __builtin_amdgcn_readlane(x.rows_to, first - 1) : 0;
-    int last = min(count, __popcll(wave_ballot(x.rows_to - row0 <= lds_rows)));
-    if (last < count) last -= (last - first) % DEPTH;
-    const int rows = __builtin_amdgcn_readlane(x.rows_to, last - 1) - row0;
-    const int spans = (F8 + 63) >> 6, parts = rows * spans;
-    for (int u0 = wave; u0 < parts; u0 += 4 * kWaves) {
-      u32x4_t v[4];
-      int to[4];
+  __syncthreads();
+  for (int i0 = 0; i0 < count; i0 += DEPTH) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int u = u0 + i * kWaves, r = u / spans, p = (u - r * spans) * 64 + lane;
-        const bool there = u < parts && p < F8;
-        v[i] = __builtin_amdgcn_raw_buffer_load_b128(act, there ? (uint32_t)((row0 + r) * F8 + p) * 16 : kPast, 0, 0);
-        to[i] = there ? r * RS + p : lds_rows * RS + lane;  // (64 pieces behind the rows)
+    for (int d = 0; d < DEPTH; d++) {
+      // (past the last expert: no token, and weights that read as zeros)
+      const int i = min(i0 + d, 63);
+      if (i0 + d == last && last < count) {
+        next_rows();
+        __syncthreads();
+        rows.all(as, parts, row0);
+        __syncthreads();
       }
+      const uint32_t m = i0 + d < count ? __builtin_amdgcn_readlane(x.tokens, i) : 0u;
+      const bool has = (m >> col) & 1;
+      // this token's row; where it does not have the expert, some row, not used
+      const int row = has ? __builtin_amdgcn_readlane(x.rows_to, i) - row0 - __popc(m >> col) : 0;
+      const uint4* const in = as + row * RS;
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+      open(d, i0 + d + DEPTH);
 #pragma unroll
-      for (int i = 0; i < 4; i++) as[to[i]] = __builtin_bit_cast(uint4, v[i]);
-    }
-    __syncthreads();
-    for (int i0 = first; i0 < last; i0 += DEPTH) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; d++) {
-        // (past the last expert: no token, weights that read as zeros)
-        const int i = min(i0 + d, 63);
-        const uint32_t m = i0 + d < last ? __builtin_amdgcn_readlane(x.tokens, i) : 0u;
-        const bool has = (m >> col) & 1;
-        // this token's row; where it does not have the expert, some row, not used
-        const int row = has ? __builtin_amdgcn_readlane(x.rows_to, i) - row0 - __popc(m >> col) : 0;
-        const uint4* const in = as + row * RS;
-        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-        open(d, i0 + d + DEPTH);
-#pragma unroll
-        for (int j = 0; j < C; j++) {
-          acc = item_mma(st[d].w[j], st[d].s[j], in + at.x[j], acc);
-          st[d].load(j, at.w[j], at.s[j]);
-        }
-        const float gt = gates[tcol * 64 + __builtin_amdgcn_readlane(x.expert, i)], g = has ? gt : 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; r++) y[r] = g != 0.f ? fmaf(g, acc[r], y[r]) : y[r];  // (0 adds nothing)
+      for (int j = 0; j < C; j++) {
+        acc = item_mma(st[d].w[j], st[d].s[j], in + at.x[j], acc);
+        st[d].load(j, at.w[j], at.s[j]);
       }
+      const float gt = gates[tcol * 64 + __builtin_amdgcn_readlane(x.expert, i)], g = has ? gt : 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; r++) y[r] = g != 0.f ? fmaf(g, acc[r], y[r]) : y[r];  // (0 adds nothing)
     }
-    first = last;
-    if (first < count) __syncthreads();
   }
   if (col < a.T) part[(wave * a.T + col) * 4 + q] = make_float4(y[0], y[1], y[2], y[3]);
   __syncthreads();
@@ -512,12 +552,16 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
     for (int p = 0; p < kWaves; p++) d[p] = reinterpret_cast<const float*>(part)[(p * a.T + out_t) * 16 + (tid & 15)];
 #pragma unroll
     for (int p = 0; p < kWaves; p++) sum += d[p];
-    for (int s = 0; s < a.k; s++) {
-      const int e = s == 0 ? id[0] : s == 1 ? id[1] : s == 2 ? id[2] : s == 3 ? id[3] : a.ws_ids[out_t * a.k + s];
-      const uint32_t b =
-          s == 0 ? bias_bits[0] : s == 1 ? bias_bits[1] : s == 2 ? bias_bits[2] : s == 3 ? bias_bits[3] : bias_of(e);
+    auto add_bias = [&](int e, uint32_t b) {
       const float g = e >= 0 && a.down_bias ? gates[out_t * 64 + e] : 0.f;
       if (g != 0.f) sum = fmaf(g, bf16_bits_to_f32(b), sum);
+    };
+#pragma unroll
+    for (int s = 0; s < 4; s++)
+      if (s < a.k) add_bias(id[s], bias_bits[s]);
+    for (int s = 4; s < a.k; s++) {
+      const int e = a.ws_ids[out_t * a.k + s];
+      add_bias(e, bias_of(e));
     }
     const float xv = __uint_as_float(a.x_f32 ? x_bits : out_at & 1 ? x_bits & 0xffff0000u : x_bits << 16);
     const float h = a.residual ? xv + sum : sum;
@@ -529,28 +573,34 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
 // items that a wave of a team holds for its share of KB blocks, by twos
 int items_of(int KB, int team) { return ((KB + 4 * team - 1) / (4 * team) + 1) / 2 * 2; }
 
-template <bool F32, bool NORM, int C, int TEAMS>
+template <bool F32, bool NORM>
+hipError_t launch_router(const MoeLayerArgs& a, hipStream_t stream) {
+  const dim3 grid(a.E), block((a.T < kRouterWaves ? a.T : kRouterWaves) * 64);
+  if (a.H / 8 <= 64 * kPieces) hipLaunchKernelGGL((layer_router_kernel<F32, NORM, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((layer_router_kernel<F32, NORM, false>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int C, int TEAMS>
 hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
-  static DynLdsLimit limit(reinterpret_cast<const void*>(layer_gate_up_kernel<F32, NORM, C, TEAMS>), kLayerUpLds);
-  // the tokens' rows, and two rounds of partial sums (the router's take the room of one)
-  const size_t lds = (size_t)a.T * row_stride(a.H / 32) * 16 + (size_t)2 * kWaves * 64 * a.T;
+  static DynLdsLimit limit(reinterpret_cast<const void*>(layer_gate_up_kernel<C, TEAMS>), kLayerUpLds);
+  const size_t lds = ((size_t)a.T * row_stride(a.H / 32) + 64) * 16 + (size_t)2 * kWaves * 64 * a.T;
   if (lds > (size_t)kLayerUpLds) return hipErrorInvalidConfiguration;
   const hipError_t e = limit.ensure();
   if (e != hipSuccess) return e;
   const int R = a.T * a.k, most = (R < a.E ? R : a.E) * (a.F / 8);  // units of all experts that the tokens can reach
-  hipLaunchKernelGGL((layer_gate_up_kernel<F32, NORM, C, TEAMS>), dim3(most < kGroups ? most : kGroups), dim3(kThreads), lds,
+  hipLaunchKernelGGL((layer_gate_up_kernel<C, TEAMS>), dim3(most < kGroups ? most : kGroups), dim3(kThreads), lds,
                      stream, a);
   return hipGetLastError();
 }
-template <bool F32, bool NORM>
 hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
   // three teams of 4 waves while a wave's share of K is 6 items at most, else one of 12
   const int KB = a.H / 32, C = items_of(KB, kWaves / 3);
-  return C == 2                     ? launch_up<F32, NORM, 2, 3>(a, stream)
-         : C == 4                   ? launch_up<F32, NORM, 4, 3>(a, stream)
-         : C == 6                   ? launch_up<F32, NORM, 6, 3>(a, stream)
-         : items_of(KB, kWaves) <= 4 ? launch_up<F32, NORM, 4, 1>(a, stream)
-                                    : launch_up<F32, NORM, 6, 1>(a, stream);
+  return C == 2                      ? launch_up<2, 3>(a, stream)
+         : C == 4                    ? launch_up<4, 3>(a, stream)
+         : C == 6                    ? launch_up<6, 3>(a, stream)
+         : items_of(KB, kWaves) <= 4 ? launch_up<4, 1>(a, stream)
+                                     : launch_up<6, 1>(a, stream);
 }
 
 template <int C, int DEPTH>
@@ -558,10 +608,7 @@ hipError_t launch_down(const MoeLayerArgs& a, hipStream_t stream) {
   static DynLdsLimit limit(reinterpret_cast<const void*>(layer_down_kernel<C, DEPTH>), kLayerDownLds);
   const size_t row = (size_t)row_stride(a.F / 32) * 16;
   const int fit = (int)(((size_t)kLayerDownLds - 64 * 16) / row), R = a.T * a.k;
-  if (fit < R && fit < DEPTH * a.T) {  // DEPTH experts' rows may not fit
-    if constexpr (DEPTH > 1) return launch_down<C, 1>(a, stream);
-    return hipErrorInvalidConfiguration;
-  }
+  if (fit < a.T) return hipErrorInvalidConfiguration;
   const hipError_t e = limit.ensure();
   if (e != hipSuccess) return e;
   const int rows = fit < R ? fit : R;
@@ -574,22 +621,32 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t moe_layer_workspace_bytes(int T, int k, int F) {
-  return T ? 1024 + (size_t)T * (64 * 4 + kLayerMaxTopK * 4) + align256((size_t)T * k * F * 2) : 0;
+size_t moe_layer_workspace_bytes(int T, int H, int k, int F) {
+  return T ? 1024 + (size_t)T * (2 * 64 * 4 + kLayerMaxTopK * 4) + align256((size_t)T * H * 2) +
+                 align256((size_t)T * k * F * 2)
+           : 0;
 }
 
 hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream) {
-  uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  a.ws_experts = reinterpret_cast<int32_t*>(ws);
-  a.ws_gates = reinterpret_cast<float*>(ws + 1024);
-  a.ws_ids = reinterpret_cast<int32_t*>(ws + 1024 + (size_t)a.T * 64 * 4);
-  a.act = reinterpret_cast<uint16_t*>(ws + 1024 + (size_t)a.T * (64 * 4 + kLayerMaxTopK * 4));
-  const hipError_t e = !a.w_norm ? launch_up<false, false>(a, stream)
-                       : a.x_f32 ? launch_up<true, true>(a, stream)
-                                 : launch_up<false, true>(a, stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto take = [&](size_t bytes) {
+    uint8_t* const p = ws;
+    ws += bytes;
+    return p;
+  };
+  a.ws_experts = reinterpret_cast<int32_t*>(take(1024));
+  a.ws_logits = reinterpret_cast<float*>(take((size_t)a.T * 64 * 4));
+  a.ws_gates = reinterpret_cast<float*>(take((size_t)a.T * 64 * 4));
+  a.ws_ids = reinterpret_cast<int32_t*>(take((size_t)a.T * kLayerMaxTopK * 4));
+  a.ws_xn = reinterpret_cast<uint16_t*>(take(align256((size_t)a.T * a.H * 2)));
+  a.act = reinterpret_cast<uint16_t*>(ws);
+  hipError_t e = !a.w_norm ? launch_router<false, false>(a, stream)
+                 : a.x_f32 ? launch_router<true, true>(a, stream)
+                           : launch_router<false, true>(a, stream);
+  if (e == hipSuccess) e = launch_up(a, stream);
   if (e != hipSuccess) return e;
   const int C = items_of(a.F / 32, kWaves);  // (6 at most)
-  return C == 2 ? launch_down<2, 3>(a, stream) : C == 4 ? launch_down<4, 2>(a, stream) : launch_down<6, 1>(a, stream);
+  return C == 2 ? launch_down<2, 2>(a, stream) : C == 4 ? launch_down<4, 1>(a, stream) : launch_down<6, 1>(a, stream);
 }
 
 }  // namespace mxfp4
