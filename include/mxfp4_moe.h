@@ -534,7 +534,7 @@ int mxfp4_expert_matmul_swiglu(const uint8_t* blocks, const uint8_t* scales, con
 size_t mxfp4_moe_layer_workspace_size(int T, int H, int E, int k, int F);
 
 /*
- * A whole expert layer for a few decoded tokens in two launches: moe_norm,
+ * A whole expert layer for a few decoded tokens in three launches: moe_norm,
  * mxfp4_moe_router, the routing, mxfp4_expert_proj_swiglu, mxfp4_expert_proj and
  * the combine with the residual.
  *

@@ -9,7 +9,7 @@
 // The borders of the launches are the two points where every workgroup needs what all
 // others made; no workgroup waits for another.  With the norm and the router in the
 // gate/up launch too (each workgroup its own) the layer took 27.3 us for one token of
-// H = F = 2880, E = 32, k = 4 instead of @ONE@: 256 CUs read the same 184 KB at 17 bytes a
+// H = F = 2880, E = 32, k = 4 instead of 23.3: 256 CUs read the same 184 KB at 17 bytes a
 // clock each, three times what a launch costs.
 //
 // Both projections stream the chosen experts' weights once for all tokens, by items of 16
@@ -79,25 +79,6 @@ __device__ __forceinline__ f32x4_t item_mma(const u32x4_t w, uint32_t scale, con
   return acc;
 }
 
-// A wave's part of a unit's K: C items held in registers; each is loaded again, for the next
-// unit, as soon as it is used.
-template <int C>
-struct Stream {
-  u32x4_t w[C];
-  uint32_t s[C];
-  __amdgpu_buffer_rsrc_t wsrc, ssrc;  // the unit's 16 rows; of no bytes if there is none: zeros
-  __device__ __forceinline__ void open(const uint8_t* blocks, const uint8_t* scales, size_t first_row, int KB,
-                                       bool any) {
-    wsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(blocks + first_row * KB * 16), (short)0,
-                                             any ? 16 * KB * 16 : 0, 0x00020000);
-    ssrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales + first_row * KB), (short)0,
-                                             any ? 16 * KB : 0, 0x00020000);
-  }
-  __device__ __forceinline__ void load(int j, uint32_t w_at, uint32_t s_at) {
-    w[j] = __builtin_amdgcn_raw_buffer_load_b128(wsrc, w_at, 0, 0);
-    s[j] = __builtin_amdgcn_raw_buffer_load_b8(ssrc, s_at, 0, 0);
-  }
-};
 // Where a lane finds its blocks b, b + 4, ... of a row: in a unit's codes and scales, zeros
 // past the row, and among the row's inputs, past it the last block's.
 template <int C>
@@ -112,6 +93,41 @@ struct Places {
       w[j] = in ? (row * KB + b + 4 * j) * 16 : kPast;
       x[j] = min(b + 4 * j, KB - 1) * 4;
     }
+  }
+};
+
+// A wave's part of a unit's K: C items held in registers; each is loaded again, for the next
+// unit, as soon as it is used.
+template <int C>
+struct Stream {
+  u32x4_t w[C];
+  uint32_t s[C];
+  __amdgpu_buffer_rsrc_t wsrc, ssrc;  // the unit's 16 rows; of no bytes if there is none: zeros
+  __device__ __forceinline__ void open(const uint8_t* blocks, const uint8_t* scales, size_t first_row, int KB,
+                                       bool any) {
+    wsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(blocks + first_row * KB * 16), (short)0,
+                                             any ? 16 * KB * 16 : 0, 0x00020000);
+    ssrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales + first_row * KB), (short)0,
+                                             any ? 16 * KB : 0, 0x00020000);
+  }
+  // Items j and j + 1: the two halves of 128 bytes of a row, one after the other.  They stay in
+  // the order of their use: the codes moved before all scales, the first item waited for all.
+  __device__ __forceinline__ void load2(int j, const Places<C>& at) {
+    w[j] = __builtin_amdgcn_raw_buffer_load_b128(wsrc, at.w[j], 0, 0);
+    w[j + 1] = __builtin_amdgcn_raw_buffer_load_b128(wsrc, at.w[j + 1], 0, 0);
+    s[j] = __builtin_amdgcn_raw_buffer_load_b8(ssrc, at.s[j], 0, 0);
+    s[j + 1] = __builtin_amdgcn_raw_buffer_load_b8(ssrc, at.s[j + 1], 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ __forceinline__ f32x4_t use(const Places<C>& at, const uint4* x) {
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < C; j += 2) {
+      acc = item_mma(w[j], s[j], x + at.x[j], acc);
+      acc = item_mma(w[j + 1], s[j + 1], x + at.x[j + 1], acc);
+      load2(j, at);
+    }
+    return acc;
   }
 };
 
@@ -206,7 +222,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void layer_router_kernel(MoeLaye
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H8 = a.H >> 3, e = blockIdx.x;
   const uint4* const router = reinterpret_cast<const uint4*>(a.router_w) + (size_t)e * H8;
-  const float bias = a.router_b ? bf16_bits_to_f32(a.router_b[e]) : 0.f;
+  const uint16_t* const bias = a.router_b ? a.router_b + e : a.router_w;  // (read and not used without one)
   for (int t = wave; t < a.T; t += kRouterWaves) {
     const uint4* const x = reinterpret_cast<const uint4*>(a.x) + (size_t)t * H8 * (F32 ? 2 : 1);
     uint4 raw[kPieces][F32 ? 2 : 1], wn[kPieces], rw[kPieces];
@@ -236,6 +252,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void layer_router_kernel(MoeLaye
         unpack8(raw[i][0], v);
       }
     };
+    const bool keeps = NORM && t % a.E == e;  // one workgroup writes a token's row
     float ss = 0.f, r = 1.f, acc = 0.f;
     auto square = [&](int p0) {
 #pragma unroll
@@ -267,12 +284,14 @@ __global__ __launch_bounds__(kRouterWaves * 64) void layer_router_kernel(MoeLaye
           s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, xv[j]), __builtin_bit_cast(bf16x2_t, wv[j]),
                                               s, false);
         acc += p < H8 ? s : 0.f;
-        if (NORM && p < H8 && t % gridDim.x == e) reinterpret_cast<uint4*>(a.ws_xn)[(size_t)t * H8 + p] = o;
+        if (keeps && p < H8) reinterpret_cast<uint4*>(a.ws_xn)[(size_t)t * H8 + p] = o;
       }
     };
     load_x(0);
+    const uint32_t bias_bits = *bias;
     if (ONCE) {
       load_w(0);
+      __builtin_amdgcn_sched_barrier(0);  // every load is on its way before the first is waited for
       if (NORM) square(0);
     } else if (NORM) {
       square(0);
@@ -292,7 +311,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void layer_router_kernel(MoeLaye
       }
     }
     acc = wave_total(acc);
-    if (lane == 0) a.ws_logits[t * 64 + e] = acc + bias;
+    if (lane == 0) a.ws_logits[t * 64 + e] = a.router_b ? acc + bf16_bits_to_f32(bias_bits) : acc;
   }
 }
 
@@ -369,8 +388,8 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
   // Units of 16 rows (8 gate and up pairs) of the chosen experts, spread evenly over the
   // workgroups; a workgroup's go to its teams in turn, one a round.
   const int per = a.F >> 3, units = count * per;  // (per >= 4)
-  const int u0 = (int)((long long)units * blockIdx.x / gridDim.x);
-  const int mine = (int)((long long)units * (blockIdx.x + 1) / gridDim.x) - u0;
+  const int u0 = (unsigned)units * blockIdx.x / gridDim.x;  // (units <= 2^16, 256 workgroups)
+  const int mine = (int)((unsigned)units * (blockIdx.x + 1) / gridDim.x) - u0;
   if (mine == 0) return;
   constexpr int kTeam = kWaves / TEAMS;
   const int team = wave / kTeam, part_of = wave - team * kTeam;
@@ -391,14 +410,13 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
   };
   next_unit();
 #pragma unroll
-  for (int j = 0; j < C; j++) st.load(j, at.w[j], at.s[j]);
+  for (int j = 0; j < C; j += 2) st.load2(j, at);
   // the sum over a team, the bias and the activation: a thread has a unit's pair of rows and a token
   const int out_pair = tid & 7, out_t = (tid >> 3) & 15, out_team = min(tid >> 7, TEAMS - 1);
   const int out_tr = min(out_t, a.T - 1);
   int out_i = (u0 + out_team) / per, out_tile = u0 + out_team - out_i * per;
   const uint16_t* const bias = a.gu_bias ? a.gu_bias : a.router_w;  // (read and not used without one)
   for (int r = 0; r < rounds; r++) {
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     const bool out = tid < TEAMS * 128 && out_t < a.T && r * TEAMS + out_team < mine;
     // its bias is loaded ahead of the next round's weights: loads return in order
     const int oi = min(out_i, count - 1), e = __shfl(x.expert, oi, 64), row = out_tile * 16 + 2 * out_pair;
@@ -407,11 +425,7 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
     const size_t bias_at = a.gu_bias ? (size_t)e * 2 * a.F + row : 0;
     const uint32_t gate_bias = bias[bias_at], up_bias = bias[bias_at + 1];
     next_unit();
-#pragma unroll
-    for (int j = 0; j < C; j++) {
-      acc = item_mma(st.w[j], st.s[j], xs + xrow + at.x[j], acc);
-      st.load(j, at.w[j], at.s[j]);
-    }
+    const f32x4_t acc = st.use(at, xs + xrow);
     float4* const mine_of = part + (r & 1) * kWaves * a.T * 4;
     if (col < a.T) mine_of[(wave * a.T + col) * 4 + q] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
@@ -493,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
     for (int d = 0; d < DEPTH; d++) {
       open(d, d);
 #pragma unroll
-      for (int j = 0; j < C; j++) st[d].load(j, at.w[j], at.s[j]);
+      for (int j = 0; j < C; j += 2) st[d].load2(j, at);
     }
 #pragma unroll
     for (int s = 0; s < 4; s++) bias_bits[s] = bias_of(id[s]);
@@ -531,14 +545,8 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
       const bool has = (m >> col) & 1;
       // this token's row; where it does not have the expert, some row, not used
       const int row = has ? __builtin_amdgcn_readlane(x.rows_to, i) - row0 - __popc(m >> col) : 0;
-      const uint4* const in = as + row * RS;
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
       open(d, i0 + d + DEPTH);
-#pragma unroll
-      for (int j = 0; j < C; j++) {
-        acc = item_mma(st[d].w[j], st[d].s[j], in + at.x[j], acc);
-        st[d].load(j, at.w[j], at.s[j]);
-      }
+      const f32x4_t acc = st[d].use(at, as + row * RS);
       const float gt = gates[tcol * 64 + __builtin_amdgcn_readlane(x.expert, i)], g = has ? gt : 0.f;
 #pragma unroll
       for (int r = 0; r < 4; r++) y[r] = g != 0.f ? fmaf(g, acc[r], y[r]) : y[r];  // (0 adds nothing)
@@ -646,7 +654,11 @@ hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream)
   if (e == hipSuccess) e = launch_up(a, stream);
   if (e != hipSuccess) return e;
   const int C = items_of(a.F / 32, kWaves);  // (6 at most)
-  return C == 2 ? launch_down<2, 2>(a, stream) : C == 4 ? launch_down<4, 1>(a, stream) : launch_down<6, 1>(a, stream);
+  // Two experts under way where their parts of K are short and most experts are reached (16
+  // tokens, E = 64, k = 8, H = F = 1024: 73 us for 82 with one); else one: the rows and the end
+  // wait for less (one token of H = F = 2880, E = 32, k = 4: 23.3 us for 25.1 with two).
+  if (C == 2 && a.F < 48 * 32 && a.T * a.k >= a.E) return launch_down<2, 2>(a, stream);
+  return C == 2 ? launch_down<2, 1>(a, stream) : C == 4 ? launch_down<4, 1>(a, stream) : launch_down<6, 1>(a, stream);
 }
 
 }  // namespace mxfp4

@@ -8,7 +8,8 @@ alike costs nothing and one near a border its whole step.
   sums    an MFMA adds the products of 32 elements to its accumulator; taken as a sum aligned to its
           largest term and cut there, 32 2^-23 of the terms' magnitudes over all steps, and each step's
           sum is rounded (2^-23 with cutting), K / 32 times, then 12 waves' partial sums and the bias:
-          (2^-18 + (K / 32 + 16) 2^-23) of the magnitudes.
+          (2^-18 + (K / 32 + 16) 2^-23) of the magnitudes.  The router's sums, a lane's products of pairs
+          (H / 128 and 4 at least, 2^-23 each) and the wave's, are within it.
   gates   the logits' error dl moves a softmax by the factor exp(2 dl) at most; the exponential, the sum
           and the quotient by (k + 8) 2^-23.
   act     the projection's box through the activation (the oracle's swiglu_range), 4e-6 relative and 2e-5
