@@ -654,10 +654,10 @@ hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream)
   if (e == hipSuccess) e = launch_up(a, stream);
   if (e != hipSuccess) return e;
   const int C = items_of(a.F / 32, kWaves);  // (6 at most)
-  // Two experts under way where their parts of K are short and most experts are reached (16
+  // Two experts under way where their parts of K are short and there are many of them (16
   // tokens, E = 64, k = 8, H = F = 1024: 73 us for 82 with one); else one: the rows and the end
   // wait for less (one token of H = F = 2880, E = 32, k = 4: 23.3 us for 25.1 with two).
-  if (C == 2 && a.F < 48 * 32 && a.T * a.k >= a.E) return launch_down<2, 2>(a, stream);
+  if (C == 2 && a.F < 48 * 32 && a.E >= 32 && a.T * a.k >= 32) return launch_down<2, 2>(a, stream);
   return C == 2 ? launch_down<2, 1>(a, stream) : C == 4 ? launch_down<4, 1>(a, stream) : launch_down<6, 1>(a, stream);
 }
 
