@@ -3,7 +3,12 @@
 //   out[r, n] = bias[e, n] + sum_k X[src(r), k] * W[e, n, k]
 //
 // where e is the expert that row r is grouped under (dense: one expert that has
-// every row, in order) and src(r) the row of X that it reads.
+// every row, in order) and src(r) the row of X that it reads.  The codes and the
+// scale bytes go to the scaled-FP4 MFMA as they are stored; its sums are fp32.
+//
+// Few rows are bound by the weights' way from HBM, many by the MFMA: with all CUs
+// at it and random codes it runs 32x32x64 at 6.7 PFLOP/s, the clock then at about
+// 1.6 GHz.  Two kernels, and three tile shapes, chosen by the rows (launch_out).
 #include <type_traits>
 
 #include "kernels.h"
@@ -98,7 +103,10 @@ __device__ __forceinline__ void store_pair(const Fp4MatmulArgs& a, int r, int n,
 
 // A workgroup takes 16 weight rows of one expert and splits K over its four
 // waves; 16 routed rows at a time are the MFMA's columns.  Lane l holds weight
-// row l % 16 (and routed row l % 16) and block 4 s + l / 16 of K step s.
+// row l % 16 (and routed row l % 16) and block 4 s + l / 16 of K step s.  Bound by
+// HBM: 16 experts' 5760 x 2880 31.8 us (4.4 TB/s), 4 experts' 8.9; the weights are on
+// their way before the rows' numbers are back (with the numbers, the inputs and the
+// weights one after the other, and the bias at the end, 39.3 and 10.4).
 constexpr int kRowsWaves = 4;
 constexpr int kRowsSteps = 6;  // K steps of 128 whose loads are in flight together
 
@@ -138,12 +146,14 @@ __global__ __launch_bounds__(kRowsWaves * 64) void fp4_rows_kernel(Fp4MatmulArgs
   const size_t wrow = (size_t)e * a.N + min(n0 + c, a.N - 1);
   const u32x4_t* wq = reinterpret_cast<const u32x4_t*>(a.w) + wrow * KB;
   const uint8_t* wsc = a.ws + wrow * KB;
+  // the bias of the end's threads, under way with the weights
+  const int nl = 2 * (tid & 7), n = n0 + nl;
+  const uint16_t* const bp = a.bias ? a.bias + (size_t)e * a.N : reinterpret_cast<const uint16_t*>(a.w);
+  const uint32_t bias0 = bp[a.bias ? min(n, a.N - 1) : 0], bias1 = bp[a.bias ? min(n + 1, a.N - 1) : 0];
   for (int p0 = b; p0 < f; p0 += 16) {
-    const int r = routed_row(a, p0 + c, f);
-    const size_t xrow = r < 0 ? 0 : a.x_div == 1 ? r : r / a.x_div;
-    const u32x4_t* xq = reinterpret_cast<const u32x4_t*>(a.x) + xrow * KB;
-    const uint8_t* xsc = a.xs + xrow * KB;
-    if (tid < 16) rows_lds[tid] = r;
+    // the row's number, then the weights, which need none, then the inputs: loads return in order
+    const int at = min(p0 + c, f - 1);
+    const int listed = *(a.rows ? a.rows + at : reinterpret_cast<const int32_t*>(a.w));  // (not used without a list)
     f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
     for (int s0 = wave; s0 < steps; s0 += kRowsWaves * kRowsSteps) {
       u32x4_t wv[kRowsSteps], xv[kRowsSteps];
@@ -153,19 +163,32 @@ __global__ __launch_bounds__(kRowsWaves * 64) void fp4_rows_kernel(Fp4MatmulArgs
         const int kb = min(4 * (s0 + kRowsWaves * u) + q, KB - 1);  // blocks past K: the last one, masked below
         wv[u] = wq[kb];
         wb[u] = wsc[kb];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      int named = listed;
+      asm volatile("" : "+v"(named));  // (nor is it waited for before the weights are on their way)
+      if (!a.rows) named = at;
+      const unsigned r = (unsigned)named < (unsigned)a.R ? named : 0u;
+      const size_t xrow = a.x_div == 1 ? r : r / (unsigned)a.x_div;
+      const u32x4_t* xq = reinterpret_cast<const u32x4_t*>(a.x) + xrow * KB;
+      const uint8_t* xsc = a.xs + xrow * KB;
+#pragma unroll
+      for (int u = 0; u < kRowsSteps; u++) {
+        const int kb = min(4 * (s0 + kRowsWaves * u) + q, KB - 1);
         xv[u] = xq[kb];
         xb[u] = xsc[kb];
       }
+      __builtin_amdgcn_sched_barrier(0);  // (no load is moved to its use)
 #pragma unroll
       for (int u = 0; u < kRowsSteps; u++) {
-        const int s = s0 + kRowsWaves * u;
-        if (s < steps) {
-          const u32x4_t xm = 4 * s + q < KB ? xv[u] : u32x4_t{0, 0, 0, 0};
-          acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wv[u]), fp4_operand(xm), acc, kFmtFp4,
-                                                                 kFmtFp4, 0, (int)wb[u], 0, (int)xb[u]);
-        }
+        // (a block past K has the last one's scales: NaN only where that makes the row NaN too)
+        const u32x4_t xm = 4 * (s0 + kRowsWaves * u) + q < KB ? xv[u] : u32x4_t{0, 0, 0, 0};
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wv[u]), fp4_operand(xm), acc, kFmtFp4,
+                                                               kFmtFp4, 0, (int)wb[u], 0, (int)xb[u]);
       }
     }
+    const int named = a.rows ? listed : at;
+    if (tid < 16) rows_lds[tid] = p0 + c < f && (unsigned)named < (unsigned)a.R ? named : -1;
     // lane (c, q): routed row c, weight rows 4 q + i
 #pragma unroll
     for (int i = 0; i < 4; i++) part[wave][c * 17 + 4 * q + i] = acc[i];
@@ -173,7 +196,6 @@ __global__ __launch_bounds__(kRowsWaves * 64) void fp4_rows_kernel(Fp4MatmulArgs
     // 128 threads: routed row tid / 8, weight rows 2 (tid % 8), + 1
     if (tid < 128) {
       const int row = rows_lds[tid >> 3];
-      const int nl = 2 * (tid & 7), n = n0 + nl;
       float v0 = 0.f, v1 = 0.f;
 #pragma unroll
       for (int w = 0; w < kRowsWaves; w++) {
@@ -182,9 +204,10 @@ __global__ __launch_bounds__(kRowsWaves * 64) void fp4_rows_kernel(Fp4MatmulArgs
       }
       if (row >= 0 && n < a.N) {
         if (a.bias) {
-          const uint16_t* bp = a.bias + (size_t)e * a.N;
-          v0 += bf16_bits_to_f32(bp[n]);
-          v1 += bf16_bits_to_f32(bp[min(n + 1, a.N - 1)]);
+          uint32_t b0 = bias0, b1 = bias1;
+          asm volatile("" : "+v"(b0), "+v"(b1));  // (waited for here)
+          v0 += bf16_bits_to_f32(b0);
+          v1 += bf16_bits_to_f32(b1);
         }
         store_pair<OUT>(a, row, n, v0, v1);
       }
@@ -316,20 +339,22 @@ __device__ __forceinline__ int row_swizzle(int r) { return (r & 7) ^ ((r >> 3) &
 // all the tile's routed rows, so a tile with few of them leaves whole
 // sub-tiles out.
 //
-// K goes by stages of eight blocks (256 elements): a row's 128 bytes of codes,
-// so that every line read from L2 is used while it is in L1 (with stages of
-// four blocks each line came twice).  A weight row belongs to one wave, so its
-// codes go straight to registers, up to two stages ahead, the four loads of a
-// line close together; the activations, which all waves share, go straight to
-// two slots of LDS.  A row's scale bytes start anywhere: a window of 32 blocks
-// comes as the three aligned 16-byte pieces that hold it (none without a byte of
-// the row); a thread a row shifts them into place and splits them into a word a
-// stage and half wave, of which the MFMA picks a byte.
+// K goes by stages of eight blocks (256 elements): a row's 128 bytes of codes.  A
+// weight row belongs to one wave, so its codes go straight to registers, a stage
+// and a half ahead, by loads of 16 rows x 64 bytes, which a CU takes from L2 at 149
+// bytes a ns (32 rows x 32 bytes: 72); an exchange between the lanes makes the
+// MFMA's operands of them.  The activations, which all waves share, go straight to
+// two slots of LDS.  A row's scale bytes start anywhere: a window of 32 blocks comes
+// as the three aligned 16-byte pieces that hold it (none without a byte of the row);
+// a thread a row shifts them into place and splits them into a word a stage and
+// half wave, of which the MFMA picks a byte.
 //
 // Two workgroups share a CU, two waves a SIMD: one wave a SIMD with half as many
 // accumulators again came to 0.6 of the rate, its loads, waits, first and last
 // steps in line with its products.  Loads are spread between the products, one
-// behind every second.
+// behind every second: a load holds up the products of a lone wave for 32 cycles,
+// those of two for 15.  4096 x 5760 x 2880 runs at 2.3 PFLOP/s (736 tiles on 512
+// places), 8192^3 at 3.1.
 template <int MT, int NT>
 struct TileShape {
   static constexpr int kWaves = 4, kThreads = kWaves * 64;
