@@ -540,7 +540,8 @@ size_t mxfp4_moe_layer_workspace_size(int T, int H, int E, int k, int F);
  *
  *   x       [T, H] bf16 or fp32 (x_dtype): the residual stream, or with w_norm
  *           NULL the normed rows themselves (bf16 only).
- *   w_norm  [H] bf16, or NULL; eps > 0 where it is given.  xn as moe_norm writes it.
+ *   w_norm  [H] bf16, or NULL; eps > 0 where it is given.  xn as in moe_norm, the squares
+ *           summed in another order.
  *   router_w [E, H] bf16, router_b [E] bf16 or NULL: logits = xn . router_w^T +
  *           router_b in fp32, not rounded.  A token's k largest logits are its
  *           experts (the lower index of equals), the softmax over them its gates.
