@@ -452,9 +452,11 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
 }
 
 // The down projection, the combine and the residual: a workgroup owns 16 output columns of
-// all tokens, its waves share K.  DEPTH experts' weights are under way; the activations lie
-// in LDS, as many experts' at a time as fit (one's at least: T rows).
-template <int C, int DEPTH>
+// all tokens.  A team of its waves shares K; with more teams than one (a short K) team i takes
+// the experts whose number is i mod TEAMS, whatever the others are.  One expert's weights are
+// under way a team; the activations lie in LDS, as many experts' at a time as fit (one's at
+// least: T rows).
+template <int C, int TEAMS>
 __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, int lds_rows) {
   extern __shared__ __attribute__((aligned(16))) uint4 as[];  // as the tokens' rows above
   __shared__ float gates[kLayerMaxT * 64];
@@ -491,24 +493,23 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
   };
   next_rows();
 
-  Stream<C> st[DEPTH];
+  constexpr int kTeam = kWaves / TEAMS;
+  const int team = wave / kTeam;
+  Stream<C> st;
   Places<C> at;
-  at.set(col, wave * 4 * C + q, KB);
-  auto open = [&](int d, int i) {
-    st[d].open(a.down, a.down_scales,
-               (size_t)__builtin_amdgcn_readlane(x.expert, min(i, 63)) * a.H + (size_t)blockIdx.x * 16,
-               KB, i < count);
+  at.set(col, (wave - team * kTeam) * 4 * C + q, KB);
+  uint64_t left = wave_ballot(x.tokens != 0 && x.expert % TEAMS == team);  // the team's, as bits of the list
+  auto open = [&]() {
+    const int e = __builtin_amdgcn_readlane(x.expert, left ? __builtin_ctzll(left) : 0);
+    st.open(a.down, a.down_scales, (size_t)e * a.H + (size_t)blockIdx.x * 16, KB, left != 0);
   };
   const uint16_t* const bias = a.down_bias ? a.down_bias : a.router_w;  // (read and not used without one)
   auto bias_of = [&](int e) { return (uint32_t)bias[a.down_bias ? (size_t)max(e, 0) * a.H + out_c : 0]; };
   uint32_t bias_bits[4], x_bits;
   auto load_weights = [&]() {
+    open();
 #pragma unroll
-    for (int d = 0; d < DEPTH; d++) {
-      open(d, d);
-#pragma unroll
-      for (int j = 0; j < C; j += 2) st[d].load2(j, at);
-    }
+    for (int j = 0; j < C; j += 2) st.load2(j, at);
 #pragma unroll
     for (int s = 0; s < 4; s++) bias_bits[s] = bias_of(id[s]);
     // (the 32 bits that hold x: x is 16-byte aligned and H even)
@@ -530,27 +531,25 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
   const int tcol = min(col, a.T - 1);
   __syncthreads();
-  for (int i0 = 0; i0 < count; i0 += DEPTH) {
-#pragma unroll
-    for (int d = 0; d < DEPTH; d++) {
-      // (past the last expert: no token, and weights that read as zeros)
-      const int i = min(i0 + d, 63);
-      if (i0 + d == last && last < count) {
-        next_rows();
-        __syncthreads();
-        rows.all(as, parts, row0);
-        __syncthreads();
-      }
-      const uint32_t m = i0 + d < count ? __builtin_amdgcn_readlane(x.tokens, i) : 0u;
+  for (;;) {
+    while (left && __builtin_ctzll(left) < last) {
+      const int i = __builtin_ctzll(left);
+      left &= left - 1;
+      const uint32_t m = __builtin_amdgcn_readlane(x.tokens, i);
       const bool has = (m >> col) & 1;
       // this token's row; where it does not have the expert, some row, not used
       const int row = has ? __builtin_amdgcn_readlane(x.rows_to, i) - row0 - __popc(m >> col) : 0;
-      open(d, i0 + d + DEPTH);
-      const f32x4_t acc = st[d].use(at, as + row * RS);
+      open();
+      const f32x4_t acc = st.use(at, as + row * RS);
       const float gt = gates[tcol * 64 + __builtin_amdgcn_readlane(x.expert, i)], g = has ? gt : 0.f;
 #pragma unroll
       for (int r = 0; r < 4; r++) y[r] = g != 0.f ? fmaf(g, acc[r], y[r]) : y[r];  // (0 adds nothing)
     }
+    if (last >= count) break;
+    next_rows();
+    __syncthreads();
+    rows.all(as, parts, row0);
+    __syncthreads();
   }
   if (col < a.T) part[(wave * a.T + col) * 4 + q] = make_float4(y[0], y[1], y[2], y[3]);
   __syncthreads();
@@ -611,16 +610,16 @@ hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
                                      : launch_up<6, 1>(a, stream);
 }
 
-template <int C, int DEPTH>
+template <int C, int TEAMS>
 hipError_t launch_down(const MoeLayerArgs& a, hipStream_t stream) {
-  static DynLdsLimit limit(reinterpret_cast<const void*>(layer_down_kernel<C, DEPTH>), kLayerDownLds);
+  static DynLdsLimit limit(reinterpret_cast<const void*>(layer_down_kernel<C, TEAMS>), kLayerDownLds);
   const size_t row = (size_t)row_stride(a.F / 32) * 16;
   const int fit = (int)(((size_t)kLayerDownLds - 64 * 16) / row), R = a.T * a.k;
   if (fit < a.T) return hipErrorInvalidConfiguration;
   const hipError_t e = limit.ensure();
   if (e != hipSuccess) return e;
   const int rows = fit < R ? fit : R;
-  hipLaunchKernelGGL((layer_down_kernel<C, DEPTH>), dim3(a.H / 16), dim3(kThreads),
+  hipLaunchKernelGGL((layer_down_kernel<C, TEAMS>), dim3(a.H / 16), dim3(kThreads),
                      rows * row + 64 * 16, stream, a, rows);
   return hipGetLastError();
 }
@@ -653,12 +652,13 @@ hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream)
                            : launch_router<false, true>(a, stream);
   if (e == hipSuccess) e = launch_up(a, stream);
   if (e != hipSuccess) return e;
-  const int C = items_of(a.F / 32, kWaves);  // (6 at most)
-  // Two experts under way where their parts of K are short and there are many of them (16
-  // tokens, E = 64, k = 8, H = F = 1024: 73 us for 82 with one); else one: the rows and the end
-  // wait for less (one token of H = F = 2880, E = 32, k = 4: 23.3 us for 25.1 with two).
-  if (C == 2 && a.F < 48 * 32 && a.E >= 32 && a.T * a.k >= 32) return launch_down<2, 2>(a, stream);
-  return C == 2 ? launch_down<2, 1>(a, stream) : C == 4 ? launch_down<4, 1>(a, stream) : launch_down<6, 1>(a, stream);
+  // one team of 12 waves, three of 4 while those hold K in two items (F <= 1024: @SHORT@)
+  const int KB = a.F / 32, C = items_of(KB, kWaves);  // (6 at most)
+  return items_of(KB, kWaves / 3) == 2 ? launch_down<2, 3>(a, stream)
+         : items_of(KB, kWaves / 2) == 2 ? launch_down<2, 2>(a, stream)
+         : C == 2                      ? launch_down<2, 1>(a, stream)
+         : C == 4                      ? launch_down<4, 1>(a, stream)
+                                       : launch_down<6, 1>(a, stream);
 }
 
 }  // namespace mxfp4
