@@ -652,13 +652,16 @@ hipError_t launch_moe_layer(MoeLayerArgs a, void* workspace, hipStream_t stream)
                            : launch_router<false, true>(a, stream);
   if (e == hipSuccess) e = launch_up(a, stream);
   if (e != hipSuccess) return e;
-  // one team of 12 waves, three of 4 while those hold K in two items (F <= 1024: @SHORT@)
+  // Three teams of 4 waves, or two of 6, while their waves hold K in two items, else one of 12
+  // (with one alone 16 tokens of F = 1024, E = 64, k = 8 took 72.8 us for 63.3, 8 of F = 1440, E = 32,
+  // k = 4 35.8 for 32.7; with more at F = 2880 eight tokens took 75 to 76 us for 73.3: the teams'
+  // experts are seldom as many).
   const int KB = a.F / 32, C = items_of(KB, kWaves);  // (6 at most)
-  return items_of(KB, kWaves / 3) == 2 ? launch_down<2, 3>(a, stream)
+  return items_of(KB, kWaves / 3) == 2   ? launch_down<2, 3>(a, stream)
          : items_of(KB, kWaves / 2) == 2 ? launch_down<2, 2>(a, stream)
-         : C == 2                      ? launch_down<2, 1>(a, stream)
-         : C == 4                      ? launch_down<4, 1>(a, stream)
-                                       : launch_down<6, 1>(a, stream);
+         : C == 2                        ? launch_down<2, 1>(a, stream)
+         : C == 4                        ? launch_down<4, 1>(a, stream)
+                                         : launch_down<6, 1>(a, stream);
 }
 
 }  // namespace mxfp4

@@ -146,7 +146,7 @@ SIZES = [  # T, E, k, H, F
     (1, 1, 1, 32, 32), (1, 4, 2, 64, 96), (2, 8, 8, 32, 512), (3, 5, 3, 288, 160), (1, 32, 4, 2880, 2880),
     (8, 32, 4, 512, 544), (16, 64, 16, 96, 64), (5, 7, 3, 1056, 32), (4, 13, 4, 2048, 768), (7, 64, 1, 160, 2880),
     (16, 3, 2, 320, 1024), (16, 2, 2, 4096, 96), (2, 3, 2, 3104, 96), (2, 3, 2, 96, 3136), (8, 2, 1, 96, 8192),
-    (1, 2, 2, 8192, 64)]
+    (1, 2, 2, 8192, 64), (8, 32, 4, 160, 1440), (1, 32, 4, 96, 1088)]
 
 
 @pytest.mark.parametrize("T,E,k,H,F", SIZES)
@@ -163,9 +163,11 @@ def test_forms(x, norm, residual, y, biases):
     run(3, 11, 4, 416, 352, x=x, norm=norm, residual=residual, y=y, biases=biases, seed=1)
 
 
-def test_rows_pass_the_lds():
+@pytest.mark.parametrize("T,E,k,H,F", [(16, 16, 16, 64, 4096), (16, 64, 8, 64, 1024), (16, 16, 16, 32, 1440),
+                                       (8, 8, 8, 32, 8192)])
+def test_rows_pass_the_lds(T, E, k, H, F):
     """More activations than fit at once: the down projection goes by groups of experts."""
-    run(16, 16, 16, 64, 4096, seed=2)
+    run(T, E, k, H, F, seed=2)
 
 
 def test_without_the_optional_outputs_and_in_place():
@@ -188,14 +190,15 @@ def test_every_call_is_the_same():
         assert torch.equal(a.y, want[0]) and torch.equal(a.ids, want[1]) and torch.equal(a.gates, want[2])
 
 
-def test_a_token_does_not_hear_of_the_others():
+@pytest.mark.parametrize("F", [288, 1440, 2080])
+def test_a_token_does_not_hear_of_the_others(F):
     """The same token alone and in a batch: bit for bit, as its sums take the same order."""
-    a = Layer(8, 16, 4, 512, 288, seed=5)
+    a = Layer(8, 16, 4, 512, F, seed=5)
     a.call()
     for t in (0, 3, 7):
-        b = Layer(8, 16, 4, 512, 288, seed=5)
+        b = Layer(8, 16, 4, 512, F, seed=5)
         y = torch.empty((1, 512), dtype=torch.bfloat16, device="cuda")
-        B.mxfp4_moe_layer(b.dx[t:t + 1], 1, 512, 16, 4, 288, b.drw, b.drb, *b.dgu, b.dbgu, *b.ddown, b.dbd, y,
+        B.mxfp4_moe_layer(b.dx[t:t + 1], 1, 512, 16, 4, F, b.drw, b.drb, *b.dgu, b.dbgu, *b.ddown, b.dbd, y,
                           w_norm=b.dw_norm, eps=EPS, residual=True, workspace=b.ws)
         assert torch.equal(y[0], a.y[t])
 
