@@ -28,8 +28,6 @@ namespace {
 
 constexpr int kQnThreads = 256;
 
-typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
-
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Scale byte of a block whose largest magnitude has fp32 bits m: the exponent

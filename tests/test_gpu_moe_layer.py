@@ -146,7 +146,8 @@ SIZES = [  # T, E, k, H, F
     (1, 1, 1, 32, 32), (1, 4, 2, 64, 96), (2, 8, 8, 32, 512), (3, 5, 3, 288, 160), (1, 32, 4, 2880, 2880),
     (8, 32, 4, 512, 544), (16, 64, 16, 96, 64), (5, 7, 3, 1056, 32), (4, 13, 4, 2048, 768), (7, 64, 1, 160, 2880),
     (16, 3, 2, 320, 1024), (16, 2, 2, 4096, 96), (2, 3, 2, 3104, 96), (2, 3, 2, 96, 3136), (8, 2, 1, 96, 8192),
-    (1, 2, 2, 8192, 64), (8, 32, 4, 160, 1440), (1, 32, 4, 96, 1088)]
+    (1, 2, 2, 8192, 64), (8, 32, 4, 160, 1440), (1, 32, 4, 96, 1088),
+    (8, 2, 2, 8192, 32), (15, 4, 2, 4352, 32), (13, 64, 3, 32, 32)]
 
 
 @pytest.mark.parametrize("T,E,k,H,F", SIZES)
