@@ -13,6 +13,7 @@
 
 #include "kernels.h"
 #include "common.h"
+#include "fp4_places.h"
 
 namespace mxfp4 {
 namespace {
@@ -388,22 +389,23 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4MatmulArgs a, int v
   const int last = (KB - 1) >> 3;  // the last stage
   const int n0 = t.nt * S::TN;
 
-  // this wave's weight rows (past N: the last one, whose products are not stored)
-  const int wn0 = min(n0 + wave * NT * 32, a.N - 1);
-  const int wrows = min(a.N - wn0, NT * 32);
+  // this wave's weight rows
+  const int wn0 = fp4_wave_first(n0 + wave * NT * 32, a.N);
+  const int wrows = fp4_wave_rows(n0 + wave * NT * 32, a.N, NT * 32);
   const __amdgpu_buffer_rsrc_t wsrc = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.w + ((size_t)t.e * a.N + wn0) * KB * 16), (short)0, wrows * KB * 16, 0x00020000);
   int woff[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; n++)
 #pragma unroll
-    for (int u = 0; u < 2; u++)
-      woff[n][u] = min(32 * n + 16 * u + (lane & 15), wrows - 1) * (KB * 16) + (lane >> 4) * 16;
+    for (int u = 0; u < 2; u++) woff[n][u] = fp4_row_at(n, u, lane, wrows, KB);
   u32x4_t w[2][NT][4];
-  // piece i of a stage's 4 NT: sub-tile i / 4, blocks 4 (i / 2 % 2) .. + 3, rows 16 (i % 2) .. + 15;
-  // past K the next row's codes or none
+  // piece i of a stage's 4 NT: sub-tile i / 4, blocks 4 (i / 2 % 2) .. + 3, rows 16 (i % 2) .. + 15.
+  // Every lane's offset lies in the wave's rows: a buffer's bounds are not checked against
+  // an offset in a scalar register, so none is left to them.
   auto load_w = [&](int s, int i) {
-    return __builtin_amdgcn_raw_buffer_load_b128(wsrc, woff[i >> 2][i & 1], min(s, last) * 128 + 32 * (i & 2), 0);
+    return __builtin_amdgcn_raw_buffer_load_b128(wsrc, woff[i >> 2][i & 1] + fp4_block_at(s, i >> 1 & 1, lane, KB), 0,
+                                                 0);
   };
   // the rows and the bias first: the barrier waits for them, not for the weights
   static_assert(S::TM <= S::kThreads, "a row a thread");
@@ -609,8 +611,8 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4MatmulArgs a, int v
       sc = next;
     };
     // Stages in pairs.  A last one with an odd number goes with them, its blocks past
-    // K (which hold other rows' finite codes, or none) under scale byte 0 on both
-    // sides: products below 2^-240, that change no sum.  A last one with an even
+    // K (the last one's codes again) under scale byte 0 on both sides: products below
+    // 2^-240, that change no sum.  A last one with an even
     // number follows, with the K steps that it has.
     for (int s = 0; s < last; s += 2) {
       stage(s, J0{});
