@@ -523,7 +523,7 @@ int mxfp4_expert_matmul(const uint8_t* blocks, const uint8_t* scales, const uint
 /*
  * The same through the gated activation of mxfp4_expert_proj_swiglu: N even,
  *   act     [T, k, N / 2] bf16 out: bf16(swiglu(p[t, s, 2 i], p[t, s, 2 i + 1])) of the
- *           fp32 projection p.
+ *           fp32 projection p; NaN where either is.
  */
 int mxfp4_expert_matmul_swiglu(const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias, int E, int N,
                                int K, const uint8_t* x_blocks, const uint8_t* x_scales, int x_per_slot, int T, int k,
@@ -549,7 +549,8 @@ size_t mxfp4_moe_layer_workspace_size(int T, int H, int E, int k, int F);
  *           takes it (rows 2 i and 2 i + 1 gate and up), the bias [E, 2 F] bf16 or
  *           NULL.  down_blocks, down_scales, down_bias: [E, H, F] and [E, H].
  *           Exact weights times bf16 activations summed in fp32; the activation
- *           between the two is rounded to bf16.
+ *           between the two is rounded to bf16.  Scale byte 255 makes a block's weights
+ *           NaN, and so every output that a token gets through that row.
  *   residual != 0: x is added to the sum (in fp32, before its one rounding).
  *   y       [T, H] bf16 or fp32 (y_dtype) out.  y may be x (of the same type).
  *   topk_ids [T, k] i32, gates [T, k] fp32 out, each or NULL.

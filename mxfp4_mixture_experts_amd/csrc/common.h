@@ -39,12 +39,13 @@ __device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
 // multiplier to [-LIMIT, LIMIT], then (up + 1) * gate * sigmoid(ALPHA * gate).
 // fp32, with sigmoid(ALPHA g) = 1 / (1 + 2^(-ALPHA log2(e) g)) on the
 // hardware exp2 and reciprocal (each within 1 ulp); a very negative gate gives
-// 2^(+large) = inf and a zero product.
+// 2^(+large) = inf and a zero product.  The clamps keep a NaN (v_minimum3_f32 and
+// v_maximum3_f32; fminf and fmaxf would make a limit of it).
 constexpr float kSwigluLimit = 7.0f;
 constexpr float kSwigluAlphaLog2e = (float)(1.702 * 1.4426950408889634);
 __device__ __forceinline__ float swiglu(float gate, float up) {
-  const float g = fminf(gate, kSwigluLimit);
-  const float u = fminf(fmaxf(up, -kSwigluLimit), kSwigluLimit);
+  const float g = __builtin_elementwise_minimum(gate, kSwigluLimit);
+  const float u = __builtin_elementwise_minimum(__builtin_elementwise_maximum(up, -kSwigluLimit), kSwigluLimit);
   const float e = __builtin_amdgcn_exp2f(-kSwigluAlphaLog2e * g);
   return (u + 1.0f) * (g * __builtin_amdgcn_rcpf(1.0f + e));
 }
