@@ -300,7 +300,7 @@ __global__ __launch_bounds__(kRouterWaves * 64) void layer_router_kernel(MoeLaye
         square(p0);
       }
     }
-    if (NORM) r = __builtin_amdgcn_rsqf(fmaf(wave_total(ss), a.inv_H, a.eps));
+    if (NORM) r = rsqrtf(fmaf(wave_total(ss), a.inv_H, a.eps));  // (as moe_norm: right for a subnormal eps too)
     if (ONCE) {
       dot(0);
     } else {

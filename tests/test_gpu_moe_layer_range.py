@@ -1,5 +1,5 @@
 """The expert layer of a few tokens where numbers leave the ordinary range: NaN blocks, the scale bytes'
-ends.
+ends, an eps below fp32's normal numbers.
 
 Tolerances are those of test_gpu_moe_layer (intervals carried through the layer).  Outputs near fp32's
 least numbers have 2^-149 for each product and sum besides (their spacing there).
@@ -10,6 +10,7 @@ import torch
 
 import oracle.moe_oracle as M
 import oracle.mx_oracle as O
+from mxfp4_mixture_experts_amd import binding as B
 from test_gpu_moe_layer import Layer, cuda, rounded, sums
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +86,20 @@ def test_the_scales_of_the_down_projection(T, E, k, H, F, lo, hi):
     got = a.y.cpu().numpy().astype(np.float64)
     err = np.abs(got - h)
     assert (err <= bound).all(), float(np.nanmax(err / bound))
+
+
+@pytest.mark.parametrize("eps", [1e-42, 1e-39, 2.0 ** -126])
+def test_an_eps_below_the_normal_numbers(eps):
+    """A row of zeros stays zeros under any eps, as in moe_norm: its experts are the router bias's."""
+    a = Layer(4, 8, 2, 288, 160, seed=46)
+    a.dx[1:3] = 0.0
+    want, ids = None, None
+    for e in (1e-5, eps):
+        a.y.fill_(float("nan"))
+        B.mxfp4_moe_layer(a.dx, *a.s, a.drw, a.drb, *a.dgu, a.dbgu, *a.ddown, a.dbd, a.y, w_norm=a.dw_norm, eps=e,
+                          residual=True, topk_ids=a.ids, gates=a.gates, workspace=a.ws)
+        if want is None:
+            want, ids = a.y[1:3].clone(), a.ids[1:3].clone()
+    assert (a.ids >= 0).all()
+    assert torch.equal(a.y[1:3], want) and torch.equal(a.ids[1:3], ids)
+    assert torch.isfinite(a.y.float()).all()
