@@ -80,18 +80,19 @@ __device__ __forceinline__ f32x4_t item_mma(const u32x4_t w, uint32_t scale, con
 }
 
 // Where a lane finds its blocks b, b + 4, ... of a row: in a unit's codes and scales, zeros
-// past the row, and among the row's inputs, past it the last block's.
+// past the row, and among the row's inputs, past it the pieces from x_past on (finite
+// numbers wherever the row's are: they meet the zeros).
 template <int C>
 struct Places {
   uint32_t w[C], s[C];
   int x[C];
-  __device__ __forceinline__ void set(int row, int b, int KB) {
+  __device__ __forceinline__ void set(int row, int b, int KB, int x_past) {
 #pragma unroll
     for (int j = 0; j < C; j++) {
       const bool in = b + 4 * j < KB;
       s[j] = in ? row * KB + b + 4 * j : kPast;
       w[j] = in ? (row * KB + b + 4 * j) * 16 : kPast;
-      x[j] = min(b + 4 * j, KB - 1) * 4;
+      x[j] = in ? (b + 4 * j) * 4 : x_past;
     }
   }
 };
@@ -331,6 +332,7 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
 
   const float first_logit = lane < a.E && wave < a.T ? a.ws_logits[wave * 64 + lane] : 0.f;
   if (tid < 64) tokens[tid] = 0;
+  if (tid < 4) xs[a.T * RS + tid] = make_uint4(0, 0, 0, 0);  // what stands past a row's end (x may be infinite)
   Rows rows;
   rows.open(a.w_norm ? a.ws_xn : a.x, a.T * a.H * 2, a.H >> 3, a.T, wave, lane);
   rows.load(wave, a.T * rows.spans, 0);
@@ -396,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void layer_gate_up_kernel(MoeLayerArgs a)
   const int rounds = (mine + TEAMS - 1) / TEAMS;
   Stream<C> st;
   Places<C> at;
-  at.set(col, part_of * 4 * C + q, KB);
+  at.set(col, part_of * 4 * C + q, KB, a.T * RS - xrow);
   int ld_i = (u0 + team) / per, ld_tile = u0 + team - ld_i * per, ld_left = mine - team;
   auto next_unit = [&]() {
     const size_t unit = (size_t)__builtin_amdgcn_readlane(x.expert, min(ld_i, 63)) * per + ld_tile;
@@ -497,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(MoeLayerArgs a, in
   const int team = wave / kTeam;
   Stream<C> st;
   Places<C> at;
-  at.set(col, (wave - team * kTeam) * 4 * C + q, KB);
+  at.set(col, (wave - team * kTeam) * 4 * C + q, KB, (KB - 1) * 4);  // (an activation is finite, or NaN)
   uint64_t left = wave_ballot(x.tokens != 0 && x.expert % TEAMS == team);  // the team's, as bits of the list
   auto open = [&]() {
     const int e = __builtin_amdgcn_readlane(x.expert, left ? __builtin_ctzll(left) : 0);

@@ -1,5 +1,5 @@
-"""The expert layer of a few tokens where numbers leave the ordinary range: NaN blocks, the scale bytes'
-ends, an eps below fp32's normal numbers.
+"""The expert layer of a few tokens where numbers leave the ordinary range: NaN blocks, every scale byte,
+an infinity at a row's end, an eps below fp32's normal numbers.
 
 Tolerances are those of test_gpu_moe_layer (intervals carried through the layer).  Outputs near fp32's
 least numbers have 2^-149 for each product and sum besides (their spacing there).
@@ -86,6 +86,27 @@ def test_the_scales_of_the_down_projection(T, E, k, H, F, lo, hi):
     got = a.y.cpu().numpy().astype(np.float64)
     err = np.abs(got - h)
     assert (err <= bound).all(), float(np.nanmax(err / bound))
+
+
+@pytest.mark.parametrize("H,F", [(288, 160), (2880, 96), (4128, 96), (544, 1088)])
+def test_an_infinity_at_the_end_of_a_row(H, F):
+    """The last element of a normed row is infinite: every logit is -infinity, so the token's experts are
+    the first, and every gate and up sum is +infinity, which the activation brings to its limit."""
+    T, E, k = 3, 4, 2
+    a = Layer(T, E, k, H, F, norm=False, residual=False, y="f32", seed=45)
+    a.drw[:, -1] = -1.0
+    a.dx[1, -1] = float("inf")
+    codes = a.gu[0].copy()
+    codes[..., -1, 15] = (codes[..., -1, 15] & 0x0f) | 0x20      # the last weight of every row: +1
+    a.dgu = (cuda(codes), a.dgu[1])
+    a.call()
+    assert a.ids[1].tolist() == [0, 1] and a.gates[1].tolist() == [0.5, 0.5]
+    act = np.full((1, k, F), M.swiglu(np.array([np.inf, np.inf]))[0])
+    ids = np.array([[0, 1]])
+    o, mag = O.expert_matmul(O.decode(*a.down), a.bd, O.bf16(act), True, ids)
+    size = 0.5 * mag.sum(1)
+    err = np.abs(a.y[1].cpu().numpy() - 0.5 * o.sum(1)[0])
+    assert (err <= 0.5 * sums(mag, F).sum(1)[0] + (2 * k + 15) * 2.0 ** -23 * size[0]).all()
 
 
 @pytest.mark.parametrize("eps", [1e-42, 1e-39, 2.0 ** -126])
