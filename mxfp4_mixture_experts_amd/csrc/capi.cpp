@@ -711,6 +711,7 @@ int expert_matmul_impl(const uint8_t* blocks, const uint8_t* scales, const uint1
   a.K = K;
   a.R = T * k;
   a.x_div = x_per_slot ? 1 : k;
+  a.T = T;
   const hipError_t e = mxfp4::launch_fp4_matmul(a, kind, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "expert_matmul launch");
   return MXFP4_OK;

@@ -313,7 +313,8 @@ __device__ __forceinline__ void lds_barrier() {
 // before any LDS read that it cannot tell apart from the destination; here
 // the arrival is waited for with vmcnt before the barrier behind which the
 // data are read.  (No output registers; the nop is the wait state between the
-// write of m0 and its use.  Nothing else here uses m0.)
+// write of m0 and its use.  The compiler keeps no value in m0, a reserved register that
+// a clobber list may not name; nothing else here uses it.)
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds_off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_off), "v"(src)
                : "memory");
@@ -719,14 +720,27 @@ hipError_t launch_rows(const Fp4MatmulArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Few rows an expert: 16 x 16 blocks that stream the weights, against the smallest tiles (us,
+// weights from HBM).  A workgroup of either pays a chain of latencies, and there are many more of
+// the blocks': they win while they are few (1 x 5760 x 2880 4.6 against 8.5, 16 x 5760 x 2880
+// 5.7 / 10.3, 16 routed rows over 32 experts of 1024 x 2304 7.9 / 11.4), and beyond that where the
+// rows are long and do not start line by line in the same place (16 routed rows of 5760 x 2880
+// 23.6 / 26.7, 64 of them 62 / 65, 64 over 64 experts of 2880 x 2880 44 / 49); else the tiles
+// do (16 routed rows of 5760 x 1024 34 / 14, of 5760 x 4096 72 / 44, 1 x 40000 x 2048 19 / 14).
+// A block goes over its expert's rows by sixteens, one token's experts differ, so up to 32 tokens
+// are two rounds: all 32 on the same 2 of 128 experts of 2880 x 2880 11.8 / 10.6, on the same 8
+// 20.8 / 13.9; 128 tokens on the same 8 of 512 experts of 1024 x 1024 would take 87 / 18.
+bool takes_rows(const Fp4MatmulArgs& a, long long groups) {
+  const long long blocks = groups * ((a.N + 15) / 16);
+  const bool few = blocks <= (a.K > 1024 ? 1024 : 512), long_rows = a.K >= 2560 && a.K % 256 != 0;
+  return (few || long_rows) && (a.offsets ? a.R <= 2 * groups && a.T <= 32 : a.R <= 16);
+}
+
 template <int OUT>
 hipError_t launch_out(const Fp4MatmulArgs& a, hipStream_t stream) {
-  // Few rows an expert: 16 x 16 blocks that stream the weights (16 rows of 5760 x
-  // 2880: 5.4 us against 8.4 in the smallest tiles; 17 rows 9.0 against 8.4; 64 routed
-  // rows over 32 experts 66 us against 73, 128 rows 80 against 74).
   const long long groups = a.offsets ? min(a.E, a.R) : 1;
-  if (a.R <= (a.offsets ? 2 * groups : 16)) return launch_rows<OUT>(a, stream);
-  // Then the smallest tiles that give no CU two workgroups, for a tile's time
+  if (takes_rows(a, groups)) return launch_rows<OUT>(a, stream);
+  // The smallest tiles that give no CU two workgroups, for a tile's time
   // hardly depends on how many run (17 to 256 rows of 5760 x 2880: 64 x 128 tiles 8.4
   // to 9.8 us, 128 x 128 9.6 to 12.0, 128 x 256 12.7 to 17.0; 1024 rows: 24.6, 21.0,
   // 19.8); and the smallest where an expert has few rows (1024 routed rows over 32

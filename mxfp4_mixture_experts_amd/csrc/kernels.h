@@ -86,6 +86,7 @@ struct Fp4MatmulArgs {
   const int32_t* rows;     // [R], with offsets
   void* out;               // [R, N] fp32 or bf16, or [R, N / 2] bf16 activations
   int E, N, K, R, x_div;
+  int T;  // tokens (with offsets)
 };
 hipError_t launch_fp4_matmul(const Fp4MatmulArgs& a, int out_kind, hipStream_t stream);
 

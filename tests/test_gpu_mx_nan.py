@@ -11,7 +11,7 @@ from test_gpu_mx_tiles import SPREAD, grouping, kernel_of
 
 pytestmark = pytest.mark.gpu
 
-CASES = [("rows", (2, 2, 1, 1), 66, 288), ("rows", (37, 20, 17, 1, 5) + (0,) * 35, 50, 4128),
+CASES = [("rows", (2, 2, 1, 1), 66, 288), ("rows", (27, 20, 11, 1, 5) + (0,) * 35, 50, 4128),
          ((64, 128), (60, 0, 70, 96), 200, 96), ((128, 128), SPREAD, 704, 544), ((128, 256), SPREAD, 1154, 288)]
 
 
@@ -20,7 +20,7 @@ CASES = [("rows", (2, 2, 1, 1), 66, 288), ("rows", (37, 20, 17, 1, 5) + (0,) * 3
 def test_routed(kernel, counts, N, K, per_slot):
     E, T, k = len(counts), sum(counts) // 2, 2
     print(f"[case] {sum(counts)} rows, {E} experts, {N}x{K} per_slot={per_slot}", flush=True)
-    assert kernel_of(T * k, N, E) == kernel
+    assert kernel_of(T * k, N, K, E, T) == kernel
     r = np.random.default_rng([61, T, N, K])
     w, x = operand(r, (E, N), K), operand(r, (T, k) if per_slot else (T,), K)
     _, db = bf16_bias(r, E, N)
@@ -79,7 +79,7 @@ def test_a_nan_of_a_tensor_reaches_the_down_projection(kernel, T):
     x[0, 5], x[T - 1, H - 1] = float("nan"), float("-inf")
     counts = np.array([T, T, 0, 0])
     _, offsets, order = grouping(r, counts)
-    assert kernel_of(T * k, 2 * F, E) == kernel
+    assert kernel_of(T * k, 2 * F, H, E, T) == kernel
     u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device="cuda")
     gu, down = tuple(map(cuda, operand(r, (E, 2 * F), H))), tuple(map(cuda, operand(r, (E, H), F)))
     xq, aq = (u8(T, H // 32, 16), u8(T, H // 32)), (u8(T, k, F // 32, 16), u8(T, k, F // 32))

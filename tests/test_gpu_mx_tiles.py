@@ -21,11 +21,12 @@ def _announce(msg):
     print(f"[case] {msg}", flush=True)
 
 
-def kernel_of(rows, N, experts=0):
-    """The kernel of a product of so many rows and outputs (routed to so many experts): "rows" or the
-    tile's rows and outputs."""
+def kernel_of(rows, N, K, experts=0, tokens=0):
+    """The kernel of a product of so many rows, outputs and inputs (of so many tokens, routed to so many
+    experts): "rows" or the tile's rows and outputs."""
     groups = min(experts, rows) if experts else 1
-    if rows <= (2 * groups if experts else 16):
+    light = groups * -(-N // 16) <= (1024 if K > 1024 else 512) or (K >= 2560 and K % 256)
+    if light and (rows <= 2 * groups and tokens <= 32 if experts else rows <= 16):
         return "rows"
 
     def tiles(tm, tn):
@@ -61,7 +62,7 @@ DENSE = [((128, 128), 1025, 2000, 32), ((128, 128), 1057, 2000, 96), ((128, 128)
 @pytest.mark.parametrize("kernel,rows,N,K", DENSE)
 def test_dense_tiles(kernel, rows, N, K, dtype):
     _announce(f"matmul {rows}x{N}x{K} {dtype}")
-    assert kernel_of(rows, N) == kernel
+    assert kernel_of(rows, N, K) == kernel
     run_matmul(rows, N, K, dtype, bias=(N + K // 32) % 2 == 0)
 
 
@@ -79,7 +80,7 @@ def test_routed_tiles(kernel, counts, N, K, per_slot):
 
 
 # 2 rows an expert and fewer on average, all in a few: several groups of 16, and K beyond one pass of 24 steps of 128
-FEW = [((37, 20, 17, 1, 5) + (0,) * 35, 50, 96), ((16, 33, 1) + (0,) * 22, 34, 2880), ((2, 2, 1, 1), 66, 4128),
+FEW = [((27, 20, 11, 1, 5) + (0,) * 35, 50, 96), ((16, 33, 1) + (0,) * 22, 34, 2880), ((2, 2, 1, 1), 66, 4128),
        ((40,) + (0,) * 19, 18, 6240), ((1, 1) + (0,) * 30, 2880, 6176), ((17, 3) + (0,) * 8, 64, 8224)]
 
 
@@ -90,16 +91,35 @@ def test_few_rows_in_several_passes(counts, N, K, per_slot):
     check_routed("rows", counts, N, K, per_slot)
 
 
+# as few rows, where the smallest tiles take them: too many workgroups, aligned rows, too many tokens
+TILED = [((1, 2, 0, 1) * 16, 1100, 96), ((2, 1, 0, 1) * 8, 800, 2560), ((1,) * 20 + (0,) * 12, 1700, 1024),
+         ((37, 20, 17, 1, 5) + (0,) * 35, 50, 96), ((64, 10) + (0,) * 40, 34, 2880)]
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("counts,N,K", TILED)
+def test_few_rows_in_tiles(counts, N, K, per_slot):
+    _announce(f"expert matmul {counts[:5]}.. of {len(counts)} experts, {N}x{K} per_slot={per_slot}")
+    check_routed((64, 128), counts, N, K, per_slot)
+
+
+@pytest.mark.parametrize("rows,N,K", [(1, 8200, 96), (16, 8201, 1024), (3, 16390, 2048), (7, 16400, 2560)])
+def test_few_dense_rows_in_tiles(rows, N, K):
+    _announce(f"matmul {rows}x{N}x{K}")
+    assert kernel_of(rows, N, K) == (64, 128)
+    run_matmul(rows, N, K, torch.float32, bias=True)
+
+
 @pytest.mark.parametrize("rows,N,K", [(1, 40, 4128), (16, 33, 6240), (5, 5760, 3136), (9, 17, 9248)])
 def test_few_dense_rows_of_a_long_k(rows, N, K):
     _announce(f"matmul {rows}x{N}x{K}")
-    assert kernel_of(rows, N) == "rows"
+    assert kernel_of(rows, N, K) == "rows"
     run_matmul(rows, N, K, torch.float32, bias=True)
 
 
 def check_routed(kernel, counts, N, K, per_slot):
     E, T, k = len(counts), sum(counts) // 2, 2
-    assert kernel_of(T * k, N, E) == kernel
+    assert kernel_of(T * k, N, K, E, T) == kernel
     r = np.random.default_rng([51, T, E, N, K])
     w, x = operand(r, (E, N), K), operand(r, (T, k) if per_slot else (T,), K)
     hb, db = bf16_bias(r, E, N)
@@ -118,7 +138,7 @@ def check_routed(kernel, counts, N, K, per_slot):
 @pytest.mark.parametrize("kernel,rows,N,K", [((128, 128), 1030, 2000, 96), ((128, 256), 2060, 2100, 288)])
 def test_every_scale_byte(kernel, rows, N, K):
     """Scales from the least to the largest whose products stay in range; tiny with tiny."""
-    assert kernel_of(rows, N) == kernel
+    assert kernel_of(rows, N, K) == kernel
     r = np.random.default_rng([52, rows])
     for a_range, b_range in (((0, 3), (200, 253)), ((60, 70), (180, 190)), ((250, 255), (0, 5)), ((0, 255), (127, 128))):
         a, b = operand(r, (rows,), K, *a_range), operand(r, (N,), K, *b_range)
@@ -130,12 +150,12 @@ def test_every_scale_byte(kernel, rows, N, K):
         assert (err <= out_bound(want, mag, K, torch.float32) + 2.0 ** -126)[keep].all()
 
 
-@pytest.mark.parametrize("kernel,counts,N", [("rows", (37, 20, 17, 1, 5) + (0,) * 35, 50), ((128, 128), SPREAD, 700),
+@pytest.mark.parametrize("kernel,counts,N", [("rows", (27, 20, 11, 1, 5) + (0,) * 35, 50), ((128, 128), SPREAD, 700),
                                              ((128, 256), SPREAD, 1150)])
 def test_bad_groupings_stay_inside(kernel, counts, N):
     """Offsets past the rows and rows out of range are clamped or skipped; every other row is right."""
     E, T, k, K = len(counts), sum(counts) // 2, 2, 64
-    assert kernel_of(T * k, N, E) == kernel
+    assert kernel_of(T * k, N, K, E, T) == kernel
     r = np.random.default_rng([53, T, N])
     w, x = operand(r, (E, N), K), operand(r, (T,), K)
     ids, offsets, order = grouping(r, counts)
@@ -156,7 +176,7 @@ def test_bad_groupings_stay_inside(kernel, counts, N):
 
 @pytest.mark.parametrize("kernel,rows,N", [((128, 128), 1030, 2000), ((128, 256), 2060, 2100)])
 def test_nothing_behind_the_outputs_is_written(kernel, rows, N):
-    assert kernel_of(rows, N) == kernel
+    assert kernel_of(rows, N, 64) == kernel
     r = np.random.default_rng([54, rows])
     a, b = operand(r, (rows,), 64), operand(r, (N,), 64)
     out = torch.full((rows * N + 4096,), 9.0, dtype=torch.float32, device="cuda")
@@ -170,7 +190,7 @@ def test_nothing_behind_the_outputs_is_written(kernel, rows, N):
 
 @pytest.mark.parametrize("kernel,rows,N,K", [((128, 128), 1030, 2000, 288), ((128, 256), 2060, 2100, 544)])
 def test_captured(kernel, rows, N, K):
-    assert kernel_of(rows, N) == kernel
+    assert kernel_of(rows, N, K) == kernel
     r = np.random.default_rng([55, rows])
     a, b = tuple(map(cuda, operand(r, (rows,), K))), tuple(map(cuda, operand(r, (N,), K)))
     out = torch.empty((rows, N), dtype=torch.bfloat16, device="cuda")
