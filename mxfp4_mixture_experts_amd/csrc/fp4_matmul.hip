@@ -105,9 +105,10 @@ __device__ __forceinline__ void store_pair(const Fp4MatmulArgs& a, int r, int n,
 // A workgroup takes 16 weight rows of one expert and splits K over its four
 // waves; 16 routed rows at a time are the MFMA's columns.  Lane l holds weight
 // row l % 16 (and routed row l % 16) and block 4 s + l / 16 of K step s.  Bound by
-// HBM: 16 experts' 5760 x 2880 31.8 us (4.4 TB/s), 4 experts' 8.9; the weights are on
-// their way before the rows' numbers are back (with the numbers, the inputs and the
-// weights one after the other, and the bias at the end, 39.3 and 10.4).
+// HBM and, with few experts, by latencies: 4 tokens through 13 experts of 5760 x 2880
+// 27.8 us (4.2 TB/s), one token through 4 of them 10.9 (3.2).  The weights are on their
+// way before the rows' numbers are back (with the numbers, the inputs and the weights
+// one after the other, and the bias at the end, 16 experts took 39.3 us for 31.8).
 constexpr int kRowsWaves = 4;
 constexpr int kRowsSteps = 6;  // K steps of 128 whose loads are in flight together
 
@@ -355,8 +356,8 @@ __device__ __forceinline__ int row_swizzle(int r) { return (r & 7) ^ ((r >> 3) &
 // accumulators again came to 0.6 of the rate, its loads, waits, first and last
 // steps in line with its products.  Loads are spread between the products, one
 // behind every second: a load holds up the products of a lone wave for 32 cycles,
-// those of two for 15.  4096 x 5760 x 2880 runs at 2.3 PFLOP/s (736 tiles on 512
-// places), 8192^3 at 3.1.
+// those of two for 15.  4096 x 5760 x 2880 runs at 2.4 PFLOP/s with its operands in the
+// last-level cache and at 2.0 from HBM (736 tiles on 512 places), 8192^3 at 3.0 and 2.8.
 template <int MT, int NT>
 struct TileShape {
   static constexpr int kWaves = 4, kThreads = kWaves * 64;
@@ -720,16 +721,16 @@ hipError_t launch_rows(const Fp4MatmulArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Few rows an expert: 16 x 16 blocks that stream the weights, against the smallest tiles (us,
-// weights from HBM).  A workgroup of either pays a chain of latencies, and there are many more of
-// the blocks': they win while they are few (1 x 5760 x 2880 4.6 against 8.5, 16 x 5760 x 2880
-// 5.7 / 10.3, 16 routed rows over 32 experts of 1024 x 2304 7.9 / 11.4), and beyond that where the
-// rows are long and do not start line by line in the same place (16 routed rows of 5760 x 2880
-// 23.6 / 26.7, 64 of them 62 / 65, 64 over 64 experts of 2880 x 2880 44 / 49); else the tiles
-// do (16 routed rows of 5760 x 1024 34 / 14, of 5760 x 4096 72 / 44, 1 x 40000 x 2048 19 / 14).
-// A block goes over its expert's rows by sixteens, one token's experts differ, so up to 32 tokens
+// Few rows an expert: 16 x 16 blocks that stream the weights, against the smallest tiles (us, two
+// or three sets of operands in turn).  A workgroup of either pays a chain of latencies, and there
+// are many more of the blocks': they win while they are few (1 x 5760 x 2880 4.6 against 8.5, 16 rows
+// 5.7 / 10.3, from HBM 5.8 / 13.6; 16 routed rows over 32 experts of 1024 x 2304 7.9 / 11.4), and
+// beyond that where the rows are long and do not start line by line in the same place (16 routed
+// rows of 5760 x 2880 23.6 / 26.7, 64 of them 62 / 65, 64 over 64 experts of 2880 x 2880 44 / 49); else
+// the tiles do (16 routed rows of 5760 x 1024 34 / 14, of 5760 x 4096 72 / 44, 1 x 40000 x 2048 19 / 14).
+// A block goes over its expert's rows by sixteens, and a token's experts differ, so up to 32 tokens
 // are two rounds: all 32 on the same 2 of 128 experts of 2880 x 2880 11.8 / 10.6, on the same 8
-// 20.8 / 13.9; 128 tokens on the same 8 of 512 experts of 1024 x 1024 would take 87 / 18.
+// 20.8 / 13.6; 128 tokens on the same 8 of 512 experts of 1024 x 1024 would take 87 / 18.
 bool takes_rows(const Fp4MatmulArgs& a, long long groups) {
   const long long blocks = groups * ((a.N + 15) / 16);
   const bool few = blocks <= (a.K > 1024 ? 1024 : 512), long_rows = a.K >= 2560 && a.K % 256 != 0;
@@ -740,12 +741,14 @@ template <int OUT>
 hipError_t launch_out(const Fp4MatmulArgs& a, hipStream_t stream) {
   const long long groups = a.offsets ? min(a.E, a.R) : 1;
   if (takes_rows(a, groups)) return launch_rows<OUT>(a, stream);
-  // The smallest tiles that give no CU two workgroups, for a tile's time
-  // hardly depends on how many run (17 to 256 rows of 5760 x 2880: 64 x 128 tiles 8.4
-  // to 9.8 us, 128 x 128 9.6 to 12.0, 128 x 256 12.7 to 17.0; 1024 rows: 24.6, 21.0,
-  // 19.8); and the smallest where an expert has few rows (1024 routed rows over 32
-  // experts of 5760 x 2880: 84 us in 64 x 128 tiles, 87 in 128 x 256; 2048 rows 119 and
-  // 96).
+  // The smallest tiles that give no CU two workgroups, for a tile's time hardly depends on how
+  // many run (17 to 256 rows of 5760 x 2880: 64 x 128 tiles 10.0 to 12.4 us, 128 x 128 11.6 to 14.7,
+  // 128 x 256 14.8 to 19.2; 1024 rows: 24.2, 21.9, 21.0); and the smallest where an expert has few
+  // rows (1024 routed rows over 32 experts of 5760 x 2880: 88 us in 64 x 128 tiles, 93 in 128 x 256,
+  // their numbers falling as a power of the expert's 97 and 104; 2048 rows 122 and 97, 126 and 112).
+  // Of 156 sizes with all three timed it misses the best by more than 8 percent at 7, by a third at
+  // most (512 rows over 8 experts of 2880 x 2880 21.8 us, 16.5 in the smallest: its count of tiles
+  // takes a broken one for every expert).
   constexpr long long kCus = 256;
   if (tiles<2, 1>(a) <= kCus || (a.offsets && a.R <= 32 * groups)) return launch_tiles<2, 1, OUT>(a, stream);
   if (tiles<4, 1>(a) <= kCus) return launch_tiles<4, 1, OUT>(a, stream);

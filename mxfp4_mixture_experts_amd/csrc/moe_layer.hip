@@ -7,10 +7,10 @@
 //   down    y = (x +) sum over slots of gate (down[e] . act + bias).
 //
 // The borders of the launches are the two points where every workgroup needs what all
-// others made; no workgroup waits for another.  With the norm and the router in the
-// gate/up launch too (each workgroup its own) the layer took 27.3 us for one token of
-// H = F = 2880, E = 32, k = 4 instead of 23.3: 256 CUs read the same 184 KB at 17 bytes a
-// clock each, three times what a launch costs.
+// others made; no workgroup waits for another.  Moving the norm and the router out of the
+// gate/up launch (where each workgroup did its own) took one token of H = F = 2880, E = 32,
+// k = 4 from 27.3 to 25.1 us: 256 CUs read the same 184 KB at 17 bytes a clock each.  Now
+// 24 to 27 us from HBM, as the experts fall, and 74 to 79 for eight tokens.
 //
 // Both projections stream the chosen experts' weights once for all tokens, by items of 16
 // weight rows x 4 blocks (lane: row lane % 16, block lane / 16), a wave's items in
@@ -603,7 +603,10 @@ hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 hipError_t launch_up(const MoeLayerArgs& a, hipStream_t stream) {
-  // three teams of 4 waves while a wave's share of K is 6 items at most, else one of 12
+  // Three teams of 4 waves while a wave's share of K is 6 items at most, else one of 12 (the layer,
+  // one token / eight: H = 288, F = 2880 16.0 / 40 us, with one team 18.7 / 52; H = F = 1440 14.7 / 33 to
+  // 15.5 / 39; 2048 20.7 / 55 to 20.4 / 68; 2880 23.5 / 75 to 23.1 / 70; beyond, with one team, 4096 44 / 148,
+  // with three of 8 items 42 / 147; 3584 x 2880 28 / 86 to 26 / 80)
   const int KB = a.H / 32, C = items_of(KB, kWaves / 3);
   return C == 2                      ? launch_up<2, 3>(a, stream)
          : C == 4                    ? launch_up<4, 3>(a, stream)

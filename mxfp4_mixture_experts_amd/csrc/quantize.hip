@@ -16,9 +16,10 @@
 // form): a lane holds a column's whole block, 32 row loads of 64 columns a wave; the
 // waves of a workgroup hold consecutive blocks of the same columns, whose codes meet
 // in LDS, so that the stores run along the columns: 512 contiguous bytes of values,
-// 128 of codes.  4096 x 2880 bf16 with values: 10.1 us, 5.3 TB/s.  (Written by the
-// lanes that made them, 16 bytes a column, 24.6; with two bf16 columns a lane in 32-bit
-// loads 11.5; the values' stores not marked as streamed 14.6.)
+// 128 of codes.  4096 x 2880 bf16 with values: 10.2 us where the tensors stay in the last-
+// level cache (5.2 TB/s), 14.3 from HBM (3.7); fp32 16.1 and 16.6 (4.6 TB/s).  (In the cache:
+// written by the lanes that made them, 16 bytes a column, 24.6; with two bf16 columns a
+// lane in 32-bit loads 11.5; the values' stores not marked as streamed 14.6.)
 
 #include "kernels.h"
 #include "common.h"
